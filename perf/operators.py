@@ -13,7 +13,8 @@ Definitions
           positive v never gets c_r = 0.
   mx4     blocks of 32 along a row; scale byte = max(exponent field of the block's largest magnitude - 2, 0) (E8M0,
           255 where the block holds a NaN or an infinity), elements e2m1 of x / scale, nearest even, at most 6; two
-          elements a byte, the even one in the low half; rows padded with zeros to whole units of 128.
+          elements a byte, the even one in the low half; rows padded with zeros to whole units of 128.  A unit is 64
+          code bytes and 4 scale bytes; codes lie as (unit, row, 64), scales as (unit, row, 4).
   product C = A B^T of two operands coded along k.
 """
 import math
@@ -103,7 +104,8 @@ def _pack_mx4(x):
     level = sum((y > e).to(torch.uint8) if i % 2 == 0 else (y >= e).to(torch.uint8)
                 for i, e in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)))
     code = (level | (torch.signbit(b).to(torch.uint8) << 3)).flatten(-2)
-    return (code[..., 0::2] | (code[..., 1::2] << 4)).contiguous(), byte.to(torch.uint8).contiguous()
+    by_unit = lambda t, width: t.unflatten(-1, (-1, width)).transpose(0, 1).contiguous()  # noqa: E731
+    return by_unit(code[..., 0::2] | (code[..., 1::2] << 4), UNIT // 2), by_unit(byte.to(torch.uint8), UNIT // BLOCK)
 
 
 def _views(sizes, dtype, device="cuda"):
@@ -264,6 +266,7 @@ def _mx4_values(x):
 
 def _mx4_decode(codes, scales, k):
     table = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], device="cuda")
+    codes, scales = codes.transpose(0, 1).flatten(1), scales.transpose(0, 1).flatten(1)
     both = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).long()
     y = table[both & 7] * (1 - 2 * (both >> 3)).float()
     return (y.unflatten(-1, (-1, BLOCK)) * _power(scales.int())[..., None]).flatten(-2)[..., :k]
@@ -448,6 +451,7 @@ def _exact_decode(codes, scales, k):
     sign = torch.tensor([1.0, -1.0], dtype=torch.float64, device="cuda")
     mag = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
     table = torch.outer(sign, mag).flatten()
+    codes, scales = (x.permute(1, 0, 2).reshape(x.shape[1], -1) for x in (codes, scales))
     v = torch.empty(codes.shape[0], codes.shape[1] * 2, dtype=torch.float64, device="cuda")
     v[:, 0::2] = table[(codes & 15).long()]
     v[:, 1::2] = table[(codes >> 4).long()]
