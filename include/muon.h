@@ -324,6 +324,144 @@ muon_status muon_group8_dequantize(int batch, int rows, int k, const void *const
                                    const void *const *scales, void *const *Y, void *stream);
 
 /*
+ * The AdamW step ([MuonBlog §1], the update Muon is compared with) for the
+ * parameters Muon is not for ([MuonBlog §1], [MuonBlog §5]: embeddings, head,
+ * norms, biases), over a list of tensors of any sizes at once:
+ *   g = s G
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   W <- W - lr ((m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *                + weight_decay W)
+ * in fp32 arithmetic; a bf16 W is rounded once, to nearest even.
+ *
+ *   tensors   length of the list, at least 1.
+ *   sizes     HOST array of `tensors` element counts (read during the call
+ *             only), 0 or more; a tensor of size 0 is passed over.
+ *   W         device array of device pointers, w_dtype F32 or BF16, updated in
+ *             place.
+ *   M, V      device arrays of device pointers to fp32 moments, updated in
+ *             place.  The first step of a run passes zeros.
+ *   G         device array of device pointers, gradients (F32, BF16 or F16).
+ *   cfg       fill with muon_adamw_config_init() and change fields; not NULL.
+ * The four arrays must be distinct, and no two of the buffers may overlap.
+ * Buffers need the alignment of their element type only; 16-byte aligned ones
+ * are faster.  Errors as for muon_step; MUON_ERR_INVALID_ARG also for lr, eps
+ * or weight_decay not finite in fp32, eps <= 0, betas outside [0, 1) or step < 1.
+ *
+ * muon_adamw_config:
+ *   lr, beta1, beta2, eps, weight_decay   defaults 1e-3, 0.9, 0.999, 1e-8, 0
+ *             (doubles: 1 - 0.999f would be off by 1e-5 of itself).
+ *   step      t, counted from 1.
+ *   step_dev  NULL, or a device pointer to t, read by the kernel instead of
+ *             `step` (values under 1 count as 1): a captured graph then takes
+ *             the step number of its replay.  The caller advances it.
+ *   grad_scale  NULL, or a device pointer to s (e.g. a clipping factor or the
+ *             inverse of a loss scale); NULL = 1.
+ *   seed      of the random roundings of muon_adamw8_step.
+ */
+typedef struct muon_adamw_config {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  const int64_t *step_dev;
+  const float *grad_scale;
+  uint32_t seed;
+} muon_adamw_config;
+
+void muon_adamw_config_init(muon_adamw_config *cfg);
+
+muon_status muon_adamw_step(int tensors, const int64_t *sizes, void *const *W, muon_dtype w_dtype,
+                            void *const *M, void *const *V, const void *const *G, muon_dtype g_dtype,
+                            const muon_adamw_config *cfg, void *stream);
+
+/*
+ * The AdamW step with its moments in 8 bits.  A tensor is cut into groups of
+ * 128 consecutive elements (the last one shorter); in a group
+ *   m = c_m s_m,   sqrt(v) = c_r s_r
+ * with codes c in the 8-bit float e4m3 (OCP, 4 exponent and 3 mantissa bits,
+ * largest value 448) and fp32 scales s = (largest magnitude of the group) /
+ * 448 (0, with codes 0, if that is under 2^-126).  The step is muon_adamw_step's
+ * on the decoded moments; W takes the new moments before they are coded.
+ *   c_m       m / s_m rounded to nearest even.
+ *   c_r       sqrt(v) / s_r =: x rounded to one of its neighbours lo <= x < hi,
+ *             up if (x - lo)(x + lo) > u (hi - lo)(hi + lo): the expected
+ *             square is v.  (v moves by 1 - beta2 of itself in a step, far less
+ *             than a code step, and would stand still if rounded to nearest.)
+ *             u = (h + 1/2) / 65536; h is the lower (even elements) or upper
+ *             half of mix(i / 2 + mix(seed + mix(t + mix(j)))) for element i of
+ *             tensor j of the list, mod 2^32, with mix(x): x ^= x >> 16;
+ *             x *= 0x9E3779B1; x ^= x >> 15; x *= 0xB7E15163; x ^= x >> 16.  A
+ *             positive v never gets code 0.
+ * A NaN or an infinity among a group's new moments makes its scale NaN or
+ * infinite and its codes 0: the whole group's moments then read as NaN.
+ *   state     device arrays of device pointers, updated in place: codes of
+ *             sizes[j] bytes, scales of ceil(sizes[j] / 128) floats.  The first
+ *             step of a run passes zeros.
+ * Everything else as for muon_adamw_step.
+ */
+typedef struct muon_adamw8_state {
+  void *const *m_codes;
+  void *const *m_scales;
+  void *const *r_codes;
+  void *const *r_scales;
+} muon_adamw8_state;
+
+muon_status muon_adamw8_step(int tensors, const int64_t *sizes, void *const *W, muon_dtype w_dtype,
+                             const muon_adamw8_state *state, const void *const *G, muon_dtype g_dtype,
+                             const muon_adamw_config *cfg, void *stream);
+
+/*
+ * Microscaled 4-bit code (the MXFP4 format of the OCP Microscaling Formats
+ * specification v1.0), for the weights a step has updated and for what they
+ * are multiplied with.  Along a row, each block of 32 elements shares a scale
+ * 2^(byte - 127): byte = max(E - 2, 0), E the biased fp32 exponent of the
+ * block's largest magnitude, and 255 (NaN) if the block holds a NaN or an
+ * infinity (its codes are then 0).  An element is stored as the e2m1 float
+ * nearest to x / scale, ties to even, magnitudes over 6 as 6 (codes 0..7 = 0,
+ * 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 = sign).  The conversion is exact arithmetic.
+ *
+ * Layout: a row of k elements is ceil(k / 128) units of four blocks, filled up
+ * with zeros (codes and scale bytes).  For a matrix of `rows` rows
+ *   codes   uint8 [units][rows][64], element 2 i in the low, 2 i + 1 in the
+ *           high half of byte i of its unit; 16-byte aligned
+ *   scales  uint8 [units][rows][4]; 4-byte aligned.
+ * Every argument is a device array of `batch` device pointers, batch <= 65535.
+ *
+ * muon_mx4_quantize codes rows x cols matrices X (F32, BF16 or F16) along
+ * their rows (codes, scales), along their columns (codes_t, scales_t: the code
+ * of the cols x rows matrix X^T), or both; the arrays of an orientation that is
+ * not wanted are NULL.  muon_mx4_dequantize writes the values of a code as F32
+ * or BF16, both exact for the codes muon_mx4_quantize makes.
+ */
+muon_status muon_mx4_quantize(int batch, int rows, int cols, const void *const *X, muon_dtype x_dtype,
+                              void *const *codes, void *const *scales,
+                              void *const *codes_t, void *const *scales_t, void *stream);
+muon_status muon_mx4_dequantize(int batch, int rows, int cols, const void *const *codes,
+                                const void *const *scales, void *const *Y, muon_dtype y_dtype, void *stream);
+
+/*
+ * C = A B^T, or C += A B^T, of matrices in that code: A is m x k, B is n x k,
+ * C is m x n in c_dtype (F32 or BF16), row-major.  With a layer's weight W
+ * (out x in), input X and output gradient dY this is the forward product X W^T
+ * (A = X, B = W), the input gradient dY W (A = dY, B = W^T) and the weight
+ * gradient dY^T X (A = dY^T, B = X^T), each operand coded along the summed axis.
+ * Products and sums are fp32; with accumulate the product is added to C in
+ * fp32; C is rounded once.  Results do not depend on timing.  A scale byte 255
+ * makes NaN of every element of C that its block enters.
+ *
+ *   workspace  device buffer of at least muon_mx4_workspace_size() bytes, 256-byte
+ *              aligned; contents on entry are ignored.  Calls that share it
+ *              must not overlap.
+ * muon_mx4_workspace_size returns 0 for invalid arguments, also for an operand
+ * of 2^31 code bytes or more.  A and B may be the same matrix; C must be a
+ * buffer of its own.
+ */
+size_t muon_mx4_workspace_size(int batch, int m, int n, int k);
+muon_status muon_mx4_matmul(int batch, int m, int n, int k,
+                            const void *const *A_codes, const void *const *A_scales,
+                            const void *const *B_codes, const void *const *B_scales,
+                            void *const *C, muon_dtype c_dtype, int accumulate,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Per-iteration coefficient schedule in the manner of the Polar Express
  * quintics that [GNS §3.2] iterates with (its printed table is garbled, so
  * the schedule is derived from the method's principle rather than copied):

@@ -46,6 +46,16 @@ class _Config(ctypes.Structure):
                 ("restart_mask", ctypes.c_uint32), ("compute", ctypes.c_int), ("shift", ctypes.c_int32)]
 
 
+class _AdamWConfig(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+        ("seed", ctypes.c_uint32)]
+
+
+class _AdamW8State(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("m_codes", "m_scales", "r_codes", "r_scales")]
+
+
 class _GraspState(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("res_codes", "res_row_scales", "res_col_scales", "P_codes", "P_scales", "R_codes", "R_scales")]
@@ -107,6 +117,21 @@ def load_library():
     for name in ("muon_group8_quantize", "muon_group8_dequantize"):
         getattr(lib, name).argtypes = [i32, i32, i32, vp, vp, vp, vp]
         getattr(lib, name).restype = i32
+    sizes, acfg = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_AdamWConfig)
+    lib.muon_adamw_config_init.argtypes = [acfg]
+    lib.muon_adamw_config_init.restype = None
+    lib.muon_adamw_step.argtypes = [i32, sizes, vp, i32, vp, vp, vp, i32, acfg, vp]
+    lib.muon_adamw_step.restype = i32
+    lib.muon_adamw8_step.argtypes = [i32, sizes, vp, i32, ctypes.POINTER(_AdamW8State), vp, i32, acfg, vp]
+    lib.muon_adamw8_step.restype = i32
+    lib.muon_mx4_quantize.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+    lib.muon_mx4_quantize.restype = i32
+    lib.muon_mx4_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, vp]
+    lib.muon_mx4_dequantize.restype = i32
+    lib.muon_mx4_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.muon_mx4_workspace_size.restype = sz
+    lib.muon_mx4_matmul.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
+    lib.muon_mx4_matmul.restype = i32
     _lib = lib
     return lib
 
@@ -194,8 +219,11 @@ def pointer_array(tensors: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
     not take: call once with the same tensors before capturing.  An array used
     during a capture is kept for the life of the process, since the graph
     reads it at every replay."""
-    ptrs = tuple(int(t.data_ptr()) for t in tensors)
-    dev = tensors[0].device
+    return _pointer_array(tuple(int(t.data_ptr()) for t in tensors), tensors[0].device, stream)
+
+
+def _pointer_array(ptrs: tuple, dev, stream=None) -> torch.Tensor:
+    """pointer_array of the data pointers themselves."""
     key = (str(dev), ptrs)
     if dev.type != "cuda":  # host tensors (argument checks without a device)
         ent = _ptr_cache.get(key)
@@ -575,3 +603,271 @@ def grasp_step(W, state: GraspState, G, mu: float, lr: float, weight_decay: floa
                               workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream),
                               _stream(aux_stream) if aux_stream is not None else None)
     _check(st_)
+
+
+# ---------------------------------------------------------------------------
+# AdamW step (muon_adamw_step, muon_adamw8_step in include/muon.h)
+# ---------------------------------------------------------------------------
+@dataclass
+class AdamW8State:
+    """8-bit moments of a list of tensors (layout of muon_adamw8_state): lists of float8_e4m3fn codes, one per
+    element, and float32 scales, one per 128 consecutive elements."""
+    m_codes: list
+    m_scales: list
+    r_codes: list
+    r_scales: list
+
+    @classmethod
+    def zeros(cls, W):
+        """The state before the first step on the tensors ``W``."""
+        def codes():
+            return [torch.zeros(w.shape, dtype=torch.float8_e4m3fn, device=w.device) for w in W]
+
+        def scales():
+            return [torch.zeros(_nb(w.numel()), dtype=torch.float32, device=w.device) for w in W]
+
+        return cls(codes(), scales(), codes(), scales())
+
+    def values(self):
+        """The moments (m, v) the codes stand for, as lists of float32 tensors."""
+        def decode(codes, scales):
+            return [(c.float().flatten() * s.repeat_interleave(GRID)[:c.numel()]).view(c.shape)
+                    for c, s in zip(codes, scales)]
+
+        return decode(self.m_codes, self.m_scales), [r * r for r in decode(self.r_codes, self.r_scales)]
+
+
+_numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
+_get_device, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _list_of(tensors, name: str, sizes, device: int, dtypes):
+    """Data pointers of a list of contiguous device tensors that share one of
+    ``dtypes`` and have the given sizes."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name}: one tensor per tensor of W is needed")
+    types = {t.dtype for t in tensors}
+    if len(types) != 1 or not types <= dtypes:
+        raise ValueError(f"{name}: all tensors must share one dtype of {sorted(str(d) for d in dtypes)}")
+    if set(map(_get_device, tensors)) != {device}:
+        raise ValueError(f"{name}: all tensors must be on the device of W")
+    if tuple(map(_numel, tensors)) != sizes:
+        raise ValueError(f"{name}: wrong number of elements")
+    if not all(map(_contiguous, tensors)):
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return tuple(map(_data_ptr, tensors))
+
+
+def _adamw_call(W, lists, G, config, stream, launch):
+    """Checks of both AdamW steps: ``lists`` = (name, tensors, sizes or None for W's, dtype) of the state;
+    ``launch(library, sizes, W, state arrays, G, w dtype, g dtype, config, stream)``."""
+    lib = load_library()
+    if len(W) == 0:
+        raise ValueError("W: empty list")
+    sizes = tuple(map(_numel, W))
+    device = W[0].get_device()
+    if device < 0:
+        raise ValueError("W: tensors must be device tensors")
+    pw = _list_of(W, "W", sizes, device, {torch.float32, torch.bfloat16})
+    pg = _list_of(G, "G", sizes, device, set(_DT))
+    ps = [_list_of(t, name, n or sizes, device, {dt}) for name, t, n, dt in lists]
+    used = [p for q in (pw, pg, *ps) for p in q if p != 0]
+    if len(set(used)) != len(used):
+        raise ValueError("W, G and the state must be tensors of their own: one of them is in the lists twice")
+    lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed = config
+    c = _AdamWConfig(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 0, None, None,
+                     int(seed) & 0xFFFFFFFF)
+    for name, t, dt in (("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(t, torch.Tensor) and (t.numel() != 1 or t.dtype != dt or t.get_device() != device):
+            raise ValueError(f"{name}: a tensor must be one {dt} on the device of W")
+    if isinstance(step, torch.Tensor):
+        c.step_dev = step.data_ptr()
+    else:
+        c.step = int(step)
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor):
+            raise ValueError("grad_scale must be a device tensor or None")
+        c.grad_scale = grad_scale.data_ptr()
+    dev = W[0].device
+    with _on(dev):
+        arrays = [_pointer_array(p, dev, stream).data_ptr() for p in (pw, pg, *ps)]
+        _check(launch(lib, (ctypes.c_int64 * len(sizes))(*sizes), arrays[0], arrays[2:], arrays[1], _DT[W[0].dtype],
+                      _DT[G[0].dtype], ctypes.byref(c), _stream(stream)))
+
+
+class _Same:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_same = _Same()
+
+
+def _on(dev):
+    """The context in which ``dev`` is the current device."""
+    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def adamw_step(W, M, V, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.0, grad_scale=None, stream=None):
+    """One AdamW step on lists of tensors of any shapes; W, M and V are updated in place:
+    W <- W - lr (m_hat / (sqrt(v_hat) + eps) + weight_decay W).
+
+    W: float32 or bfloat16, M and V: float32, G: float32, bfloat16 or float16 (one dtype per list).  ``step`` counts
+    from 1; as a one-element int64 device tensor it is read by the kernel, so that a captured graph can advance it.
+    ``grad_scale``: None or a one-element float32 device tensor the gradients are multiplied with."""
+    def launch(lib, sizes, w, state, g, wdt, gdt, cfg, s):
+        return lib.muon_adamw_step(len(W), sizes, w, wdt, state[0], state[1], g, gdt, cfg, s)
+
+    f32 = torch.float32
+    _adamw_call(W, (("M", M, None, f32), ("V", V, None, f32)), G,
+                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, 0), stream, launch)
+
+
+def adamw8_step(W, state: AdamW8State, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, seed: int = 0, stream=None):
+    """adamw_step with the moments in 8 bits: W and the state are updated in place.  ``seed`` with ``step`` fixes the
+    random roundings of the second moment's codes."""
+    def launch(lib, sizes, w, arrays, g, wdt, gdt, cfg, s):
+        return lib.muon_adamw8_step(len(W), sizes, w, wdt, ctypes.byref(_AdamW8State(*arrays)), g, gdt, cfg, s)
+
+    groups = tuple(_nb(w.numel()) for w in W)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _adamw_call(W, (("m_codes", state.m_codes, None, f8), ("m_scales", state.m_scales, groups, f32),
+                    ("r_codes", state.r_codes, None, f8), ("r_scales", state.r_scales, groups, f32)), G,
+                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed), stream, launch)
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit code and product (muon_mx4_* in include/muon.h)
+# ---------------------------------------------------------------------------
+@dataclass
+class MX4:
+    """A batch of same-shape matrices in the microscaled 4-bit code: per matrix uint8 codes (units, rows, 64) and scales
+    (units, rows, 4), units = ceil(cols / 128).  ``cols`` is the length of a row."""
+    codes: list
+    scales: list
+    cols: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes[0].shape[1]
+
+    @classmethod
+    def empty(cls, batch: int, rows: int, cols: int, device, stream=None):
+        dev = torch.device(device)
+        units = _nb(cols)
+        if stream is None:
+            buf = torch.empty(batch, units * rows * 68, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(_stream_obj(stream, dev)):
+                buf = torch.empty(batch, units * rows * 68, dtype=torch.uint8, device=dev)
+        split = batch * units * rows * 64  # all codes first, so that every matrix's codes are 16-byte aligned
+        flat = buf.view(-1)
+        return cls(list(flat[:split].view(batch, units, rows, 64).unbind(0)),
+                   list(flat[split:].view(batch, units, rows, 4).unbind(0)), int(cols))
+
+
+def _mx4_check(q, name: str):
+    """(batch, rows, cols, device) of a code."""
+    if len(q.codes) == 0 or len(q.codes) != len(q.scales):
+        raise ValueError(f"{name}: codes and scales must hold one tensor per matrix")
+    c0 = q.codes[0]
+    shape, dev = c0.shape, c0.device
+    if len(shape) != 3 or shape[0] != _nb(q.cols) or shape[1] < 1 or shape[2] != 64 or q.cols < 1:
+        raise ValueError(f"{name}: codes must be (ceil(cols / 128), rows, 64)")
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: codes must be device tensors")
+    for t, last, align in [(c, 64, 16) for c in q.codes] + [(s, 4, 4) for s in q.scales]:
+        if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != (shape[0], shape[1], last):
+            raise ValueError(f"{name}: all codes and scales must be uint8 of one shape and device")
+        if not t.is_contiguous() or t.data_ptr() % align:
+            raise ValueError(f"{name}: codes and scales must be contiguous, codes 16-byte and scales 4-byte aligned")
+    return len(q.codes), shape[1], q.cols, dev
+
+
+def mx4_quantize(X, transpose=False, out=None, stream=None):
+    """The microscaled 4-bit code of the matrices ``X`` (float32, bfloat16 or float16) along their rows, or with
+    ``transpose=True`` that of their transposes (along the columns), or with ``transpose="both"`` the pair of both from
+    one read.  ``out``: an MX4 (or a pair) of the right shape to write into, e.g. under graph capture."""
+    lib = load_library()
+    rows, cols, dt = _batch(X, "X")
+    if transpose not in (False, True, "both"):
+        raise ValueError('transpose must be False, True or "both"')
+    dev = X[0].device
+    want = ((rows, cols),) if transpose is False else ((cols, rows),) if transpose is True else ((rows, cols), (cols, rows))
+    if out is None:
+        made = [MX4.empty(len(X), r, c, dev, stream) for r, c in want]
+    else:
+        made = list(out) if transpose == "both" else [out]
+        if len(made) != len(want) or any(_mx4_check(q, "out") != (len(X), r, c, dev) for q, (r, c) in zip(made, want)):
+            raise ValueError("out must have the shape, batch and device of the result")
+    along = made[0] if transpose is not True else None
+    across = made[-1] if transpose is not False else None
+    with _on(dev):
+        ptrs = [pointer_array(t, stream).data_ptr() if t is not None else None for t in
+                (X, along and along.codes, along and along.scales, across and across.codes, across and across.scales)]
+        _check(lib.muon_mx4_quantize(len(X), rows, cols, ptrs[0], dt, *ptrs[1:], _stream(stream)))
+    if out is not None:
+        return out
+    return tuple(made) if transpose == "both" else made[0]
+
+
+def _outputs(batch, rows, cols, dtype, dev, stream):
+    if stream is None:
+        return list(torch.empty(batch, rows, cols, dtype=dtype, device=dev).unbind(0))
+    with torch.cuda.stream(_stream_obj(stream, dev)):
+        return list(torch.empty(batch, rows, cols, dtype=dtype, device=dev).unbind(0))
+
+
+def mx4_dequantize(q: MX4, dtype=torch.float32, out=None, stream=None):
+    """The values of a code as float32 or bfloat16 matrices."""
+    lib = load_library()
+    batch, rows, cols, dev = _mx4_check(q, "q")
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32 or bfloat16")
+    Y = _outputs(batch, rows, cols, dtype, dev, stream) if out is None else out
+    if out is not None and (_batch(out, "out") != (rows, cols, _DT[dtype]) or len(out) != batch or out[0].device != dev):
+        raise ValueError("out must have the shape, batch, dtype and device of the result")
+    with _on(dev):
+        _check(lib.muon_mx4_dequantize(batch, rows, cols, pointer_array(q.codes, stream).data_ptr(),
+                                       pointer_array(q.scales, stream).data_ptr(), pointer_array(Y, stream).data_ptr(),
+                                       _DT[dtype], _stream(stream)))
+    return Y
+
+
+def mx4_matmul(A: MX4, B: MX4, dtype=torch.bfloat16, out=None, accumulate: bool = False, workspace=None, stream=None):
+    """C = A B^T of every pair of coded matrices (A: m x k, B: n x k), as float32 or bfloat16 m x n matrices; with
+    ``accumulate`` C += A B^T into ``out``."""
+    lib = load_library()
+    batch, m, k, dev = _mx4_check(A, "A")
+    b2, n, k2, dev2 = _mx4_check(B, "B")
+    if b2 != batch or k2 != k or dev2 != dev:
+        raise ValueError("A and B must share the batch, the row length and the device")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None:
+        rows, cols, cdt = _batch(out, "out")
+        if (rows, cols) != (m, n) or len(out) != batch or out[0].device != dev:
+            raise ValueError("out must have one m x n matrix per pair, on the same device")
+        C = out
+    else:
+        if dtype not in _DT:
+            raise ValueError("dtype must be float32 or bfloat16")
+        C, cdt = _outputs(batch, m, n, dtype, dev, stream), _DT[dtype]
+    need = int(lib.muon_mx4_workspace_size(batch, m, n, k))
+    if need == 0:
+        raise MuonError(1, "invalid arguments for the workspace size")
+    with _on(dev):
+        if workspace is None:
+            # from the allocator at every call: its memory is reused in the stream's order, and under capture it
+            # belongs to the graph, so two graphs never share it
+            with torch.cuda.stream(_stream_obj(stream, dev)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ptrs = [pointer_array(t, stream).data_ptr() for t in (A.codes, A.scales, B.codes, B.scales, C)]
+        _check(lib.muon_mx4_matmul(batch, m, n, k, *ptrs, cdt, 1 if accumulate else 0, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    return C

@@ -1,0 +1,512 @@
+// The AdamW step over a list of tensors of any sizes, for the parameters that
+// are not hidden 2-D weights (embeddings, head, norms, biases), with the two
+// moments in fp32 or in 8-bit codes, and the host side of its entry points.
+//
+//   g = s G,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2,
+//   W <- W - lr ((m / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps) + wd W)
+//
+// (AdamW update [MuonBlog §1], weight decay decoupled as in the Muon update.)
+// All arithmetic is fp32; a bf16 W is rounded once, to nearest even.
+//
+// One launch covers up to kMaxTensors tensors: each is cut into chunks of
+// kChunk elements, one block per chunk, and a block finds its tensor in the
+// chunk starts that travel with the kernel arguments (no table in memory, so
+// nothing has to be copied to the device and a captured graph holds it).
+#include <math.h>
+#include <string.h>
+
+#include "../../include/muon.h"
+#include "muon_convert.h"
+#include "muon_internal.h"
+
+namespace muon {
+namespace {
+
+constexpr int kMaxTensors = 256;
+constexpr int kThreads = 256;
+constexpr int kQuads = 4;                              // 4-element pieces per thread, 32-bit states
+constexpr int kChunk32 = kThreads * 4 * kQuads;        // elements per block, 32-bit states
+constexpr int kGroup = 128;                            // elements per scale, 8-bit states
+constexpr int kChunk8 = kThreads * 8;                  // elements per block, 8-bit states (16 groups)
+
+struct TensorTable {
+  int count;                         // tensors in this launch
+  int first;                         // list index of the launch's first tensor
+  uint32_t start[kMaxTensors + 1];   // first block of each tensor
+  int64_t size[kMaxTensors];
+};
+
+struct AdamwScalars {
+  float lr, wd, eps, b1, ob1, b2, ob2;
+  float c1, c2;              // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) for the host's t
+  double beta1, beta2;
+  int64_t step;
+  const int64_t* step_dev;   // t in device memory, or null
+  const float* grad_scale;   // s in device memory, or null (1)
+  uint32_t seed;
+};
+
+struct Adamw32Args {
+  void* const* W;
+  const void* const* G;
+  void* const* M;
+  void* const* V;
+  AdamwScalars s;
+  TensorTable t;
+};
+
+struct Adamw8Args {
+  void* const* W;
+  const void* const* G;
+  void* const* mc;
+  void* const* ms;
+  void* const* rc;
+  void* const* rs;
+  AdamwScalars s;
+  TensorTable t;
+};
+
+// The tensor of this block (the last one whose start is not beyond it; empty
+// tensors have the next one's start and are passed over).
+__device__ __forceinline__ int find_tensor(const TensorTable& t, uint32_t block) {
+  int lo = 0, hi = t.count;  // start[lo] <= block < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.start[mid] <= block) {
+      lo = mid;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double int_power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+// The scalars with a step number or a gradient scale from device memory.
+struct Scalars {
+  float c1, c2, gs;
+  int64_t step;
+};
+__device__ __forceinline__ Scalars load_scalars(const AdamwScalars& s) {
+  Scalars r{s.c1, s.c2, 1.0f, s.step};
+  if (s.step_dev != nullptr) {
+    const int64_t t = *s.step_dev;
+    r.step = t < 1 ? 1 : t;
+    r.c1 = static_cast<float>(1.0 / (1.0 - int_power(s.beta1, r.step)));
+    r.c2 = static_cast<float>(1.0 / sqrt(1.0 - int_power(s.beta2, r.step)));
+  }
+  if (s.grad_scale != nullptr) r.gs = *s.grad_scale;
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ float load_f(const void* p, int64_t i) {
+  return load_as_f32(p, i, D);
+}
+
+// Four consecutive elements as fp32 (one 16- or 8-byte load).
+template <int D>
+__device__ __forceinline__ void load4(const void* p, int64_t i, float (&x)[4]) {
+  if constexpr (D == kF32) {
+    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    const uint16_t h[4] = {static_cast<uint16_t>(v.x), static_cast<uint16_t>(v.x >> 16), static_cast<uint16_t>(v.y),
+                           static_cast<uint16_t>(v.y >> 16)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = D == kBF16 ? bf16_to_f32(h[k]) : f16_to_f32(h[k]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) {
+  if constexpr (D == kF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+        make_uint2(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]));
+  }
+}
+
+// One element's moments and weight.
+__device__ __forceinline__ void update(float& w, float g, float& m, float& v, const AdamwScalars& s, const Scalars& r) {
+  g *= r.gs;
+  m = s.b1 * m + s.ob1 * g;
+  v = s.b2 * v + (s.ob2 * g) * g;
+  w = w - s.lr * (m * r.c1 / (sqrtf(v) * r.c2 + s.eps) + s.wd * w);
+}
+
+template <int DW, int DG>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Adamw32Args a) {
+  const int t = find_tensor(a.t, blockIdx.x);
+  const int64_t n = a.t.size[t];
+  void* W = a.W[a.t.first + t];
+  const void* G = a.G[a.t.first + t];
+  float* M = static_cast<float*>(a.M[a.t.first + t]);
+  float* V = static_cast<float*>(a.V[a.t.first + t]);
+  const Scalars r = load_scalars(a.s);
+  const int64_t base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk32;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(W) & (DW == kF32 ? 15 : 7)) |
+                        (reinterpret_cast<uintptr_t>(G) & (DG == kF32 ? 15 : 7)) |
+                        (reinterpret_cast<uintptr_t>(M) & 15) | (reinterpret_cast<uintptr_t>(V) & 15)) == 0;
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const int64_t i = base + (q * kThreads + static_cast<int>(threadIdx.x)) * 4;
+    if (aligned && i + 4 <= n) {
+      float w[4], g[4], m[4], v[4];
+      load4<DW>(W, i, w);
+      load4<DG>(G, i, g);
+      load4<kF32>(M, i, m);
+      load4<kF32>(V, i, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) update(w[k], g[k], m[k], v[k], a.s, r);
+      store4<kF32>(M, i, m);
+      store4<kF32>(V, i, v);
+      store4<DW>(W, i, w);
+    } else {
+      for (int k = 0; k < 4 && i + k < n; ++k) {
+        float w = load_f<DW>(W, i + k);
+        update(w, load_f<DG>(G, i + k), M[i + k], V[i + k], a.s, r);
+        store_from_f32(W, i + k, DW, w);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit states: per group of 128 consecutive elements of a tensor (the last
+// group of a tensor may be shorter) m = c_m s_m and sqrt(v) = c_r s_r with
+// codes c in e4m3 and fp32 scales s = (largest magnitude of the group) / 448.
+// e4m3 keeps a relative precision of 2^-4 over 2^14.8 below the largest value,
+// and 2^-9 absolute under it; the root of v is kept, not v, because the update
+// divides by the root and the same code then spans the square of that range.
+//
+// c_m is rounded to nearest: with b1 = 0.9 a step moves m by a tenth, more
+// than half a code step (1/16).  c_r cannot be: a step moves v by 1 - b2 =
+// 1e-3 of itself, so to nearest it would stand still from about the tenth step
+// on.  It goes to one of its two neighbours lo <= x < hi with the chance that
+// keeps the expected square: up when (x - lo)(x + lo) > u (hi - lo)(hi + lo)
+// (rounding at random in the root itself would raise v by the variance at
+// every step).  u comes from a hash of (seed, t, tensor, element), so a step
+// is reproducible.  A positive v never gets code 0: the update would then
+// divide by eps alone.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  // xor-shift and multiply rounds; the constants are the odd numbers next to
+  // 2^32 times the golden ratio's inverse and 2^32 times (e - 2)
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0xB7E15163u;
+  return x ^ (x >> 16);
+}
+
+// 1 / s, or 0 where the group is stored as zeros (s zero or not finite).
+__device__ __forceinline__ float code_inverse(float s) { return s > 0.0f && s < INFINITY ? 1.0f / s : 0.0f; }
+
+// The scale of a group from the bits of its largest magnitude (NaN counts as
+// largest).  A scale under 2^-126 is taken as 0.
+__device__ __forceinline__ float code_scale(uint32_t top_bits) {
+  const float s = __uint_as_float(top_bits) / 448.0f;
+  return s < 0x1p-126f ? 0.0f : s;
+}
+
+// Code of x in [0, 448] with chance h16 / 65536 (see above).
+__device__ __forceinline__ uint32_t root_code(float x, uint32_t h16, bool positive) {
+  const uint32_t bits = __float_as_uint(x);
+  uint32_t code;
+  float lo, step;
+  if (x < 0x1p-6f) {
+    code = static_cast<uint32_t>(x * 512.0f);
+    lo = static_cast<float>(code) * (1.0f / 512.0f);
+    step = 0x1p-9f;
+  } else {
+    code = (bits >> 20) - (120u << 3);
+    lo = __uint_as_float(bits & ~0xFFFFFu);
+    step = __uint_as_float((bits & 0x7F800000u) - (3u << 23));
+  }
+  const float u = (static_cast<float>(h16) + 0.5f) * (1.0f / 65536.0f);
+  const float hi = lo + step;
+  const bool up = (x - lo) * (x + lo) > u * ((hi - lo) * (hi + lo)) || (code == 0 && positive);
+  return code + (up ? 1u : 0u);
+}
+
+__device__ __forceinline__ uint32_t group_max(uint32_t x) {  // over 16 consecutive lanes
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), d));
+    x = x > y ? x : y;
+  }
+  return x;
+}
+
+template <int DW, int DG>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Adamw8Args a) {
+  const int t = find_tensor(a.t, blockIdx.x);
+  const int64_t n = a.t.size[t];
+  void* W = a.W[a.t.first + t];
+  const void* G = a.G[a.t.first + t];
+  uint8_t* mc = static_cast<uint8_t*>(a.mc[a.t.first + t]);
+  uint8_t* rc = static_cast<uint8_t*>(a.rc[a.t.first + t]);
+  float* ms = static_cast<float*>(a.ms[a.t.first + t]);
+  float* rs = static_cast<float*>(a.rs[a.t.first + t]);
+  const Scalars r = load_scalars(a.s);
+  const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
+  const int64_t i = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8 + 8 * static_cast<int>(threadIdx.x);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(W) & 15) | (reinterpret_cast<uintptr_t>(G) & 15) |
+                        (reinterpret_cast<uintptr_t>(mc) & 7) | (reinterpret_cast<uintptr_t>(rc) & 7)) == 0;
+  const bool whole = aligned && i + 8 <= n;
+  const bool any = i < n;
+  float w[8], g[8], m[8], v[8];
+  uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
+  if (whole) {
+    float x[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load4<DW>(W, i + 4 * h, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[4 * h + k] = x[k];
+      load4<DG>(G, i + 4 * h, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[4 * h + k] = x[k];
+    }
+    const uint2 a2 = *reinterpret_cast<const uint2*>(mc + i), b2 = *reinterpret_cast<const uint2*>(rc + i);
+    cm[0] = a2.x; cm[1] = a2.y; cr[0] = b2.x; cr[1] = b2.y;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = i + k < n;
+      w[k] = in ? load_f<DW>(W, i + k) : 0.0f;
+      g[k] = in ? load_f<DG>(G, i + k) : 0.0f;
+      cm[k >> 2] |= (in ? static_cast<uint32_t>(mc[i + k]) : 0u) << (8 * (k & 3));
+      cr[k >> 2] |= (in ? static_cast<uint32_t>(rc[i + k]) : 0u) << (8 * (k & 3));
+    }
+  }
+  const float sm = any ? ms[i / kGroup] : 0.0f, sr = any ? rs[i / kGroup] : 0.0f;
+  uint32_t top_m = 0, top_v = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t cmk = cm[k >> 2], crk = cr[k >> 2];
+    const auto pm = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(cmk, true) : __builtin_amdgcn_cvt_pk_f32_fp8(cmk, false);
+    const auto pr = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(crk, true) : __builtin_amdgcn_cvt_pk_f32_fp8(crk, false);
+    m[k] = pm[k & 1] * sm;
+    const float root = pr[k & 1] * sr;
+    v[k] = root * root;
+    update(w[k], g[k], m[k], v[k], a.s, r);
+    if (i + k >= n) m[k] = v[k] = 0.0f;
+    const uint32_t bm = __float_as_uint(m[k]) & 0x7fffffffu, bv = __float_as_uint(v[k]) & 0x7fffffffu;
+    top_m = bm > top_m ? bm : top_m;
+    top_v = bv > top_v ? bv : top_v;
+  }
+  const float sm2 = code_scale(group_max(top_m));
+  const float sr2 = code_scale(__float_as_uint(sqrtf(__uint_as_float(group_max(top_v)))));
+  const float im = code_inverse(sm2), ir = code_inverse(sr2);
+  uint32_t nm[2] = {0, 0}, nr[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const float x0 = im > 0.0f ? fminf(fmaxf(m[k] * im, -448.0f), 448.0f) : 0.0f;
+    const float x1 = im > 0.0f ? fminf(fmaxf(m[k + 1] * im, -448.0f), 448.0f) : 0.0f;
+    if (k & 2) {
+      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, nm[k >> 2], true);
+    } else {
+      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, nm[k >> 2], false);
+    }
+    const uint32_t h = mix(static_cast<uint32_t>((i + k) >> 1) + key);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = ir > 0.0f ? fminf(sqrtf(v[k + e]) * ir, 448.0f) : 0.0f;
+      const uint32_t c = root_code(x, e == 0 ? h & 0xffffu : h >> 16, ir > 0.0f && v[k + e] > 0.0f);
+      nr[k >> 2] |= c << (8 * ((k + e) & 3));
+    }
+  }
+  if (whole) {
+    float x[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = w[4 * h + k];
+      store4<DW>(W, i + 4 * h, x);
+    }
+    *reinterpret_cast<uint2*>(mc + i) = make_uint2(nm[0], nm[1]);
+    *reinterpret_cast<uint2*>(rc + i) = make_uint2(nr[0], nr[1]);
+  } else {
+    for (int k = 0; k < 8 && i + k < n; ++k) {
+      store_from_f32(W, i + k, DW, w[k]);
+      mc[i + k] = static_cast<uint8_t>(nm[k >> 2] >> (8 * (k & 3)));
+      rc[i + k] = static_cast<uint8_t>(nr[k >> 2] >> (8 * (k & 3)));
+    }
+  }
+  if (any && (threadIdx.x & 15) == 0) {
+    ms[i / kGroup] = sm2;
+    rs[i / kGroup] = sr2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+muon_status make_scalars(const muon_adamw_config* cfg, AdamwScalars* s) {
+  if (cfg == nullptr) return MUON_ERR_INVALID_ARG;
+  if (!isfinite(cfg->lr) || !isfinite(cfg->weight_decay) || !isfinite(cfg->eps)) return MUON_ERR_INVALID_ARG;
+  if (!(cfg->beta1 >= 0.0) || !(cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0) || !(cfg->beta2 < 1.0))
+    return MUON_ERR_INVALID_ARG;
+  if (!(static_cast<float>(cfg->eps) > 0.0f)) return MUON_ERR_INVALID_ARG;
+  if (cfg->step_dev == nullptr && cfg->step < 1) return MUON_ERR_INVALID_ARG;
+  memset(s, 0, sizeof(*s));
+  s->lr = static_cast<float>(cfg->lr);
+  s->wd = static_cast<float>(cfg->weight_decay);
+  s->eps = static_cast<float>(cfg->eps);
+  if (!isfinite(s->lr) || !isfinite(s->wd) || !isfinite(s->eps)) return MUON_ERR_INVALID_ARG;
+  s->beta1 = cfg->beta1;
+  s->beta2 = cfg->beta2;
+  s->b1 = static_cast<float>(cfg->beta1);
+  s->b2 = static_cast<float>(cfg->beta2);
+  s->ob1 = static_cast<float>(1.0 - cfg->beta1);  // rounded once: 1 - (float)beta2 is off by 1e-5
+  s->ob2 = static_cast<float>(1.0 - cfg->beta2);
+  s->step = cfg->step;
+  s->step_dev = cfg->step_dev;
+  s->grad_scale = cfg->grad_scale;
+  s->seed = cfg->seed;
+  if (cfg->step_dev == nullptr) {
+    s->c1 = static_cast<float>(1.0 / (1.0 - pow(cfg->beta1, static_cast<double>(cfg->step))));
+    s->c2 = static_cast<float>(1.0 / sqrt(1.0 - pow(cfg->beta2, static_cast<double>(cfg->step))));
+  }
+  return MUON_OK;
+}
+
+// Sizes in range, pointer arrays present and distinct, types known.
+muon_status check_lists(int tensors, const int64_t* sizes, const void* const* arrays, int narrays, muon_dtype w_dtype,
+                        muon_dtype g_dtype, int chunk) {
+  if (tensors < 1 || sizes == nullptr) return MUON_ERR_INVALID_ARG;
+  for (int i = 0; i < narrays; ++i) {
+    if (arrays[i] == nullptr) return MUON_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (arrays[i] == arrays[j]) return MUON_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < tensors; ++i)
+    if (sizes[i] < 0 || sizes[i] / chunk >= (1 << 23)) return MUON_ERR_INVALID_ARG;  // over any device's memory
+  const muon_dtype types[2] = {w_dtype, g_dtype};
+  for (muon_dtype d : types)
+    if (d != MUON_F32 && d != MUON_BF16 && d != MUON_F16) return MUON_ERR_INVALID_ARG;
+  if (w_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
+  return MUON_OK;
+}
+
+// The next launch's table from tensor `at` on: as many tensors as fit and as
+// keep the blocks under the grid's limit.  Returns the blocks.
+uint32_t fill_table(TensorTable* t, int tensors, const int64_t* sizes, int at, int chunk) {
+  t->first = at;
+  t->count = 0;
+  uint32_t blocks = 0;
+  t->start[0] = 0;
+  while (t->count < kMaxTensors && at + t->count < tensors) {
+    const int64_t n = sizes[at + t->count];
+    const uint32_t b = static_cast<uint32_t>((n + chunk - 1) / chunk);
+    if (t->count > 0 && blocks + b > (1u << 23)) break;
+    blocks += b;
+    t->size[t->count++] = n;
+    t->start[t->count] = blocks;
+  }
+  return blocks;
+}
+
+// Calls fn<DW, DG> for the given types.
+#define ADAMW_DISPATCH(kernel, args, blocks, w, g, s)                                                             \
+  do {                                                                                                            \
+    const dim3 grid_(blocks), block_(kThreads);                                                                   \
+    if ((w) == MUON_F32) {                                                                                        \
+      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kF32, kF32>), grid_, block_, 0, s, args);                   \
+      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kF32, kBF16>), grid_, block_, 0, s, args);            \
+      else hipLaunchKernelGGL((kernel<kF32, kF16>), grid_, block_, 0, s, args);                                   \
+    } else {                                                                                                      \
+      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kBF16, kF32>), grid_, block_, 0, s, args);                  \
+      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kBF16, kBF16>), grid_, block_, 0, s, args);           \
+      else hipLaunchKernelGGL((kernel<kBF16, kF16>), grid_, block_, 0, s, args);                                  \
+    }                                                                                                             \
+  } while (0)
+
+template <class Args, class Launch>
+muon_status run_lists(Args& a, int tensors, const int64_t* sizes, int chunk, double state_bytes, muon_dtype w_dtype,
+                      muon_dtype g_dtype, const char* kernel, const char* role, hipStream_t s, Launch&& launch) {
+  for (int at = 0; at < tensors;) {
+    const uint32_t blocks = fill_table(&a.t, tensors, sizes, at, chunk);
+    at += a.t.count;
+    if (blocks == 0) continue;  // empty tensors only
+    double elems = 0.0;
+    for (int i = 0; i < a.t.count; ++i) elems += static_cast<double>(a.t.size[i]);
+    const double bytes = elems * ((w_dtype == MUON_F32 ? 8.0 : 4.0) + (g_dtype == MUON_F32 ? 4.0 : 2.0) + state_bytes);
+    const hipError_t err = traced_launch(s, kernel, role, 0.0, bytes, [&] {
+      launch(blocks);
+      return hipGetLastError();
+    });
+    if (err != hipSuccess) return MUON_ERR_HIP;
+  }
+  return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+void muon_adamw_config_init(muon_adamw_config* cfg) {
+  if (cfg == nullptr) return;
+  memset(cfg, 0, sizeof(*cfg));
+  cfg->lr = 1e-3;
+  cfg->beta1 = 0.9;
+  cfg->beta2 = 0.999;
+  cfg->eps = 1e-8;
+  cfg->step = 1;
+}
+
+muon_status muon_adamw_step(int tensors, const int64_t* sizes, void* const* W, muon_dtype w_dtype, void* const* M,
+                            void* const* V, const void* const* G, muon_dtype g_dtype, const muon_adamw_config* cfg,
+                            void* stream) {
+  const void* arrays[4] = {W, M, V, G};
+  muon_status st = check_lists(tensors, sizes, arrays, 4, w_dtype, g_dtype, kChunk32);
+  if (st != MUON_OK) return st;
+  Adamw32Args a;
+  st = make_scalars(cfg, &a.s);
+  if (st != MUON_OK) return st;
+  a.W = W;
+  a.G = G;
+  a.M = M;
+  a.V = V;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return run_lists(a, tensors, sizes, kChunk32, 16.0, w_dtype, g_dtype, "adamw_kernel", "adamw", s,
+                   [&](uint32_t blocks) { ADAMW_DISPATCH(adamw_kernel, a, blocks, w_dtype, g_dtype, s); });
+}
+
+muon_status muon_adamw8_step(int tensors, const int64_t* sizes, void* const* W, muon_dtype w_dtype,
+                             const muon_adamw8_state* state, const void* const* G, muon_dtype g_dtype,
+                             const muon_adamw_config* cfg, void* stream) {
+  if (state == nullptr) return MUON_ERR_INVALID_ARG;
+  const void* arrays[6] = {W, state->m_codes, state->m_scales, state->r_codes, state->r_scales, G};
+  muon_status st = check_lists(tensors, sizes, arrays, 6, w_dtype, g_dtype, kChunk8);
+  if (st != MUON_OK) return st;
+  Adamw8Args a;
+  st = make_scalars(cfg, &a.s);
+  if (st != MUON_OK) return st;
+  a.W = W;
+  a.G = G;
+  a.mc = state->m_codes;
+  a.ms = state->m_scales;
+  a.rc = state->r_codes;
+  a.rs = state->r_scales;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return run_lists(a, tensors, sizes, kChunk8, 4.0 + 16.0 / kGroup, w_dtype, g_dtype, "adamw8_kernel", "adamw8", s,
+                   [&](uint32_t blocks) { ADAMW_DISPATCH(adamw8_kernel, a, blocks, w_dtype, g_dtype, s); });
+}
+
+}  // extern "C"

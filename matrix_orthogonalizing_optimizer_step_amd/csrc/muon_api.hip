@@ -1041,6 +1041,11 @@ muon_status group8_codec(bool dequantize, int batch, int rows, int k, void* cons
 // ---------------------------------------------------------------------------
 }  // namespace
 
+hipError_t muon::traced_launch(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
+                               const std::function<hipError_t()>& launch) {
+  return traced(s, kernel, role, flops, bytes, launch);
+}
+
 // Scratch memory of muon_step_fixed_scratch, for callers that cannot
 // allocate: one copy per device, held until the process ends.  Host code
 // never uses this name as an address; it takes the device address from

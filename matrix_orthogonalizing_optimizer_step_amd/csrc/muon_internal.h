@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <functional>
+
 namespace muon {
 
 // Every workspace dimension is padded to a multiple of this, so the GEMM
@@ -99,6 +101,11 @@ hipError_t launch_gemm_bf16(const GemmArgs& a, int batch, int kind, hipStream_t 
 hipError_t launch_gemm_f16(const GemmArgs& a, int batch, int kind, hipStream_t s);
 hipError_t launch_gemm_f32(const GemmArgs& a, int batch, hipStream_t s);
 int gemm_tile(int op);  // block tile edge of the GEMM kernel used for an operand type
+
+// Runs `launch`, bracketed by the launch trace's events if the trace is on
+// (muon_trace_enable), with the launch's kernel, role and algorithmic work.
+hipError_t traced_launch(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
+                         const std::function<hipError_t()>& launch);
 
 struct NormArgs {
   const void* const* M;   // user matrices

@@ -1,0 +1,345 @@
+"""AdamW steps (32-bit and 8-bit moments) on the device against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import matrix_orthogonalizing_optimizer_step_amd as mu
+from oracle import adamw_oracle as ao
+from synth import inputs as syn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}  # half a step relative to the value
+f64 = syn.to_f64
+
+
+def make(sizes, w, g, seed, offset=0, first=False, zero_every=0):
+    """Lists W, M, V, G on the device; ``offset`` elements in front make the views misaligned."""
+    rng = np.random.default_rng(seed)
+
+    def put(a, dt):
+        buf = torch.zeros(a.size + offset + 3, dtype=dt, device=DEV)
+        buf[offset:offset + a.size] = torch.from_numpy(a).to(DEV).to(dt)
+        return buf[offset:offset + a.size]
+
+    W, M, V, G = [], [], [], []
+    for j, n in enumerate(sizes):
+        gr = rng.standard_normal(n).astype(np.float32) * 1e-2
+        if zero_every:
+            gr[(np.arange(n) // zero_every) % 2 == 0] = 0.0
+        W.append(put(rng.standard_normal(n).astype(np.float32) * 0.1, DT[w]))
+        M.append(put((0 if first else 1) * rng.standard_normal(n).astype(np.float32) * 3e-3, torch.float32))
+        V.append(put((0 if first else 1) * np.square(rng.standard_normal(n).astype(np.float32) * 1e-2), torch.float32))
+        G.append(put(gr, DT[g]))
+    return W, M, V, G
+
+
+def compare32(W, M, V, G, W0, M0, V0, t, w, **kw):
+    for k in range(len(W)):
+        args = (f64(W0[k]), f64(M0[k]), f64(V0[k]), f64(G[k]), t, kw["lr"], kw["beta1"], kw["beta2"], kw["eps"],
+                kw["weight_decay"], kw.get("scale", 1.0))
+        want = ao.adamw(*args)
+        tol = ao.adamw_tolerance(*args, w_half=HALF[w])
+        for name, got, ref, bound in zip("WMV", (W[k], M[k], V[k]), want, tol):
+            bad = np.abs(f64(got) - ref) > bound
+            assert not bad.any(), f"tensor {k} {name}: {bad.sum()} of {bad.size} out of bounds"
+
+
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.05)
+
+
+@pytest.mark.parametrize("w", ["f32", "bf16"])
+@pytest.mark.parametrize("g", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("sizes,offset", [((1,), 0), ((3, 0, 4096, 5), 0), ((4097, 2, 12345), 0), ((4099, 257), 1),
+                                          ((8192 + 3, 1, 1, 64), 4)])
+def test_adamw_against_oracle(w, g, sizes, offset):
+    print(w, g, sizes, offset, flush=True)
+    W, M, V, G = make(sizes, w, g, 11, offset)
+    W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+    G0 = [x.clone() for x in G]
+    mu.adamw_step(W, M, V, G, 7, **HYPER)
+    torch.cuda.synchronize()
+    compare32(W, M, V, G, W0, M0, V0, 7, w, **HYPER)
+    assert all(torch.equal(a, b) for a, b in zip(G, G0))
+    for L in (W, M, V):  # nothing in front of or behind a tensor is touched
+        for x in L:
+            whole = torch.as_strided(x, (x.numel() + offset + 3,), (1,), 0)
+            assert not whole[:offset].any() and not whole[offset + x.numel():].any()
+
+
+@pytest.mark.parametrize("count", [255, 256, 257, 700])
+def test_adamw_many_tensors(count):
+    """Lists over the number of tensors of one launch, sizes 0 among them."""
+    sizes = [(37 * i) % 311 for i in range(count)]
+    W, M, V, G = make(sizes, "f32", "f32", 12)
+    W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+    mu.adamw_step(W, M, V, G, 2, **HYPER)
+    compare32(W, M, V, G, W0, M0, V0, 2, "f32", **HYPER)
+
+
+def test_adamw_first_steps_and_shapes():
+    """From zero moments, three steps on tensors of several dimensions."""
+    W = [torch.randn(s, device=DEV, generator=torch.Generator(DEV).manual_seed(i)) for i, s in enumerate([(3, 5, 7), (64,), (33, 65)])]
+    M, V = [torch.zeros_like(x) for x in W], [torch.zeros_like(x) for x in W]
+    for t in (1, 2, 3):
+        G = [torch.randn(x.shape, device=DEV, generator=torch.Generator(DEV).manual_seed(100 * t + i)) for i, x in enumerate(W)]
+        W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+        mu.adamw_step(W, M, V, G, t, **HYPER)
+        compare32(W, M, V, G, W0, M0, V0, t, "f32", **HYPER)
+
+
+@pytest.mark.parametrize("beta1,beta2,t", [(0.0, 0.0, 1), (0.0, 0.99, 3), (0.9, 0.999, 10 ** 6), (0.95, 0.9999, 1)])
+def test_adamw_betas_and_steps(beta1, beta2, t):
+    hyper = dict(HYPER, beta1=beta1, beta2=beta2)
+    W, M, V, G = make((5000,), "f32", "f32", 13)
+    W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+    mu.adamw_step(W, M, V, G, t, **hyper)
+    compare32(W, M, V, G, W0, M0, V0, t, "f32", **hyper)
+
+
+def test_adamw_step_and_scale_on_the_device():
+    """step and grad_scale read from device memory give what the host's values give, up to the constants' rounding."""
+    scale = torch.tensor([0.25], device=DEV)
+    for t in (1, 5, 12345):
+        W, M, V, G = make((4100, 9), "f32", "bf16", 14)
+        W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+        mu.adamw_step(W, M, V, G, torch.tensor([t], device=DEV), grad_scale=scale, **HYPER)
+        compare32(W, M, V, G, W0, M0, V0, t, "f32", scale=0.25, **HYPER)
+    W, M, V, G = make((300,), "f32", "f32", 14)
+    W1, M1, V1, _ = make((300,), "f32", "f32", 14)
+    mu.adamw_step(W, M, V, G, torch.tensor([-4], device=DEV), **HYPER)  # under 1 counts as 1
+    mu.adamw_step(W1, M1, V1, G, torch.tensor([1], device=DEV), **HYPER)
+    assert torch.equal(W[0], W1[0])
+
+
+def test_adamw_non_finite_gradients_stay_in_their_elements():
+    W, M, V, G = make((5000,), "f32", "f32", 15)
+    W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+    G[0][17], G[0][4999], G[0][2] = float("nan"), float("inf"), float("-inf")
+    mu.adamw_step(W, M, V, G, 4, **HYPER)
+    bad = torch.zeros(5000, dtype=torch.bool, device=DEV)
+    bad[[17, 4999, 2]] = True
+    assert torch.isnan(W[0][bad]).all() and not torch.isfinite(M[0][bad]).any() and not torch.isfinite(V[0][bad]).any()
+    keep = [x[~bad] for x in (W[0], M[0], V[0], G[0], W0[0], M0[0], V0[0])]
+    compare32(*[[x] for x in keep], 4, "f32", **HYPER)
+
+
+def test_adamw_zero_gradient_and_state():
+    W, M, V, G = make((300,), "f32", "f32", 16, first=True)
+    G[0].zero_()
+    W0 = W[0].clone()
+    mu.adamw_step(W, M, V, G, 1, lr=0.1)
+    assert torch.equal(W[0], W0) and not M[0].any() and not V[0].any()
+
+
+def test_adamw_refuses_a_tensor_twice():
+    a, b = torch.zeros(8, device=DEV), torch.zeros(8, device=DEV)
+    z = lambda: torch.zeros(8, device=DEV)  # noqa: E731
+    with pytest.raises(ValueError, match="twice"):
+        mu.adamw_step([a, a], [z(), z()], [z(), z()], [z(), z()], 1, 1e-3)
+    with pytest.raises(ValueError, match="twice"):
+        mu.adamw_step([a], [b], [b], [z()], 1, 1e-3)
+    with pytest.raises(ValueError, match="twice"):
+        mu.adamw_step([a], [z()], [z()], [a], 1, 1e-3)
+    with pytest.raises(ValueError, match="step"):
+        mu.adamw_step([a], [z()], [z()], [z()], torch.ones(2, dtype=torch.int64, device=DEV), 1e-3)
+    with pytest.raises(ValueError, match="grad_scale"):
+        mu.adamw_step([a], [z()], [z()], [z()], 1, 1e-3, grad_scale=torch.ones(1))
+    with pytest.raises(mu.MuonError):
+        mu.adamw_step([a], [z()], [z()], [z()], 0, 1e-3)
+    assert not a.any()
+
+
+# --- 8-bit moments -------------------------------------------------------------------------------------------------
+# m and v before they are coded are fp32 values with the relative errors of adamw_tolerance, on top of the decoded
+# moments (one product each, h; v's square 2 h more): at most 10 h of the magnitudes of their terms, so x = sqrt(v) / s
+# is off by at most 12 h and x^2 - lo^2 by 24 h x^2; hi^2 - lo^2 is at least x^2 / 4.6 in the normal range (lo = 15/8
+# binade steps: (16^2 - 15^2) / 15^2 = 0.138 x^2), so the share is off by at most 24 h / 0.138 < 2^-16 < 1e-4.
+SLACK = 1e-4
+
+
+def state_of(M, V, offset=0):
+    """8-bit state coding the given moments (by the oracle's scales, torch's nearest rounding)."""
+    def view(x):
+        buf = torch.zeros(x.numel() + offset + 3, dtype=x.dtype, device=DEV)
+        buf[offset:offset + x.numel()] = x
+        return buf[offset:offset + x.numel()]
+
+    out = mu.AdamW8State([], [], [], [])
+    for codes, scales, values in ((out.m_codes, out.m_scales, M), (out.r_codes, out.r_scales, [v.sqrt() for v in V])):
+        for x in values:
+            each, s = ao.group_scales(f64(x))
+            y = np.divide(f64(x), each, out=np.zeros(x.numel()), where=each > 0)
+            codes.append(view(torch.from_numpy(np.clip(y, -448, 448)).to(torch.float8_e4m3fn).to(DEV)))
+            scales.append(view(torch.from_numpy(s).float().to(DEV)))
+    return out
+
+
+def bytes_of(x):
+    return x.view(torch.uint8).cpu().numpy()
+
+
+def step8(W, state, G, t, seed, w, hyper, scale=1.0):
+    """Runs adamw8_step and checks W, codes and scales of every tensor."""
+    W0 = [f64(x) for x in W]
+    old = [[f64(c.float()) * np.repeat(f64(s), 128)[:c.numel()] for c, s in zip(cs, ss)]
+           for cs, ss in ((state.m_codes, state.m_scales), (state.r_codes, state.r_scales))]
+    kw = {} if scale == 1.0 else dict(grad_scale=torch.tensor([scale], device=DEV))
+    mu.adamw8_step(W, state, G, t, seed=seed, **kw, **hyper)
+    torch.cuda.synchronize()
+    for k in range(len(W)):
+        n = W0[k].size
+        if n == 0:
+            continue
+        args = (W0[k], old[0][k], old[1][k] ** 2, f64(G[k]), t, hyper["lr"], hyper["beta1"], hyper["beta2"],
+                hyper["eps"], hyper["weight_decay"], scale)
+        w_new, m, v = ao.adamw(*args)
+        tol = ao.adamw_tolerance(*args, w_half=HALF[w])[0]
+        # decoding adds h to m and 3 h to v: 1 h of the first and 1.5 h of the second term of 17 h
+        assert np.all(np.abs(f64(W[k]) - w_new) <= tol * 1.25), f"tensor {k}: W"
+        bad = ao.check_moment_codes(bytes_of(state.m_codes[k]), f64(state.m_scales[k]), m, SLACK)
+        assert bad == 0, f"tensor {k}: {bad} codes of m"
+        bad = ao.check_root_codes(bytes_of(state.r_codes[k]), f64(state.r_scales[k]), v,
+                                  ao.chances(n, seed, t, k), SLACK)
+        assert bad == 0, f"tensor {k}: {bad} codes of the root of v"
+
+
+@pytest.mark.parametrize("w,g", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f16"), ("f32", "f16"),
+                                 ("bf16", "f32")])
+@pytest.mark.parametrize("sizes,offset", [((1,), 0), ((5, 0, 2048, 127, 128, 129), 0), ((12345,), 0), ((3001, 2), 1)])
+def test_adamw8_against_oracle(w, g, sizes, offset):
+    print(w, g, sizes, offset, flush=True)
+    W, M, V, G = make(sizes, w, g, 21, offset)
+    state = state_of(M, V, offset)
+    step8(W, state, G, 9, 3, w, HYPER)
+    for L in (W, state.m_codes, state.r_codes, state.m_scales, state.r_scales):
+        for x in L:
+            whole = torch.as_strided(x, (x.numel() + offset + 3,), (1,), 0).view(torch.uint8)
+            e = x.element_size()
+            assert not whole[:offset * e].any() and not whole[(offset + x.numel()) * e:].any()
+
+
+def test_adamw8_several_steps_from_zero():
+    W, _, _, _ = make((4096 + 77, 300), "f32", "f32", 22)
+    state = mu.AdamW8State.zeros(W)
+    for t in range(1, 5):
+        _, _, _, G = make((4096 + 77, 300), "f32", "bf16", 100 + t, zero_every=512)
+        step8(W, state, G, t, 99, "f32", HYPER, scale=0.5 if t == 3 else 1.0)
+    m, v = state.values()
+    assert [x.shape for x in m] == [x.shape for x in W] and all((x >= 0).all() for x in v)
+
+
+def test_adamw8_is_reproducible_and_depends_on_seed_and_step():
+    def run(seed, t):
+        W, M, V, G = make((6000,), "f32", "f32", 23)
+        s = state_of(M, V)
+        mu.adamw8_step(W, s, G, t, 1e-3, seed=seed)
+        return bytes_of(s.r_codes[0]), W[0].cpu()
+
+    a, wa = run(1, 5)
+    b, wb = run(1, 5)
+    assert np.array_equal(a, b) and torch.equal(wa, wb)
+    c, wc = run(2, 5)
+    assert not np.array_equal(a, c) and torch.equal(wa, wc)
+    assert not np.array_equal(a, run(1, 6)[0])
+
+
+def test_adamw8_non_finite_gradient_poisons_its_group_only():
+    W, M, V, G = make((1000,), "f32", "f32", 24)
+    s, clean = state_of(M, V), state_of(M, V)
+    W2 = [W[0].clone()]
+    mu.adamw8_step(W2, clean, G, 3, 1e-3)
+    G[0][130] = float("nan")
+    G[0][900] = float("inf")
+    mu.adamw8_step(W, s, G, 3, 1e-3)
+    bad = torch.zeros(1000, dtype=torch.bool)
+    bad[128:256] = bad[896:1000] = True
+    m, v = s.values()
+    assert torch.equal(~torch.isfinite(m[0].cpu()), bad) and torch.equal(~torch.isfinite(v[0].cpu()), bad)
+    assert not s.m_codes[0].float().cpu()[bad].any() and not s.r_codes[0].float().cpu()[bad].any()
+    assert torch.equal(m[0].cpu()[~bad], clean.values()[0][0].cpu()[~bad])
+    wrong = (W[0] != W2[0]).cpu()
+    assert wrong.sum() <= 2 and wrong[130]  # W sees the gradient's own element only
+
+
+def test_adamw8_follows_a_second_moment_that_changes_slowly():
+    """Constant |g| = 2 after a state of 1: v has to approach 4 as 1 - 0.999^t does, which rounding to nearest would
+    not do at all.  4096 elements, 400 steps: mean v = 4 - 3 * 0.999^400 = 1.990.  The mean over 4096 independent
+    elements has a standard deviation of at most (v's spread, under one code step of v, 25 %) * 2 / 64 < 1 %."""
+    n = 4096
+    W = [torch.zeros(n, device=DEV)]
+    one = torch.ones(n, device=DEV)
+    one[::128] = 4.0  # a larger neighbour in every group keeps the scale away from the others
+    state = state_of([one * 0], [one * one])
+    G = [torch.where(one > 1, 4.0, 2.0)]
+    for t in range(1, 401):
+        mu.adamw8_step(W, state, G, t, 0.0, seed=8)
+    v = state.values()[1][0][one == 1]
+    want = 4 - 3 * 0.999 ** 400
+    assert abs(v.double().mean().item() - want) < 0.05 * want
+
+
+# --- graphs, streams -----------------------------------------------------------------------------------------------
+def test_adamw_captured_with_a_step_on_the_device():
+    """Replays of one captured step of both kinds equal eager steps, with eager work in between."""
+    sizes = (5000, 33)
+    W, M, V, G = make(sizes, "f32", "bf16", 31)
+    W8, M8, V8, _ = make(sizes, "f32", "bf16", 32)
+    s8 = state_of(M8, V8)
+    t = torch.tensor([4], device=DEV)
+    copy = lambda L: [x.clone() for x in L]  # noqa: E731
+    eW, eM, eV, eW8 = copy(W), copy(M), copy(V), copy(W8)
+    e8 = mu.AdamW8State(*(copy(L) for L in (s8.m_codes, s8.m_scales, s8.r_codes, s8.r_scales)))
+
+    def both(W, M, V, W8, s8, t):
+        mu.adamw_step(W, M, V, G, t, **HYPER)
+        mu.adamw8_step(W8, s8, G, t, seed=1, **HYPER)
+
+    keep = [copy(L) for L in (W, M, V, W8, s8.m_codes, s8.m_scales, s8.r_codes, s8.r_scales)]
+    both(W, M, V, W8, s8, t)  # builds the pointer arrays
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        t += 1
+        both(W, M, V, W8, s8, t)
+    for L, K in zip((W, M, V, W8, s8.m_codes, s8.m_scales, s8.r_codes, s8.r_scales), keep):
+        for x, k in zip(L, K):
+            x.copy_(k)
+    for i in range(4):
+        graph.replay()
+        both(eW, eM, eV, eW8, e8, torch.tensor([5 + i], device=DEV))
+        torch.cuda.synchronize()
+        for a, b in zip([*W, *M, *V, *W8, *s8.m_scales, *s8.r_scales], [*eW, *eM, *eV, *eW8, *e8.m_scales, *e8.r_scales]):
+            assert torch.equal(a, b), i
+        for a, b in zip([*s8.m_codes, *s8.r_codes], [*e8.m_codes, *e8.r_codes]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+    assert t.item() == 8
+
+
+def test_adamw_on_side_streams():
+    """Two calls at once on two streams, on tensors made there."""
+    ref = make((70000,), "f32", "f32", 41)
+    mu.adamw_step(*ref, 3, **HYPER)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sets = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            sets.append(make((70000,), "f32", "f32", 41))
+    torch.cuda.synchronize()
+    for s, x in zip(streams, sets):
+        mu.adamw_step(*x, 3, stream=s, **HYPER)
+    torch.cuda.synchronize()
+    for x in sets:
+        assert all(torch.equal(a[0], b[0]) for a, b in zip(x, ref))
+
+
+def test_adamw_launches_are_traced():
+    W, M, V, G = make((5000,), "f32", "bf16", 42)
+    mu.trace_enable(True)
+    mu.adamw_step(W, M, V, G, 1, 1e-3)
+    mu.adamw8_step(W, mu.AdamW8State.zeros(W), G, 1, 1e-3)
+    recs = mu.trace_collect()
+    mu.trace_enable(False)
+    assert [r["role"] for r in recs] == ["adamw", "adamw8"]
