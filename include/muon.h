@@ -26,7 +26,8 @@
  *   Matrices are dense, row-major, contiguous (leading dimension = cols) and
  *   live in device memory.  A call works on a batch of `batch` matrices of one
  *   shape rows x cols; matrix arguments are DEVICE arrays of `batch` device
- *   pointers (one per matrix), so independent tensors can be batched.  The
+ *   pointers (one per matrix), so independent tensors can be batched (the AdamW
+ *   step and the microscaled code take HOST arrays, see there).  The
  *   caller owns every buffer, including the workspace; the library allocates
  *   no device memory.  A matrix with rows > cols is iterated transposed
  *   ([GNS §1.2] works with n = min(rows, cols) <= m = max(rows, cols)); the
@@ -336,13 +337,15 @@ muon_status muon_group8_dequantize(int batch, int rows, int k, const void *const
  *   tensors   length of the list, at least 1.
  *   sizes     HOST array of `tensors` element counts (read during the call
  *             only), 0 or more; a tensor of size 0 is passed over.
- *   W         device array of device pointers, w_dtype F32 or BF16, updated in
- *             place.
- *   M, V      device arrays of device pointers to fp32 moments, updated in
- *             place.  The first step of a run passes zeros.
- *   G         device array of device pointers, gradients (F32, BF16 or F16).
+ *   W         device pointers, w_dtype F32 or BF16, updated in place.
+ *   M, V      device pointers to fp32 moments, updated in place.  The first
+ *             step of a run passes zeros.
+ *   G         device pointers, gradients (F32, BF16 or F16).
  *   cfg       fill with muon_adamw_config_init() and change fields; not NULL.
- * The four arrays must be distinct, and no two of the buffers may overlap.
+ * W, M, V and G are HOST arrays of `tensors` device pointers, read during the
+ * call only: such lists are long and their gradients move, so the pointers
+ * travel as kernel arguments (one launch per 87 tensors) instead of in an array
+ * in device memory.  They must be distinct, and no two of the buffers may overlap.
  * Buffers need the alignment of their element type only; 16-byte aligned ones
  * are faster.  Errors as for muon_step; MUON_ERR_INVALID_ARG also for lr, eps
  * or weight_decay not finite in fp32, eps <= 0, betas outside [0, 1) or step < 1.
@@ -392,9 +395,9 @@ muon_status muon_adamw_step(int tensors, const int64_t *sizes, void *const *W, m
  *             positive v never gets code 0.
  * A NaN or an infinity among a group's new moments makes its scale NaN or
  * infinite and its codes 0: the whole group's moments then read as NaN.
- *   state     device arrays of device pointers, updated in place: codes of
+ *   state     HOST arrays of device pointers, updated in place: codes of
  *             sizes[j] bytes, scales of ceil(sizes[j] / 128) floats.  The first
- *             step of a run passes zeros.
+ *             step of a run passes zeros.  One launch per 64 tensors.
  * Everything else as for muon_adamw_step.
  */
 typedef struct muon_adamw8_state {
@@ -423,7 +426,9 @@ muon_status muon_adamw8_step(int tensors, const int64_t *sizes, void *const *W, 
  *   codes   uint8 [units][rows][64], element 2 i in the low, 2 i + 1 in the
  *           high half of byte i of its unit; 16-byte aligned
  *   scales  uint8 [units][rows][4]; 4-byte aligned.
- * Every argument is a device array of `batch` device pointers, batch <= 65535.
+ * Every matrix argument is a HOST array of `batch` device pointers, read during
+ * the call only (a layer's products come one or a few at a time; the pointers
+ * travel as kernel arguments, one launch per 16 matrices).
  *
  * muon_mx4_quantize codes rows x cols matrices X (F32, BF16 or F16) along
  * their rows (codes, scales), along their columns (codes_t, scales_t: the code

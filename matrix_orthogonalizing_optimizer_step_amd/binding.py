@@ -10,6 +10,7 @@ fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from collections import OrderedDict
 from dataclasses import dataclass
@@ -219,11 +220,8 @@ def pointer_array(tensors: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
     not take: call once with the same tensors before capturing.  An array used
     during a capture is kept for the life of the process, since the graph
     reads it at every replay."""
-    return _pointer_array(tuple(int(t.data_ptr()) for t in tensors), tensors[0].device, stream)
-
-
-def _pointer_array(ptrs: tuple, dev, stream=None) -> torch.Tensor:
-    """pointer_array of the data pointers themselves."""
+    ptrs = tuple(int(t.data_ptr()) for t in tensors)
+    dev = tensors[0].device
     key = (str(dev), ptrs)
     if dev.type != "cuda":  # host tensors (argument checks without a device)
         ent = _ptr_cache.get(key)
@@ -639,6 +637,7 @@ class AdamW8State:
 
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
 _get_device, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_dtype = operator.attrgetter("dtype")
 
 
 def _list_of(tensors, name: str, sizes, device: int, dtypes):
@@ -646,7 +645,7 @@ def _list_of(tensors, name: str, sizes, device: int, dtypes):
     ``dtypes`` and have the given sizes."""
     if len(tensors) != len(sizes):
         raise ValueError(f"{name}: one tensor per tensor of W is needed")
-    types = {t.dtype for t in tensors}
+    types = set(map(_dtype, tensors))
     if len(types) != 1 or not types <= dtypes:
         raise ValueError(f"{name}: all tensors must share one dtype of {sorted(str(d) for d in dtypes)}")
     if set(map(_get_device, tensors)) != {device}:
@@ -658,41 +657,9 @@ def _list_of(tensors, name: str, sizes, device: int, dtypes):
     return tuple(map(_data_ptr, tensors))
 
 
-def _adamw_call(W, lists, G, config, stream, launch):
-    """Checks of both AdamW steps: ``lists`` = (name, tensors, sizes or None for W's, dtype) of the state;
-    ``launch(library, sizes, W, state arrays, G, w dtype, g dtype, config, stream)``."""
-    lib = load_library()
-    if len(W) == 0:
-        raise ValueError("W: empty list")
-    sizes = tuple(map(_numel, W))
-    device = W[0].get_device()
-    if device < 0:
-        raise ValueError("W: tensors must be device tensors")
-    pw = _list_of(W, "W", sizes, device, {torch.float32, torch.bfloat16})
-    pg = _list_of(G, "G", sizes, device, set(_DT))
-    ps = [_list_of(t, name, n or sizes, device, {dt}) for name, t, n, dt in lists]
-    used = [p for q in (pw, pg, *ps) for p in q if p != 0]
-    if len(set(used)) != len(used):
-        raise ValueError("W, G and the state must be tensors of their own: one of them is in the lists twice")
-    lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed = config
-    c = _AdamWConfig(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 0, None, None,
-                     int(seed) & 0xFFFFFFFF)
-    for name, t, dt in (("step", step, torch.int64), ("grad_scale", grad_scale, torch.float32)):
-        if isinstance(t, torch.Tensor) and (t.numel() != 1 or t.dtype != dt or t.get_device() != device):
-            raise ValueError(f"{name}: a tensor must be one {dt} on the device of W")
-    if isinstance(step, torch.Tensor):
-        c.step_dev = step.data_ptr()
-    else:
-        c.step = int(step)
-    if grad_scale is not None:
-        if not isinstance(grad_scale, torch.Tensor):
-            raise ValueError("grad_scale must be a device tensor or None")
-        c.grad_scale = grad_scale.data_ptr()
-    dev = W[0].device
-    with _on(dev):
-        arrays = [_pointer_array(p, dev, stream).data_ptr() for p in (pw, pg, *ps)]
-        _check(launch(lib, (ctypes.c_int64 * len(sizes))(*sizes), arrays[0], arrays[2:], arrays[1], _DT[W[0].dtype],
-                      _DT[G[0].dtype], ctypes.byref(c), _stream(stream)))
+def _host_pointers(ptrs):
+    """A host array of device pointers (read by the library during the call)."""
+    return (ctypes.c_void_p * len(ptrs))(*ptrs)
 
 
 class _Same:
@@ -706,9 +673,55 @@ class _Same:
 _same = _Same()
 
 
-def _on(dev):
-    """The context in which ``dev`` is the current device."""
-    return _same if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _on(index: int):
+    """The context in which device ``index`` is the current one."""
+    return _same if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _raw_stream(stream, index: int) -> int:
+    """The handle of ``stream`` (None = device ``index``'s current stream)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+
+
+_W_TYPES, _F32, _F8 = {torch.float32, torch.bfloat16}, {torch.float32}, {torch.float8_e4m3fn}
+_G_TYPES = set(_DT)
+
+
+def _adamw_call(entry: str, W, lists, G, config, stream):
+    """Checks and call of both AdamW steps: ``lists`` = (name, tensors, sizes or None for W's, dtypes) of the state."""
+    lib = load_library()
+    if len(W) == 0:
+        raise ValueError("W: empty list")
+    sizes = tuple(map(_numel, W))
+    device = W[0].get_device()
+    if device < 0:
+        raise ValueError("W: tensors must be device tensors")
+    pw = _list_of(W, "W", sizes, device, _W_TYPES)
+    pg = _list_of(G, "G", sizes, device, _G_TYPES)
+    ps = [_list_of(t, name, n or sizes, device, types) for name, t, n, types in lists]
+    used = [p for q in (pw, pg, *ps) for p in q if p]
+    if len(set(used)) != len(used):
+        raise ValueError("W, G and the state must be tensors of their own: one of them is in the lists twice")
+    lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed = config
+    c = _AdamWConfig(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 0, None, None,
+                     int(seed) & 0xFFFFFFFF)
+    if isinstance(step, torch.Tensor):
+        if step.numel() != 1 or step.dtype != torch.int64 or step.get_device() != device:
+            raise ValueError("step: a tensor must be one int64 on the device of W")
+        c.step_dev = step.data_ptr()
+    else:
+        c.step = int(step)
+    if grad_scale is not None:
+        if not isinstance(grad_scale, torch.Tensor) or grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 \
+                or grad_scale.get_device() != device:
+            raise ValueError("grad_scale must be None or one float32 on the device of W")
+        c.grad_scale = grad_scale.data_ptr()
+    arrays = [_host_pointers(p) for p in ps]  # held until the call returns
+    state = arrays if entry == "muon_adamw_step" else [ctypes.byref(_AdamW8State(*map(ctypes.addressof, arrays)))]
+    n = len(sizes)
+    with _on(device):
+        _check(getattr(lib, entry)(n, (ctypes.c_int64 * n)(*sizes), _host_pointers(pw), _DT[W[0].dtype], *state,
+                                   _host_pointers(pg), _DT[G[0].dtype], ctypes.byref(c), _raw_stream(stream, device)))
 
 
 def adamw_step(W, M, V, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -719,26 +732,19 @@ def adamw_step(W, M, V, G, step, lr: float, beta1: float = 0.9, beta2: float = 0
     W: float32 or bfloat16, M and V: float32, G: float32, bfloat16 or float16 (one dtype per list).  ``step`` counts
     from 1; as a one-element int64 device tensor it is read by the kernel, so that a captured graph can advance it.
     ``grad_scale``: None or a one-element float32 device tensor the gradients are multiplied with."""
-    def launch(lib, sizes, w, state, g, wdt, gdt, cfg, s):
-        return lib.muon_adamw_step(len(W), sizes, w, wdt, state[0], state[1], g, gdt, cfg, s)
-
-    f32 = torch.float32
-    _adamw_call(W, (("M", M, None, f32), ("V", V, None, f32)), G,
-                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, 0), stream, launch)
+    _adamw_call("muon_adamw_step", W, (("M", M, None, _F32), ("V", V, None, _F32)), G,
+                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, 0), stream)
 
 
 def adamw8_step(W, state: AdamW8State, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                 eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, seed: int = 0, stream=None):
     """adamw_step with the moments in 8 bits: W and the state are updated in place.  ``seed`` with ``step`` fixes the
     random roundings of the second moment's codes."""
-    def launch(lib, sizes, w, arrays, g, wdt, gdt, cfg, s):
-        return lib.muon_adamw8_step(len(W), sizes, w, wdt, ctypes.byref(_AdamW8State(*arrays)), g, gdt, cfg, s)
-
-    groups = tuple(_nb(w.numel()) for w in W)
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    _adamw_call(W, (("m_codes", state.m_codes, None, f8), ("m_scales", state.m_scales, groups, f32),
-                    ("r_codes", state.r_codes, None, f8), ("r_scales", state.r_scales, groups, f32)), G,
-                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed), stream, launch)
+    groups = tuple([(w.numel() + GRID - 1) // GRID for w in W])
+    _adamw_call("muon_adamw8_step", W,
+                (("m_codes", state.m_codes, None, _F8), ("m_scales", state.m_scales, groups, _F32),
+                 ("r_codes", state.r_codes, None, _F8), ("r_scales", state.r_scales, groups, _F32)), G,
+                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed), stream)
 
 
 # ---------------------------------------------------------------------------
@@ -758,84 +764,91 @@ class MX4:
 
     @classmethod
     def empty(cls, batch: int, rows: int, cols: int, device, stream=None):
-        dev = torch.device(device)
+        """Uninitialised buffers for the code of ``batch`` rows x cols matrices."""
         units = _nb(cols)
-        if stream is None:
-            buf = torch.empty(batch, units * rows * 68, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(_stream_obj(stream, dev)):
-                buf = torch.empty(batch, units * rows * 68, dtype=torch.uint8, device=dev)
         split = batch * units * rows * 64  # all codes first, so that every matrix's codes are 16-byte aligned
-        flat = buf.view(-1)
-        return cls(list(flat[:split].view(batch, units, rows, 64).unbind(0)),
-                   list(flat[split:].view(batch, units, rows, 4).unbind(0)), int(cols))
+        flat = _allocate((batch * units * rows * 68,), torch.uint8, device, stream)
+        codes = torch.as_strided(flat, (batch, units, rows, 64), (units * rows * 64, rows * 64, 64, 1))
+        scales = torch.as_strided(flat, (batch, units, rows, 4), (units * rows * 4, rows * 4, 4, 1), split)
+        return cls(list(codes.unbind(0)), list(scales.unbind(0)), int(cols))
+
+
+def _allocate(shape, dtype, device, stream):
+    """torch.empty whose memory belongs to ``stream`` (None = the current stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_obj(stream, torch.device(device))):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _mx4_check(q, name: str):
-    """(batch, rows, cols, device) of a code."""
+    """(batch, rows, cols, device index) of a code, and the data pointers of its codes and scales."""
     if len(q.codes) == 0 or len(q.codes) != len(q.scales):
         raise ValueError(f"{name}: codes and scales must hold one tensor per matrix")
-    c0 = q.codes[0]
-    shape, dev = c0.shape, c0.device
-    if len(shape) != 3 or shape[0] != _nb(q.cols) or shape[1] < 1 or shape[2] != 64 or q.cols < 1:
+    shape, device, cols = tuple(q.codes[0].shape), q.codes[0].get_device(), q.cols
+    if len(shape) != 3 or cols < 1 or shape[0] != _nb(cols) or shape[1] < 1 or shape[2] != 64:
         raise ValueError(f"{name}: codes must be (ceil(cols / 128), rows, 64)")
-    if dev.type != "cuda":
+    if device < 0:
         raise ValueError(f"{name}: codes must be device tensors")
-    for t, last, align in [(c, 64, 16) for c in q.codes] + [(s, 4, 4) for s in q.scales]:
-        if t.dtype != torch.uint8 or t.device != dev or tuple(t.shape) != (shape[0], shape[1], last):
-            raise ValueError(f"{name}: all codes and scales must be uint8 of one shape and device")
-        if not t.is_contiguous() or t.data_ptr() % align:
-            raise ValueError(f"{name}: codes and scales must be contiguous, codes 16-byte and scales 4-byte aligned")
-    return len(q.codes), shape[1], q.cols, dev
+    pointers = []
+    for tensors, want, align in ((q.codes, shape, 16), (q.scales, (shape[0], shape[1], 4), 4)):
+        ptrs = []
+        for t in tensors:
+            p = t.data_ptr()
+            if t.dtype != torch.uint8 or t.get_device() != device or t.shape != want:
+                raise ValueError(f"{name}: all codes and scales must be uint8 of one shape and device")
+            if not t.is_contiguous() or p % align:
+                raise ValueError(f"{name}: codes and scales must be contiguous, codes 16-byte and scales 4-byte aligned")
+            ptrs.append(p)
+        pointers.append(ptrs)
+    return (len(q.codes), shape[1], cols, device), pointers
+
+
+def _matrices(tensors, name: str):
+    """_batch, with the device index and the data pointers: ((batch, rows, cols, device), dtype, pointers)."""
+    rows, cols, dt = _batch(tensors, name)
+    return (len(tensors), rows, cols, tensors[0].get_device()), dt, [t.data_ptr() for t in tensors]
 
 
 def mx4_quantize(X, transpose=False, out=None, stream=None):
     """The microscaled 4-bit code of the matrices ``X`` (float32, bfloat16 or float16) along their rows, or with
     ``transpose=True`` that of their transposes (along the columns), or with ``transpose="both"`` the pair of both from
-    one read.  ``out``: an MX4 (or a pair) of the right shape to write into, e.g. under graph capture."""
+    one read.  ``out``: an MX4 (or a pair) of the right shape to write into."""
     lib = load_library()
-    rows, cols, dt = _batch(X, "X")
+    (batch, rows, cols, device), dt, px = _matrices(X, "X")
     if transpose not in (False, True, "both"):
         raise ValueError('transpose must be False, True or "both"')
-    dev = X[0].device
     want = ((rows, cols),) if transpose is False else ((cols, rows),) if transpose is True else ((rows, cols), (cols, rows))
-    if out is None:
-        made = [MX4.empty(len(X), r, c, dev, stream) for r, c in want]
-    else:
-        made = list(out) if transpose == "both" else [out]
-        if len(made) != len(want) or any(_mx4_check(q, "out") != (len(X), r, c, dev) for q, (r, c) in zip(made, want)):
-            raise ValueError("out must have the shape, batch and device of the result")
-    along = made[0] if transpose is not True else None
-    across = made[-1] if transpose is not False else None
-    with _on(dev):
-        ptrs = [pointer_array(t, stream).data_ptr() if t is not None else None for t in
-                (X, along and along.codes, along and along.scales, across and across.codes, across and across.scales)]
-        _check(lib.muon_mx4_quantize(len(X), rows, cols, ptrs[0], dt, *ptrs[1:], _stream(stream)))
+    made = [MX4.empty(batch, r, c, X[0].device, stream) for r, c in want] if out is None else \
+        list(out) if transpose == "both" else [out]
+    checked = [_mx4_check(q, "out") for q in made]
+    if [c[0] for c in checked] != [(batch, r, c, device) for r, c in want]:
+        raise ValueError("out must have the shape, batch and device of the result")
+    none = [None, None]
+    along = [_host_pointers(p) for p in checked[0][1]] if transpose is not True else none
+    across = [_host_pointers(p) for p in checked[-1][1]] if transpose is not False else none
+    with _on(device):
+        _check(lib.muon_mx4_quantize(batch, rows, cols, _host_pointers(px), dt, *along, *across,
+                                     _raw_stream(stream, device)))
     if out is not None:
         return out
     return tuple(made) if transpose == "both" else made[0]
 
 
-def _outputs(batch, rows, cols, dtype, dev, stream):
-    if stream is None:
-        return list(torch.empty(batch, rows, cols, dtype=dtype, device=dev).unbind(0))
-    with torch.cuda.stream(_stream_obj(stream, dev)):
-        return list(torch.empty(batch, rows, cols, dtype=dtype, device=dev).unbind(0))
-
-
 def mx4_dequantize(q: MX4, dtype=torch.float32, out=None, stream=None):
     """The values of a code as float32 or bfloat16 matrices."""
     lib = load_library()
-    batch, rows, cols, dev = _mx4_check(q, "q")
+    shape, (pc, ps) = _mx4_check(q, "q")
+    batch, rows, cols, device = shape
     if dtype not in _DT:
         raise ValueError("dtype must be float32 or bfloat16")
-    Y = _outputs(batch, rows, cols, dtype, dev, stream) if out is None else out
-    if out is not None and (_batch(out, "out") != (rows, cols, _DT[dtype]) or len(out) != batch or out[0].device != dev):
+    Y = list(_allocate((batch, rows, cols), dtype, q.codes[0].device, stream).unbind(0)) if out is None else out
+    got, dt, py = _matrices(Y, "out")
+    if got != shape or dt != _DT[dtype]:
         raise ValueError("out must have the shape, batch, dtype and device of the result")
-    with _on(dev):
-        _check(lib.muon_mx4_dequantize(batch, rows, cols, pointer_array(q.codes, stream).data_ptr(),
-                                       pointer_array(q.scales, stream).data_ptr(), pointer_array(Y, stream).data_ptr(),
-                                       _DT[dtype], _stream(stream)))
+    with _on(device):
+        _check(lib.muon_mx4_dequantize(batch, rows, cols, _host_pointers(pc), _host_pointers(ps), _host_pointers(py), dt,
+                                       _raw_stream(stream, device)))
     return Y
 
 
@@ -843,31 +856,30 @@ def mx4_matmul(A: MX4, B: MX4, dtype=torch.bfloat16, out=None, accumulate: bool 
     """C = A B^T of every pair of coded matrices (A: m x k, B: n x k), as float32 or bfloat16 m x n matrices; with
     ``accumulate`` C += A B^T into ``out``."""
     lib = load_library()
-    batch, m, k, dev = _mx4_check(A, "A")
-    b2, n, k2, dev2 = _mx4_check(B, "B")
-    if b2 != batch or k2 != k or dev2 != dev:
+    (batch, m, k, device), pa = _mx4_check(A, "A")
+    (b2, n, k2, device2), pb = _mx4_check(B, "B")
+    if b2 != batch or k2 != k or device2 != device:
         raise ValueError("A and B must share the batch, the row length and the device")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if out is not None:
-        rows, cols, cdt = _batch(out, "out")
-        if (rows, cols) != (m, n) or len(out) != batch or out[0].device != dev:
-            raise ValueError("out must have one m x n matrix per pair, on the same device")
-        C = out
-    else:
+    if out is None:
         if dtype not in _DT:
             raise ValueError("dtype must be float32 or bfloat16")
-        C, cdt = _outputs(batch, m, n, dtype, dev, stream), _DT[dtype]
-    need = int(lib.muon_mx4_workspace_size(batch, m, n, k))
+        C = list(_allocate((batch, m, n), dtype, A.codes[0].device, stream).unbind(0))
+    else:
+        C = out
+    got, cdt, pc = _matrices(C, "out")
+    if got != (batch, m, n, device):
+        raise ValueError("out must have one m x n matrix per pair, on the same device")
+    need = lib.muon_mx4_workspace_size(batch, m, n, k)
     if need == 0:
         raise MuonError(1, "invalid arguments for the workspace size")
-    with _on(dev):
+    with _on(device):
         if workspace is None:
             # from the allocator at every call: its memory is reused in the stream's order, and under capture it
             # belongs to the graph, so two graphs never share it
-            with torch.cuda.stream(_stream_obj(stream, dev)):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ptrs = [pointer_array(t, stream).data_ptr() for t in (A.codes, A.scales, B.codes, B.scales, C)]
-        _check(lib.muon_mx4_matmul(batch, m, n, k, *ptrs, cdt, 1 if accumulate else 0, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+            workspace = _allocate((need,), torch.uint8, A.codes[0].device, stream)
+        _check(lib.muon_mx4_matmul(batch, m, n, k, *map(_host_pointers, (*pa, *pb, pc)), cdt, 1 if accumulate else 0,
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _raw_stream(stream, device)))
     return C

@@ -8,10 +8,10 @@
 // (AdamW update [MuonBlog §1], weight decay decoupled as in the Muon update.)
 // All arithmetic is fp32; a bf16 W is rounded once, to nearest even.
 //
-// One launch covers up to kMaxTensors tensors: each is cut into chunks of
-// kChunk elements, one block per chunk, and a block finds its tensor in the
-// chunk starts that travel with the kernel arguments (no table in memory, so
-// nothing has to be copied to the device and a captured graph holds it).
+// One launch covers up to Args::kMax tensors: each is cut into chunks, one
+// block per chunk, and a block finds its tensor in the chunk starts that travel
+// with the kernel arguments, as the pointers do (no table in memory, so nothing
+// has to be copied to the device first and a captured graph holds everything).
 #include <math.h>
 #include <string.h>
 
@@ -22,19 +22,11 @@
 namespace muon {
 namespace {
 
-constexpr int kMaxTensors = 256;
 constexpr int kThreads = 256;
 constexpr int kQuads = 4;                              // 4-element pieces per thread, 32-bit states
 constexpr int kChunk32 = kThreads * 4 * kQuads;        // elements per block, 32-bit states
 constexpr int kGroup = 128;                            // elements per scale, 8-bit states
 constexpr int kChunk8 = kThreads * 8;                  // elements per block, 8-bit states (16 groups)
-
-struct TensorTable {
-  int count;                         // tensors in this launch
-  int first;                         // list index of the launch's first tensor
-  uint32_t start[kMaxTensors + 1];   // first block of each tensor
-  int64_t size[kMaxTensors];
-};
 
 struct AdamwScalars {
   float lr, wd, eps, b1, ob1, b2, ob2;
@@ -46,29 +38,32 @@ struct AdamwScalars {
   uint32_t seed;
 };
 
-struct Adamw32Args {
-  void* const* W;
-  const void* const* G;
-  void* const* M;
-  void* const* V;
-  AdamwScalars s;
-  TensorTable t;
+// The tensors of one launch: P pointers each.  As many as keep the arguments
+// within the 4 KB that a launch takes.
+template <int P>
+struct Lists {
+  static constexpr int kPtrs = P;
+  static constexpr int kMax = 3840 / (8 * P + 12);
+  int count;                  // tensors in this launch
+  int first;                  // list index of the first one
+  uint32_t start[kMax + 1];   // first block of each tensor
+  int64_t size[kMax];
+  void* ptr[P][kMax];
 };
 
-struct Adamw8Args {
-  void* const* W;
-  const void* const* G;
-  void* const* mc;
-  void* const* ms;
-  void* const* rc;
-  void* const* rs;
+template <int P>
+struct AdamwArgs {
   AdamwScalars s;
-  TensorTable t;
+  Lists<P> t;
 };
+using Adamw32Args = AdamwArgs<4>;  // W, G, M, V
+using Adamw8Args = AdamwArgs<6>;   // W, G, codes and scales of m, codes and scales of the root of v
+static_assert(sizeof(Adamw32Args) <= 4096 && sizeof(Adamw8Args) <= 4096, "kernel arguments");
 
 // The tensor of this block (the last one whose start is not beyond it; empty
 // tensors have the next one's start and are passed over).
-__device__ __forceinline__ int find_tensor(const TensorTable& t, uint32_t block) {
+template <int P>
+__device__ __forceinline__ int find_tensor(const Lists<P>& t, uint32_t block) {
   int lo = 0, hi = t.count;  // start[lo] <= block < start[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -137,8 +132,11 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) 
   }
 }
 
-// One element's moments and weight.
+// One element's moments and weight.  The moments' products and sums are
+// rounded one at a time: their codes (8-bit states) then do not depend on what a
+// compiler fuses.
 __device__ __forceinline__ void update(float& w, float g, float& m, float& v, const AdamwScalars& s, const Scalars& r) {
+#pragma clang fp contract(off)
   g *= r.gs;
   m = s.b1 * m + s.ob1 * g;
   v = s.b2 * v + (s.ob2 * g) * g;
@@ -149,10 +147,10 @@ template <int DW, int DG>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Adamw32Args a) {
   const int t = find_tensor(a.t, blockIdx.x);
   const int64_t n = a.t.size[t];
-  void* W = a.W[a.t.first + t];
-  const void* G = a.G[a.t.first + t];
-  float* M = static_cast<float*>(a.M[a.t.first + t]);
-  float* V = static_cast<float*>(a.V[a.t.first + t]);
+  void* W = a.t.ptr[0][t];
+  const void* G = a.t.ptr[1][t];
+  float* M = static_cast<float*>(a.t.ptr[2][t]);
+  float* V = static_cast<float*>(a.t.ptr[3][t]);
   const Scalars r = load_scalars(a.s);
   const int64_t base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk32;
   const bool aligned = ((reinterpret_cast<uintptr_t>(W) & (DW == kF32 ? 15 : 7)) |
@@ -216,7 +214,7 @@ __device__ __forceinline__ float code_inverse(float s) { return s > 0.0f && s < 
 // The scale of a group from the bits of its largest magnitude (NaN counts as
 // largest).  A scale under 2^-126 is taken as 0.
 __device__ __forceinline__ float code_scale(uint32_t top_bits) {
-  const float s = __uint_as_float(top_bits) / 448.0f;
+  const float s = __uint_as_float(top_bits) * (1.0f / 448.0f);
   return s < 0x1p-126f ? 0.0f : s;
 }
 
@@ -253,12 +251,12 @@ template <int DW, int DG>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(Adamw8Args a) {
   const int t = find_tensor(a.t, blockIdx.x);
   const int64_t n = a.t.size[t];
-  void* W = a.W[a.t.first + t];
-  const void* G = a.G[a.t.first + t];
-  uint8_t* mc = static_cast<uint8_t*>(a.mc[a.t.first + t]);
-  uint8_t* rc = static_cast<uint8_t*>(a.rc[a.t.first + t]);
-  float* ms = static_cast<float*>(a.ms[a.t.first + t]);
-  float* rs = static_cast<float*>(a.rs[a.t.first + t]);
+  void* W = a.t.ptr[0][t];
+  const void* G = a.t.ptr[1][t];
+  uint8_t* mc = static_cast<uint8_t*>(a.t.ptr[2][t]);
+  float* ms = static_cast<float*>(a.t.ptr[3][t]);
+  uint8_t* rc = static_cast<uint8_t*>(a.t.ptr[4][t]);
+  float* rs = static_cast<float*>(a.t.ptr[5][t]);
   const Scalars r = load_scalars(a.s);
   const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
   const int64_t i = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8 + 8 * static_cast<int>(threadIdx.x);
@@ -384,8 +382,8 @@ muon_status make_scalars(const muon_adamw_config* cfg, AdamwScalars* s) {
 }
 
 // Sizes in range, pointer arrays present and distinct, types known.
-muon_status check_lists(int tensors, const int64_t* sizes, const void* const* arrays, int narrays, muon_dtype w_dtype,
-                        muon_dtype g_dtype, int chunk) {
+muon_status check_lists(int tensors, const int64_t* sizes, const void* const* const* arrays, int narrays,
+                        muon_dtype w_dtype, muon_dtype g_dtype, int chunk) {
   if (tensors < 1 || sizes == nullptr) return MUON_ERR_INVALID_ARG;
   for (int i = 0; i < narrays; ++i) {
     if (arrays[i] == nullptr) return MUON_ERR_INVALID_ARG;
@@ -398,23 +396,30 @@ muon_status check_lists(int tensors, const int64_t* sizes, const void* const* ar
   for (muon_dtype d : types)
     if (d != MUON_F32 && d != MUON_BF16 && d != MUON_F16) return MUON_ERR_INVALID_ARG;
   if (w_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
+  for (int i = 0; i < tensors; ++i)
+    for (int j = 0; j < narrays; ++j)
+      if (sizes[i] > 0 && arrays[j][i] == nullptr) return MUON_ERR_INVALID_ARG;
   return MUON_OK;
 }
 
-// The next launch's table from tensor `at` on: as many tensors as fit and as
-// keep the blocks under the grid's limit.  Returns the blocks.
-uint32_t fill_table(TensorTable* t, int tensors, const int64_t* sizes, int at, int chunk) {
+// The next launch's tensors from `at` on: as many as fit and as keep the
+// blocks under the grid's limit.  Returns the blocks.
+template <int P>
+uint32_t fill_lists(Lists<P>* t, int tensors, const int64_t* sizes, const void* const* const* arrays, int at,
+                    int chunk) {
   t->first = at;
   t->count = 0;
   uint32_t blocks = 0;
   t->start[0] = 0;
-  while (t->count < kMaxTensors && at + t->count < tensors) {
-    const int64_t n = sizes[at + t->count];
+  while (t->count < Lists<P>::kMax && at + t->count < tensors) {
+    const int c = t->count;
+    const int64_t n = sizes[at + c];
     const uint32_t b = static_cast<uint32_t>((n + chunk - 1) / chunk);
-    if (t->count > 0 && blocks + b > (1u << 23)) break;
+    if (c > 0 && blocks + b > (1u << 23)) break;
     blocks += b;
-    t->size[t->count++] = n;
-    t->start[t->count] = blocks;
+    t->size[c] = n;
+    for (int j = 0; j < P; ++j) t->ptr[j][c] = const_cast<void*>(arrays[j][at + c]);
+    t->start[++t->count] = blocks;
   }
   return blocks;
 }
@@ -435,10 +440,11 @@ uint32_t fill_table(TensorTable* t, int tensors, const int64_t* sizes, int at, i
   } while (0)
 
 template <class Args, class Launch>
-muon_status run_lists(Args& a, int tensors, const int64_t* sizes, int chunk, double state_bytes, muon_dtype w_dtype,
-                      muon_dtype g_dtype, const char* kernel, const char* role, hipStream_t s, Launch&& launch) {
+muon_status run_lists(Args& a, int tensors, const int64_t* sizes, const void* const* const* arrays, int chunk,
+                      double state_bytes, muon_dtype w_dtype, muon_dtype g_dtype, const char* kernel, const char* role,
+                      hipStream_t s, Launch&& launch) {
   for (int at = 0; at < tensors;) {
-    const uint32_t blocks = fill_table(&a.t, tensors, sizes, at, chunk);
+    const uint32_t blocks = fill_lists(&a.t, tensors, sizes, arrays, at, chunk);
     at += a.t.count;
     if (blocks == 0) continue;  // empty tensors only
     double elems = 0.0;
@@ -473,18 +479,14 @@ void muon_adamw_config_init(muon_adamw_config* cfg) {
 muon_status muon_adamw_step(int tensors, const int64_t* sizes, void* const* W, muon_dtype w_dtype, void* const* M,
                             void* const* V, const void* const* G, muon_dtype g_dtype, const muon_adamw_config* cfg,
                             void* stream) {
-  const void* arrays[4] = {W, M, V, G};
+  const void* const* arrays[4] = {W, G, M, V};
   muon_status st = check_lists(tensors, sizes, arrays, 4, w_dtype, g_dtype, kChunk32);
   if (st != MUON_OK) return st;
   Adamw32Args a;
   st = make_scalars(cfg, &a.s);
   if (st != MUON_OK) return st;
-  a.W = W;
-  a.G = G;
-  a.M = M;
-  a.V = V;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return run_lists(a, tensors, sizes, kChunk32, 16.0, w_dtype, g_dtype, "adamw_kernel", "adamw", s,
+  return run_lists(a, tensors, sizes, arrays, kChunk32, 16.0, w_dtype, g_dtype, "adamw_kernel", "adamw", s,
                    [&](uint32_t blocks) { ADAMW_DISPATCH(adamw_kernel, a, blocks, w_dtype, g_dtype, s); });
 }
 
@@ -492,20 +494,15 @@ muon_status muon_adamw8_step(int tensors, const int64_t* sizes, void* const* W, 
                              const muon_adamw8_state* state, const void* const* G, muon_dtype g_dtype,
                              const muon_adamw_config* cfg, void* stream) {
   if (state == nullptr) return MUON_ERR_INVALID_ARG;
-  const void* arrays[6] = {W, state->m_codes, state->m_scales, state->r_codes, state->r_scales, G};
+  const void* const* arrays[6] = {W, G, state->m_codes, state->m_scales, state->r_codes, state->r_scales};
   muon_status st = check_lists(tensors, sizes, arrays, 6, w_dtype, g_dtype, kChunk8);
   if (st != MUON_OK) return st;
   Adamw8Args a;
   st = make_scalars(cfg, &a.s);
   if (st != MUON_OK) return st;
-  a.W = W;
-  a.G = G;
-  a.mc = state->m_codes;
-  a.ms = state->m_scales;
-  a.rc = state->r_codes;
-  a.rs = state->r_scales;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return run_lists(a, tensors, sizes, kChunk8, 4.0 + 16.0 / kGroup, w_dtype, g_dtype, "adamw8_kernel", "adamw8", s,
+  return run_lists(a, tensors, sizes, arrays, kChunk8, 4.0 + 16.0 / kGroup, w_dtype, g_dtype, "adamw8_kernel",
+                   "adamw8", s,
                    [&](uint32_t blocks) { ADAMW_DISPATCH(adamw8_kernel, a, blocks, w_dtype, g_dtype, s); });
 }
 

@@ -20,35 +20,38 @@ constexpr int kMxUnit = 128;
 
 inline int64_t mx4_units(int64_t k) { return (k + kMxUnit - 1) / kMxUnit; }
 
+// Matrices of one launch; their pointers travel with the kernel arguments.
+constexpr int kMxBatch = 16;
+
 struct Mx4QuantArgs {
-  const void* const* X;
   int x_dtype;
   int rows, cols;
-  void* const* codes;    // of X, or null
-  void* const* scales;
-  void* const* codes_t;  // of X^T, or null
-  void* const* scales_t;
+  const void* X[kMxBatch];
+  void* codes[kMxBatch];    // of X, or null
+  void* scales[kMxBatch];
+  void* codes_t[kMxBatch];  // of X^T, or null
+  void* scales_t[kMxBatch];
 };
 hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, int batch, hipStream_t s);
 
 struct Mx4DequantArgs {
-  const void* const* codes;
-  const void* const* scales;
   int rows, cols;
-  void* const* Y;
   int y_dtype;
+  const void* codes[kMxBatch];
+  const void* scales[kMxBatch];
+  void* Y[kMxBatch];
 };
 hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int batch, hipStream_t s);
 
 struct Mx4GemmArgs {
   int m, n, k, units;
-  const void* const* A;   // codes of m x k
-  const void* const* As;  // scales
-  const void* const* B;   // codes of n x k
-  const void* const* Bs;
-  void* const* C;         // m x n, row-major
   int c_dtype;
-  int accumulate;         // C += A B^T
+  int accumulate;               // C += A B^T
+  const void* A[kMxBatch];      // codes of m x k
+  const void* As[kMxBatch];     // scales
+  const void* B[kMxBatch];      // codes of n x k
+  const void* Bs[kMxBatch];
+  void* C[kMxBatch];            // m x n, row-major
 };
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, int batch, hipStream_t s);
 

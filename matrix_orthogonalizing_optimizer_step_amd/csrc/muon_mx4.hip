@@ -131,11 +131,11 @@ uint32_t grid_for(int64_t threads) {
 
 template <int D>
 void quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) {
-  if (a.codes != nullptr) {
+  if (a.codes[0] != nullptr) {
     const int64_t units = mx4_units(a.cols);
     hipLaunchKernelGGL(mx4_rows_kernel<D>, dim3(grid_for(units * a.rows * 16), 1, batch), dim3(kThreads), 0, s, a, units);
   }
-  if (a.codes_t != nullptr) {
+  if (a.codes_t[0] != nullptr) {
     const int64_t units = mx4_units(a.rows);
     hipLaunchKernelGGL(mx4_columns_kernel<D>, dim3(grid_for(units * 4 * a.cols), 1, batch), dim3(kThreads), 0, s, a,
                        units);
@@ -170,10 +170,21 @@ using namespace muon;
 
 namespace {
 
-constexpr int kMaxBatch = 65535;  // the batch is grid z
-
 bool mx4_shape_ok(int batch, int rows, int cols) {
-  return batch >= 1 && batch <= kMaxBatch && rows >= 1 && cols >= 1 && rows <= MUON_MAX_DIM && cols <= MUON_MAX_DIM;
+  return batch >= 1 && rows >= 1 && cols >= 1 && rows <= MUON_MAX_DIM && cols <= MUON_MAX_DIM;
+}
+
+// A host array of `batch` non-null device pointers.
+bool pointers_ok(int batch, const void* const* p) {
+  if (p == nullptr) return false;
+  for (int i = 0; i < batch; ++i)
+    if (p[i] == nullptr) return false;
+  return true;
+}
+
+template <class T>
+void take(T* to, T const* from, int at, int count) {
+  for (int i = 0; i < count; ++i) to[i] = from != nullptr ? from[at + i] : nullptr;
 }
 
 bool mx4_type_ok(muon_dtype d) { return d == MUON_F32 || d == MUON_BF16 || d == MUON_F16; }
@@ -190,39 +201,63 @@ extern "C" {
 muon_status muon_mx4_quantize(int batch, int rows, int cols, const void* const* X, muon_dtype x_dtype,
                               void* const* codes, void* const* scales, void* const* codes_t, void* const* scales_t,
                               void* stream) {
-  if (!mx4_shape_ok(batch, rows, cols) || X == nullptr || !mx4_type_ok(x_dtype)) return MUON_ERR_INVALID_ARG;
+  if (!mx4_shape_ok(batch, rows, cols) || !mx4_type_ok(x_dtype)) return MUON_ERR_INVALID_ARG;
   if ((codes == nullptr) != (scales == nullptr) || (codes_t == nullptr) != (scales_t == nullptr))
     return MUON_ERR_INVALID_ARG;
   if (codes == nullptr && codes_t == nullptr) return MUON_ERR_INVALID_ARG;
-  const void* arrays[5] = {X, codes, scales, codes_t, scales_t};
-  for (int i = 0; i < 5; ++i)
+  const void* const* arrays[5] = {X, codes, scales, codes_t, scales_t};
+  for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < i; ++j)
       if (arrays[i] != nullptr && arrays[i] == arrays[j]) return MUON_ERR_INVALID_ARG;
-  Mx4QuantArgs a{X, static_cast<int>(x_dtype), rows, cols, codes, scales, codes_t, scales_t};
-  const double r = rows, c = cols;
-  const double bytes = batch * (r * c * (x_dtype == MUON_F32 ? 4.0 : 2.0) + (codes != nullptr ? code_bytes(r, c) : 0.0) +
-                                (codes_t != nullptr ? code_bytes(c, r) : 0.0));
+    if ((i == 0 || arrays[i] != nullptr) && !pointers_ok(batch, arrays[i])) return MUON_ERR_INVALID_ARG;
+  }
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t err = traced_launch(s, "mx4_quantize", "mx4_quantize", 0.0, bytes,
-                                       [&] { return launch_mx4_quantize(a, batch, s); });
-  return err == hipSuccess ? MUON_OK : MUON_ERR_HIP;
+  const double r = rows, c = cols;
+  const double bytes = r * c * (x_dtype == MUON_F32 ? 4.0 : 2.0) + (codes != nullptr ? code_bytes(r, c) : 0.0) +
+                       (codes_t != nullptr ? code_bytes(c, r) : 0.0);
+  for (int at = 0; at < batch; at += kMxBatch) {
+    const int count = batch - at < kMxBatch ? batch - at : kMxBatch;
+    Mx4QuantArgs a;
+    a.x_dtype = x_dtype;
+    a.rows = rows;
+    a.cols = cols;
+    take(a.X, X, at, count);
+    take(a.codes, codes, at, count);
+    take(a.scales, scales, at, count);
+    take(a.codes_t, codes_t, at, count);
+    take(a.scales_t, scales_t, at, count);
+    if (traced_launch(s, "mx4_quantize", "mx4_quantize", 0.0, bytes * count,
+                      [&] { return launch_mx4_quantize(a, count, s); }) != hipSuccess)
+      return MUON_ERR_HIP;
+  }
+  return MUON_OK;
 }
 
 muon_status muon_mx4_dequantize(int batch, int rows, int cols, const void* const* codes, const void* const* scales,
                                 void* const* Y, muon_dtype y_dtype, void* stream) {
-  if (!mx4_shape_ok(batch, rows, cols) || codes == nullptr || scales == nullptr || Y == nullptr)
+  if (!mx4_shape_ok(batch, rows, cols) || !pointers_ok(batch, codes) || !pointers_ok(batch, scales) ||
+      !pointers_ok(batch, Y))
     return MUON_ERR_INVALID_ARG;
   if (!mx4_type_ok(y_dtype) || codes == scales || static_cast<const void*>(codes) == Y ||
       static_cast<const void*>(scales) == Y)
     return MUON_ERR_INVALID_ARG;
   if (y_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;  // the code's range is that of binary32
-  Mx4DequantArgs a{codes, scales, rows, cols, Y, static_cast<int>(y_dtype)};
-  const double bytes = batch * (static_cast<double>(rows) * cols * (y_dtype == MUON_F32 ? 4.0 : 2.0) +
-                                code_bytes(rows, cols));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t err = traced_launch(s, "mx4_values_kernel", "mx4_dequantize", 0.0, bytes,
-                                       [&] { return launch_mx4_dequantize(a, batch, s); });
-  return err == hipSuccess ? MUON_OK : MUON_ERR_HIP;
+  const double bytes = static_cast<double>(rows) * cols * (y_dtype == MUON_F32 ? 4.0 : 2.0) + code_bytes(rows, cols);
+  for (int at = 0; at < batch; at += kMxBatch) {
+    const int count = batch - at < kMxBatch ? batch - at : kMxBatch;
+    Mx4DequantArgs a;
+    a.rows = rows;
+    a.cols = cols;
+    a.y_dtype = y_dtype;
+    take(a.codes, codes, at, count);
+    take(a.scales, scales, at, count);
+    take(a.Y, Y, at, count);
+    if (traced_launch(s, "mx4_values_kernel", "mx4_dequantize", 0.0, bytes * count,
+                      [&] { return launch_mx4_dequantize(a, count, s); }) != hipSuccess)
+      return MUON_ERR_HIP;
+  }
+  return MUON_OK;
 }
 
 size_t muon_mx4_workspace_size(int batch, int m, int n, int k) {
@@ -235,25 +270,37 @@ muon_status muon_mx4_matmul(int batch, int m, int n, int k, const void* const* A
                             muon_dtype c_dtype, int accumulate, void* workspace, size_t ws_bytes, void* stream) {
   const size_t need = muon_mx4_workspace_size(batch, m, n, k);
   if (need == 0) return MUON_ERR_INVALID_ARG;
-  if (A_codes == nullptr || A_scales == nullptr || B_codes == nullptr || B_scales == nullptr || C == nullptr)
-    return MUON_ERR_INVALID_ARG;
-  // A and B may be one matrix (A A^T); C is written
-  const void* in[4] = {A_codes, A_scales, B_codes, B_scales};
-  for (const void* p : in)
-    if (p == static_cast<const void*>(C)) return MUON_ERR_INVALID_ARG;
+  const void* const* in[4] = {A_codes, A_scales, B_codes, B_scales};
+  if (!pointers_ok(batch, C)) return MUON_ERR_INVALID_ARG;
+  for (const void* const* p : in)  // A and B may be one matrix (A A^T); C is written
+    if (!pointers_ok(batch, p) || static_cast<const void*>(p) == C) return MUON_ERR_INVALID_ARG;
   if (!mx4_type_ok(c_dtype) || (accumulate != 0 && accumulate != 1)) return MUON_ERR_INVALID_ARG;
   if (c_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
   if (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return MUON_ERR_WORKSPACE;
-  Mx4GemmArgs a{m, n, k, static_cast<int>(mx4_units(k)), A_codes, A_scales, B_codes, B_scales, C,
-                static_cast<int>(c_dtype), accumulate};
-  const double mn = static_cast<double>(m) * n;
-  const double bytes = batch * (code_bytes(m, k) + code_bytes(n, k) +
-                                mn * (c_dtype == MUON_F32 ? 4.0 : 2.0) * (accumulate ? 2.0 : 1.0));
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t err = traced_launch(s, "mx4_gemm_kernel", "mx4_matmul", 2.0 * batch * mn * k, bytes,
-                                       [&] { return launch_mx4_gemm(a, batch, s); });
-  return err == hipSuccess ? MUON_OK : MUON_ERR_HIP;
+  const double mn = static_cast<double>(m) * n;
+  const double bytes = code_bytes(m, k) + code_bytes(n, k) +
+                       mn * (c_dtype == MUON_F32 ? 4.0 : 2.0) * (accumulate ? 2.0 : 1.0);
+  for (int at = 0; at < batch; at += kMxBatch) {
+    const int count = batch - at < kMxBatch ? batch - at : kMxBatch;
+    Mx4GemmArgs a;
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.units = static_cast<int>(mx4_units(k));
+    a.c_dtype = c_dtype;
+    a.accumulate = accumulate;
+    take(a.A, A_codes, at, count);
+    take(a.As, A_scales, at, count);
+    take(a.B, B_codes, at, count);
+    take(a.Bs, B_scales, at, count);
+    take(a.C, C, at, count);
+    if (traced_launch(s, "mx4_gemm_kernel", "mx4_matmul", 2.0 * count * mn * k, bytes * count,
+                      [&] { return launch_mx4_gemm(a, count, s); }) != hipSuccess)
+      return MUON_ERR_HIP;
+  }
+  return MUON_OK;
 }
 
 }  // extern "C"

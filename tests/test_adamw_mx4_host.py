@@ -84,7 +84,20 @@ def test_mx4_oracle_error_bound():
 
 
 # --- refusals ------------------------------------------------------------------------------------------------------
-def _adamw(lib, tensors=1, sizes=(4,), W=16, wdt=0, M=32, V=48, G=64, gdt=0, null_cfg=False, **cfg):
+_keep = []
+
+
+def ptrs(*values):
+    """The address of a new host array of (bogus, never used) device pointers."""
+    a = (ctypes.c_void_p * len(values))(*values)
+    _keep.append(a)
+    return ctypes.addressof(a)
+
+
+P = [ptrs(*[4096 * (i + 1)] * 3) for i in range(8)]
+
+
+def _adamw(lib, tensors=1, sizes=(4,), W=P[0], wdt=0, M=P[1], V=P[2], G=P[3], gdt=0, null_cfg=False, **cfg):
     c = bd._AdamWConfig()
     lib.muon_adamw_config_init(ctypes.byref(c))
     for k, v in cfg.items():
@@ -92,7 +105,7 @@ def _adamw(lib, tensors=1, sizes=(4,), W=16, wdt=0, M=32, V=48, G=64, gdt=0, nul
     arr = (ctypes.c_int64 * len(sizes))(*sizes) if sizes is not None else None
     p = None if null_cfg else ctypes.byref(c)
     a = lib.muon_adamw_step(tensors, arr, W, wdt, M, V, G, gdt, p, None)
-    st = bd._AdamW8State(M, V, 80, 96)
+    st = bd._AdamW8State(M, V, P[4], P[5])
     b = lib.muon_adamw8_step(tensors, arr, W, wdt, ctypes.byref(st), G, gdt, p, None)
     return a, b
 
@@ -102,7 +115,8 @@ def test_adamw_refusals_before_any_device_work():
     nan, inf = float("nan"), float("inf")
     for kw, code in [(dict(tensors=0), 1), (dict(tensors=-1), 1), (dict(sizes=None), 1), (dict(sizes=(-1,)), 1),
                      (dict(sizes=(1 << 50,)), 1), (dict(W=None), 1), (dict(M=None), 1), (dict(V=None), 1),
-                     (dict(G=None), 1), (dict(M=16), 1), (dict(G=16), 1), (dict(V=32), 1), (dict(null_cfg=True), 1),
+                     (dict(G=None), 1), (dict(M=P[0]), 1), (dict(G=P[0]), 1), (dict(V=P[1]), 1), (dict(null_cfg=True), 1),
+                     (dict(W=ptrs(None)), 1), (dict(tensors=2, sizes=(0, 4), G=ptrs(None, None)), 1),
                      (dict(wdt=7), 1), (dict(gdt=9), 1), (dict(wdt=2), 2), (dict(lr=nan), 1), (dict(lr=inf), 1),
                      (dict(lr=1e39), 1), (dict(weight_decay=nan), 1), (dict(eps=0.0), 1), (dict(eps=-1e-8), 1),
                      (dict(eps=1e-60), 1), (dict(beta1=1.0), 1), (dict(beta1=-0.1), 1), (dict(beta2=1.0), 1),
@@ -112,16 +126,17 @@ def test_adamw_refusals_before_any_device_work():
     c = bd._AdamWConfig()
     lib.muon_adamw_config_init(ctypes.byref(c))
     assert (c.lr, c.beta1, c.beta2, c.eps, c.weight_decay, c.step) == (1e-3, 0.9, 0.999, 1e-8, 0.0, 1)
-    assert lib.muon_adamw8_step(1, full, 16, 0, None, 64, 0, ctypes.byref(c), None) == 1
+    assert lib.muon_adamw8_step(1, full, P[0], 0, None, P[3], 0, ctypes.byref(c), None) == 1
     for missing in range(4):
-        st = bd._AdamW8State(*[None if i == missing else 80 + 16 * i for i in range(4)])
-        assert lib.muon_adamw8_step(1, full, 16, 0, ctypes.byref(st), 64, 0, ctypes.byref(c), None) == 1
+        st = bd._AdamW8State(*[None if i == missing else P[4 + i] for i in range(4)])
+        assert lib.muon_adamw8_step(1, full, P[0], 0, ctypes.byref(st), P[3], 0, ctypes.byref(c), None) == 1
     lib.muon_adamw_config_init(None)  # no-op
 
 
 def test_empty_tensors_need_no_device():
     """A list of empty tensors has nothing to launch."""
-    assert _adamw(mu.load_library(), tensors=3, sizes=(0, 0, 0)) == (0, 0)
+    none = [ptrs(None, None, None) for _ in range(4)]
+    assert _adamw(mu.load_library(), tensors=3, sizes=(0, 0, 0), W=none[0], M=none[1], V=none[2], G=none[3]) == (0, 0)
 
 
 def test_adamw_binding_refusals():
@@ -146,26 +161,28 @@ def test_adamw_binding_refusals():
 
 def test_mx4_refusals_before_any_device_work():
     lib = mu.load_library()
-    q = lambda b=1, r=4, c=4, X=16, dt=0, codes=32, scales=48, ct=64, st=80: (  # noqa: E731
+    q = lambda b=1, r=4, c=4, X=P[0], dt=0, codes=P[1], scales=P[2], ct=P[3], st=P[4]: (  # noqa: E731
         lib.muon_mx4_quantize(b, r, c, X, dt, codes, scales, ct, st, None))
-    for kw in [dict(b=0), dict(b=65536), dict(r=0), dict(c=0), dict(r=(1 << 20) + 1), dict(c=(1 << 20) + 1), dict(X=None),
+    for kw in [dict(b=0), dict(r=0), dict(c=0), dict(r=(1 << 20) + 1), dict(c=(1 << 20) + 1), dict(X=None),
                dict(dt=5), dict(codes=None), dict(scales=None), dict(ct=None), dict(st=None),
-               dict(codes=None, scales=None, ct=None, st=None), dict(codes=16), dict(st=48)]:
+               dict(codes=None, scales=None, ct=None, st=None), dict(codes=P[0]), dict(st=P[2]),
+               dict(X=ptrs(None)), dict(b=2, ct=ptrs(64, None))]:
         assert q(**kw) == 1, kw
-    d = lambda b=1, r=4, c=4, codes=16, scales=32, Y=48, dt=0: (  # noqa: E731
+    d = lambda b=1, r=4, c=4, codes=P[0], scales=P[1], Y=P[2], dt=0: (  # noqa: E731
         lib.muon_mx4_dequantize(b, r, c, codes, scales, Y, dt, None))
     for kw, code in [(dict(b=0), 1), (dict(r=0), 1), (dict(c=-1), 1), (dict(codes=None), 1), (dict(scales=None), 1),
-                     (dict(Y=None), 1), (dict(dt=9), 1), (dict(Y=16), 1), (dict(scales=16), 1), (dict(dt=2), 2)]:
+                     (dict(Y=None), 1), (dict(dt=9), 1), (dict(Y=P[0]), 1), (dict(scales=P[0]), 1), (dict(dt=2), 2),
+                     (dict(Y=ptrs(None)), 1)]:
         assert d(**kw) == code, kw
     assert lib.muon_mx4_workspace_size(1, 4, 4, 4) > 0
-    for args in [(0, 4, 4, 4), (1, 0, 4, 4), (1, 4, 0, 4), (1, 4, 4, 0), (65536, 4, 4, 4), (1, 1 << 17, 4, 1 << 15),
+    for args in [(0, 4, 4, 4), (1, 0, 4, 4), (1, 4, 0, 4), (1, 4, 4, 0), (1, 1 << 17, 4, 1 << 15),
                  (1, 4, 1 << 20, 1 << 12)]:
         assert lib.muon_mx4_workspace_size(*args) == 0, args
     assert lib.muon_mx4_workspace_size(1, (1 << 16) - 1, 4, 1 << 16) > 0
-    g = lambda b=1, m=4, n=4, k=4, A=16, As=32, B=48, Bs=64, C=80, dt=0, acc=0, ws=256, wsb=1 << 40: (  # noqa: E731
+    g = lambda b=1, m=4, n=4, k=4, A=P[0], As=P[1], B=P[2], Bs=P[3], C=P[4], dt=0, acc=0, ws=256, wsb=1 << 40: (  # noqa: E731
         lib.muon_mx4_matmul(b, m, n, k, A, As, B, Bs, C, dt, acc, ws, wsb, None))
     for kw, code in [(dict(b=0), 1), (dict(m=0), 1), (dict(k=0), 1), (dict(A=None), 1), (dict(As=None), 1),
-                     (dict(B=None), 1), (dict(Bs=None), 1), (dict(C=None), 1), (dict(C=16), 1), (dict(C=64), 1),
+                     (dict(B=None), 1), (dict(Bs=None), 1), (dict(C=None), 1), (dict(C=P[0]), 1), (dict(C=P[3]), 1), (dict(C=ptrs(None)), 1),
                      (dict(dt=4), 1), (dict(acc=2), 1), (dict(dt=2), 2), (dict(ws=None), 3), (dict(wsb=0), 3),
                      (dict(ws=272), 3), (dict(m=1 << 17, k=1 << 15), 1)]:
         assert g(**kw) == code, kw
