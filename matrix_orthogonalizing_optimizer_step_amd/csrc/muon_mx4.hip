@@ -13,132 +13,320 @@
 namespace muon {
 namespace {
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// Rows of odd length start anywhere: loads and stores of 8 and 16 bytes that
+// need the alignment of one element only.
+typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+
+template <int D>
+__device__ __forceinline__ float half_of(uint32_t w, int upper) {
+  const uint16_t h = static_cast<uint16_t>(upper ? w >> 16 : w);
+  return D == kBF16 ? bf16_to_f32(h) : f16_to_f32(h);
+}
+
+// Scale as the converters take it: its exponent field is the scale byte.
+__device__ __forceinline__ float scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Two e2m1 codes of (lo, hi) / scale into byte S of w (nearest even, saturating).
+template <int S>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, float lo, float hi, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, lo, hi, scale, S);
+}
+
+__device__ __forceinline__ uint32_t code8(const float (&x)[8], float scale) {
+  uint32_t w = code_pair<0>(0, x[0], x[1], scale);
+  w = code_pair<1>(w, x[2], x[3], scale);
+  w = code_pair<2>(w, x[4], x[5], scale);
+  return code_pair<3>(w, x[6], x[7], scale);
+}
+
+// Largest magnitude of three, NaN if one is NaN.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(a), fabsf(b)), fabsf(c));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {  // of non-negative floats' bits (NaN is largest)
+  const uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), CTRL, 0xf, 0xf, true));
+  return x > y ? x : y;
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;  // quad permutations, reversal within 8 lanes
+
+// ---------------------------------------------------------------------------
+// Codes along rows: a thread takes 8 consecutive elements, 4 threads a block of
+// 32, 16 a unit; a wave takes 4 rows, a block 16, and kUnitsPerThread units one
+// after the other with all loads out first.
+// ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
-constexpr int kMaxBlocks = 1 << 16;
+constexpr int kRowsPerBlock = 16, kUnitsPerThread = 4;
 
-// e2m1 code of x times a power of two: y in [0, 8) after scaling.
-__device__ __forceinline__ uint32_t e2m1_code(float x, float inverse) {
-  const float y = fabsf(x) * inverse;
-  const float c = y < 2.0f ? rintf(y * 2.0f) : (y < 4.0f ? rintf(y) + 2.0f : fminf(rintf(y * 0.5f), 3.0f) + 4.0f);
-  return static_cast<uint32_t>(c) | ((__float_as_uint(x) >> 28) & 8u);
-}
-
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float mag = e == 0u ? 0.5f * static_cast<float>(m)
-                            : __uint_as_float(((126u + e) << 23) | (m << 22));
-  return (c & 8u) ? -mag : mag;
-}
-
-// 2^(127 - byte); byte is at most 252.
-__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-__device__ __forceinline__ uint32_t max_bits(uint32_t top, float x) {
-  const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
-  return b > top ? b : top;
-}
-
-// Codes along the rows of X: a thread takes 8 elements, 4 threads a block, 16
-// a unit; consecutive threads write consecutive bytes.
 template <int D>
-__global__ __launch_bounds__(kThreads) void mx4_rows_kernel(Mx4QuantArgs a, int64_t units) {
-  const void* X = a.X[blockIdx.z];
-  uint32_t* codes = static_cast<uint32_t*>(a.codes[blockIdx.z]);
-  uint8_t* scales = static_cast<uint8_t*>(a.scales[blockIdx.z]);
-  const int64_t total = units * a.rows * 16, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; id < total; id += step) {
-    const int64_t line = id >> 4;  // u rows + r
-    const int64_t u = line / a.rows, r = line - u * a.rows;
-    const int64_t c0 = u * kMxUnit + 8 * (id & 15);
-    float x[8];
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = c0 + e < a.cols ? load_as_f32(X, r * a.cols + c0 + e, D) : 0.0f;
-      top = max_bits(top, x[e]);
-    }
-    // total is a multiple of 16, so the 4 threads of a block are here together
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d));
-      top = y > top ? y : top;
-    }
-    const uint32_t byte = mx4_scale_byte(top);
-    uint32_t code = 0;
-    if (byte != 255u) {
-      const float inv = scale_inverse(byte);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) code |= e2m1_code(x[e], inv) << (4 * e);
-    }
-    codes[id] = code;
-    if ((id & 3) == 0) scales[id >> 2] = static_cast<uint8_t>(byte);
-  }
-}
+struct Raw8 {
+  u32x4_t v[D == kF32 ? 2 : 1];
+};
 
-// Codes along the columns of X (the code of X^T): a thread takes one block of
-// 32 rows of a column; consecutive threads take consecutive columns.
 template <int D>
-__global__ __launch_bounds__(kThreads) void mx4_columns_kernel(Mx4QuantArgs a, int64_t units) {
-  const void* X = a.X[blockIdx.z];
-  uint4* codes = static_cast<uint4*>(a.codes_t[blockIdx.z]);
-  uint8_t* scales = static_cast<uint8_t*>(a.scales_t[blockIdx.z]);
-  const int64_t total = units * 4 * a.cols, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; id < total; id += step) {
-    const int64_t block = id / a.cols, j = id - block * a.cols;  // block of 32 rows, column
-    const int64_t r0 = block * kMxBlock;
-    float x[kMxBlock];
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < kMxBlock; ++e) {
-      x[e] = r0 + e < a.rows ? load_as_f32(X, (r0 + e) * a.cols + j, D) : 0.0f;
-      top = max_bits(top, x[e]);
+__device__ __forceinline__ Raw8<D> load8(const void* X, int64_t at, int left) {
+  Raw8<D> r;
+  if (left >= 8) {
+    if constexpr (D == kF32) {
+      const u32x4_a4* p = reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at);
+      r.v[0] = p[0];
+      r.v[1] = p[1];
+    } else {
+      r.v[0] = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(X) + at);
     }
-    const uint32_t byte = mx4_scale_byte(top);
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (byte != 255u) {
-      const float inv = scale_inverse(byte);
+  } else {
 #pragma unroll
-      for (int e = 0; e < kMxBlock; ++e) w[e >> 3] |= e2m1_code(x[e], inv) << (4 * (e & 7));
-    }
-    const int64_t at = ((block >> 2) * a.cols + j) * 4 + (block & 3);
-    codes[at] = make_uint4(w[0], w[1], w[2], w[3]);
-    scales[at] = static_cast<uint8_t>(byte);
-  }
-}
-
-// Values of the code, row-major: a thread takes 8 elements of a row.
-template <int D>
-__global__ __launch_bounds__(kThreads) void mx4_values_kernel(Mx4DequantArgs a, int64_t octets) {
-  const uint32_t* codes = static_cast<const uint32_t*>(a.codes[blockIdx.z]);
-  const uint8_t* scales = static_cast<const uint8_t*>(a.scales[blockIdx.z]);
-  void* Y = a.Y[blockIdx.z];
-  const int64_t total = octets * a.rows, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; id < total; id += step) {
-    const int64_t r = id / octets, o = id - r * octets;
-    const int64_t line = (o >> 4) * a.rows + r;
-    const uint32_t code = codes[line * 16 + (o & 15)];
-    const float s = e8m0_to_f32(scales[line * 4 + ((o & 15) >> 2)]);
+    for (int e = 0; e < (D == kF32 ? 2 : 1); ++e) r.v[e] = (u32x4_t){0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (o * 8 + e < a.cols) store_from_f32(Y, r * a.cols + o * 8 + e, D, e2m1_value((code >> (4 * e)) & 15u) * s);
+      if (e < left) {
+        if constexpr (D == kF32) {
+          r.v[e >> 2][e & 3] = static_cast<const uint32_t*>(X)[at + e];
+        } else {
+          r.v[0][e >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(X)[at + e]) << (16 * (e & 1));
+        }
+      }
+  }
+  return r;
+}
+
+template <int D>
+__device__ __forceinline__ void expand8(const Raw8<D>& r, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (D == kF32) {
+      x[e] = __uint_as_float(r.v[e >> 2][e & 3]);
+    } else {
+      x[e] = half_of<D>(r.v[0][e >> 1], e & 1);
+    }
   }
 }
 
-uint32_t grid_for(int64_t threads) {
-  const int64_t b = (threads + kThreads - 1) / kThreads;
-  return static_cast<uint32_t>(b < kMaxBlocks ? b : kMaxBlocks);
+template <int D>
+__global__ __launch_bounds__(kThreads) void mx4_rows_kernel(Mx4QuantArgs a, int units) {
+  const int b = blockIdx.z, o = threadIdx.x & 15;
+  const int r = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x >> 4);
+  if (r >= a.rows) return;  // all 16 threads of a row together
+  const int u0 = blockIdx.y * kUnitsPerThread;
+  const void* X = a.X[b];
+  uint32_t* codes = static_cast<uint32_t*>(a.codes[b]);
+  uint8_t* scales = static_cast<uint8_t*>(a.scales[b]);
+  Raw8<D> raw[kUnitsPerThread];
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int c = (u0 + k) * kMxUnit + 8 * o;
+    raw[k] = load8<D>(X, static_cast<int64_t>(r) * a.cols + c, a.cols - c);
+  }
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    float x[8];
+    expand8<D>(raw[k], x);
+    uint32_t top = __float_as_uint(top3(top3(x[0], x[1], x[2]), x[3], top3(top3(x[4], x[5], x[6]), x[7], 0.0f)));
+    top = dpp_max<kXor1>(top);
+    top = dpp_max<kXor2>(top);
+    const uint32_t byte = mx4_scale_byte(top);
+    const uint32_t w = code8(x, scale_operand(byte));
+    if (u0 + k < units) {
+      const int64_t line = static_cast<int64_t>(u0 + k) * a.rows + r;
+      codes[line * 16 + o] = byte == 255u ? 0u : w;
+      if ((o & 3) == 0) scales[line * 4 + (o >> 2)] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Codes along columns, or along both, from one read of X: a block of 128
+// threads takes a 128 x 128 tile, a thread 32 rows x 4 columns of it in
+// registers.  A column's block is then one thread's, a row's block that of 8
+// neighbouring lanes.  Each tile's codes are one contiguous 8 KB piece of either
+// output; they are put together in LDS and written in whole lines.
+// ---------------------------------------------------------------------------
+constexpr int kTileThreads = 128;
+constexpr int kColPitch = 80;  // bytes of a column's codes in LDS: 64, and 16 against bank conflicts
+
+template <int D, bool FULL>
+__device__ __forceinline__ void load_tile(const void* X, int64_t at, int64_t pitch, int rows_left, int cols_left,
+                                          float (&x)[32][4]) {
+  if constexpr (FULL) {
+    if constexpr (D == kF32) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at + e * pitch);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[e][c] = __uint_as_float(v[c]);
+      }
+    } else {
+      u32x2_t v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        v[e] = *reinterpret_cast<const u32x2_a2*>(static_cast<const uint16_t*>(X) + at + e * pitch);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[e][c] = half_of<D>(v[e][c >> 1], c & 1);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[e][c] = e < rows_left && c < cols_left ? load_as_f32(X, at + e * pitch + c, D) : 0.0f;
+  }
+}
+
+template <int D, bool ROWS>
+__global__ __launch_bounds__(kTileThreads) void mx4_tile_kernel(Mx4QuantArgs a) {
+  __shared__ __align__(16) uint8_t col_code[128 * kColPitch];
+  __shared__ __align__(16) uint8_t row_code[ROWS ? 128 * 64 : 16];
+  __shared__ __align__(16) uint8_t col_scale[128 * 4];
+  __shared__ __align__(16) uint8_t row_scale[ROWS ? 128 * 4 : 16];
+  const int b = blockIdx.z, tid = threadIdx.x, h = tid >> 5, l = tid & 31;
+  const int i0 = blockIdx.y * 128, j0 = blockIdx.x * 128;
+  const int i = i0 + 32 * h, j = j0 + 4 * l;
+  const int64_t at = static_cast<int64_t>(i) * a.cols + j;
+  float x[32][4];
+  if (i0 + 128 <= a.rows && j0 + 128 <= a.cols) {
+    load_tile<D, true>(a.X[b], at, a.cols, 32, 4, x);
+  } else {
+    load_tile<D, false>(a.X[b], at, a.cols, a.rows - i, a.cols - j, x);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) top = top3(x[e][c], x[e + 1][c], top);
+    const uint32_t byte = mx4_scale_byte(__float_as_uint(top));
+    const float scale = scale_operand(byte);
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float y[8] = {x[8 * q][c],     x[8 * q + 1][c], x[8 * q + 2][c], x[8 * q + 3][c],
+                          x[8 * q + 4][c], x[8 * q + 5][c], x[8 * q + 6][c], x[8 * q + 7][c]};
+      w[q] = byte == 255u ? 0u : code8(y, scale);
+    }
+    // column 4 l + c at place 32 c + l, so that the lanes' stores are neighbours
+    *reinterpret_cast<uint4*>(col_code + (32 * c + l) * kColPitch + 16 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+    col_scale[(32 * c + l) * 4 + h] = static_cast<uint8_t>(byte);
+  }
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int e8 = 0; e8 < 32; e8 += 8) {
+      uint32_t mine = 0;  // scale byte of row e8 + l % 8 of this lane's block of 32 columns
+#pragma unroll
+      for (int e = e8; e < e8 + 8; ++e) {
+        uint32_t top = __float_as_uint(top3(top3(x[e][0], x[e][1], x[e][2]), x[e][3], 0.0f));
+        top = dpp_max<kXor1>(top);
+        top = dpp_max<kXor2>(top);
+        top = dpp_max<kHalfMirror>(top);
+        const uint32_t byte = mx4_scale_byte(top);
+        const float scale = scale_operand(byte);
+        uint32_t w = code_pair<1>(code_pair<0>(0, x[e][0], x[e][1], scale), x[e][2], x[e][3], scale);
+        w = byte == 255u ? 0u : w;
+        *reinterpret_cast<uint16_t*>(row_code + (32 * h + e) * 64 + 2 * l) = static_cast<uint16_t>(w);
+        mine = (l & 7) == e - e8 ? byte : mine;
+      }
+      row_scale[(32 * h + e8 + (l & 7)) * 4 + (l >> 3)] = static_cast<uint8_t>(mine);
+    }
+  }
+  __syncthreads();
+  {
+    const int cols_left = a.cols - j0;
+    const int64_t line = static_cast<int64_t>(blockIdx.y) * a.cols + j0;
+    uint4* codes = static_cast<uint4*>(a.codes_t[b]) + line * 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = q * kTileThreads + tid, col = p >> 2;
+      if (col < cols_left)
+        codes[p] = *reinterpret_cast<const uint4*>(col_code + (32 * (col & 3) + (col >> 2)) * kColPitch + 16 * (p & 3));
+    }
+    if (tid < cols_left)
+      static_cast<uint32_t*>(a.scales_t[b])[line + tid] =
+          reinterpret_cast<const uint32_t*>(col_scale)[32 * (tid & 3) + (tid >> 2)];
+  }
+  if constexpr (ROWS) {
+    const int rows_left = a.rows - i0;
+    const int64_t line = static_cast<int64_t>(blockIdx.x) * a.rows + i0;
+    uint4* codes = static_cast<uint4*>(a.codes[b]) + line * 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = q * kTileThreads + tid;
+      if ((p >> 2) < rows_left) codes[p] = reinterpret_cast<const uint4*>(row_code)[p];
+    }
+    if (tid < rows_left)
+      static_cast<uint32_t*>(a.scales[b])[line + tid] = reinterpret_cast<const uint32_t*>(row_scale)[tid];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Values of the code, row-major: threads as in mx4_rows_kernel.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(kThreads) void mx4_values_kernel(Mx4DequantArgs a, int units) {
+  const int b = blockIdx.z, o = threadIdx.x & 15;
+  const int r = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x >> 4);
+  if (r >= a.rows) return;
+  const int u0 = blockIdx.y * kUnitsPerThread;
+  const uint32_t* codes = static_cast<const uint32_t*>(a.codes[b]);
+  const uint8_t* scales = static_cast<const uint8_t*>(a.scales[b]);
+  void* Y = a.Y[b];
+  uint32_t code[kUnitsPerThread], byte[kUnitsPerThread];
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int u = u0 + k < units ? u0 + k : units - 1;
+    const int64_t line = static_cast<int64_t>(u) * a.rows + r;
+    code[k] = codes[line * 16 + o];
+    byte[k] = scales[line * 4 + (o >> 2)];
+  }
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int c = (u0 + k) * kMxUnit + 8 * o, left = a.cols - c;
+    const float s = e8m0_to_f32(byte[k]);
+    const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 0);
+    const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 1);
+    const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 2);
+    const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 3);
+    const float y[8] = {p0[0] * s, p0[1] * s, p1[0] * s, p1[1] * s, p2[0] * s, p2[1] * s, p3[0] * s, p3[1] * s};
+    const int64_t at = static_cast<int64_t>(r) * a.cols + c;
+    if (left >= 8) {
+      if constexpr (D == kF32) {
+        u32x4_a4* p = reinterpret_cast<u32x4_a4*>(static_cast<float*>(Y) + at);
+        p[0] = __builtin_bit_cast(u32x4_t, make_float4(y[0], y[1], y[2], y[3]));
+        p[1] = __builtin_bit_cast(u32x4_t, make_float4(y[4], y[5], y[6], y[7]));
+      } else {
+        *reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(Y) + at) =
+            (u32x4_t){f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]), f32x2_to_bf16x2(y[4], y[5]),
+                      f32x2_to_bf16x2(y[6], y[7])};
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) store_from_f32(Y, at + e, D, y[e]);
+    }
+  }
+}
+
+dim3 row_grid(int rows, int units, int batch) {
+  return dim3((rows + kRowsPerBlock - 1) / kRowsPerBlock, (units + kUnitsPerThread - 1) / kUnitsPerThread, batch);
 }
 
 template <int D>
 void quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) {
-  if (a.codes[0] != nullptr) {
-    const int64_t units = mx4_units(a.cols);
-    hipLaunchKernelGGL(mx4_rows_kernel<D>, dim3(grid_for(units * a.rows * 16), 1, batch), dim3(kThreads), 0, s, a, units);
+  if (a.codes_t[0] == nullptr) {
+    const int units = static_cast<int>(mx4_units(a.cols));
+    hipLaunchKernelGGL(mx4_rows_kernel<D>, row_grid(a.rows, units, batch), dim3(kThreads), 0, s, a, units);
+    return;
   }
-  if (a.codes_t[0] != nullptr) {
-    const int64_t units = mx4_units(a.rows);
-    hipLaunchKernelGGL(mx4_columns_kernel<D>, dim3(grid_for(units * 4 * a.cols), 1, batch), dim3(kThreads), 0, s, a,
-                       units);
+  const dim3 grid(static_cast<uint32_t>(mx4_units(a.cols)), static_cast<uint32_t>(mx4_units(a.rows)), batch);
+  if (a.codes[0] != nullptr) {
+    hipLaunchKernelGGL((mx4_tile_kernel<D, true>), grid, dim3(kTileThreads), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((mx4_tile_kernel<D, false>), grid, dim3(kTileThreads), 0, s, a);
   }
 }
 
@@ -154,12 +342,12 @@ hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) 
 }
 
 hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int batch, hipStream_t s) {
-  const int64_t octets = (static_cast<int64_t>(a.cols) + 7) / 8;
-  const dim3 grid(grid_for(octets * a.rows), 1, batch), block(kThreads);
+  const int units = static_cast<int>(mx4_units(a.cols));
+  const dim3 grid = row_grid(a.rows, units, batch), block(kThreads);
   if (a.y_dtype == kF32) {
-    hipLaunchKernelGGL(mx4_values_kernel<kF32>, grid, block, 0, s, a, octets);
+    hipLaunchKernelGGL(mx4_values_kernel<kF32>, grid, block, 0, s, a, units);
   } else {
-    hipLaunchKernelGGL(mx4_values_kernel<kBF16>, grid, block, 0, s, a, octets);
+    hipLaunchKernelGGL(mx4_values_kernel<kBF16>, grid, block, 0, s, a, units);
   }
   return hipGetLastError();
 }
@@ -226,7 +414,7 @@ muon_status muon_mx4_quantize(int batch, int rows, int cols, const void* const* 
     take(a.scales, scales, at, count);
     take(a.codes_t, codes_t, at, count);
     take(a.scales_t, scales_t, at, count);
-    if (traced_launch(s, "mx4_quantize", "mx4_quantize", 0.0, bytes * count,
+    if (traced_launch(s, codes_t != nullptr ? "mx4_tile_kernel" : "mx4_rows_kernel", "mx4_quantize", 0.0, bytes * count,
                       [&] { return launch_mx4_quantize(a, count, s); }) != hipSuccess)
       return MUON_ERR_HIP;
   }

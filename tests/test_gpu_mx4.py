@@ -314,3 +314,17 @@ def test_mx4_launches_are_traced():
     mu.trace_enable(False)
     assert [r["role"] for r in recs] == ["mx4_quantize", "mx4_dequantize", "mx4_matmul"]
     assert recs[2]["flops"] == 2.0 * 64 * 64 * 128
+
+
+def test_values_of_every_scale_byte():
+    """All scale bytes with all codes: fp32 holds every product exactly up to byte 252 (6 times 2^125)."""
+    units, rows = 2, 256
+    scales = torch.arange(256, dtype=torch.uint8).view(1, 256, 1).expand(units, rows, 4).contiguous()
+    codes = torch.arange(64, dtype=torch.uint8).mul(37).view(1, 1, 64).expand(units, rows, 64).contiguous()
+    codes[..., :16] = torch.arange(16, dtype=torch.uint8) * 17
+    q = mu.MX4([codes.to(DEV)], [scales.to(DEV)], 256)
+    want = xo.decode(codes.numpy(), scales.numpy(), 256)
+    big = np.abs(want) >= 2.0 ** 128  # over fp32's largest value (bytes 253 and 254): infinite
+    want[big] = np.sign(want[big]) * np.inf
+    for dt in (torch.float32, torch.bfloat16):
+        assert np.array_equal(want, f64(mu.mx4_dequantize(q, dt)[0]), equal_nan=True)
