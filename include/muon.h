@@ -346,9 +346,8 @@ muon_status muon_group8_dequantize(int batch, int rows, int k, const void *const
  * call only: such lists are long and their gradients move, so the pointers
  * travel as kernel arguments (one launch per 87 tensors) instead of in an array
  * in device memory.  They must be distinct, and no two of the buffers may overlap.
- * Buffers need the alignment of their element type only; 16-byte aligned ones
- * are faster.  Errors as for muon_step; MUON_ERR_INVALID_ARG also for lr, eps
- * or weight_decay not finite in fp32, eps <= 0, betas outside [0, 1) or step < 1.
+ * Buffers need the alignment of their element type only.  Errors as for muon_step; MUON_ERR_INVALID_ARG also for lr, eps
+ * or weight_decay not finite in fp32, eps < 2^-126, betas outside [0, 1) or step < 1.
  *
  * muon_adamw_config:
  *   lr, beta1, beta2, eps, weight_decay   defaults 1e-3, 0.9, 0.999, 1e-8, 0

@@ -102,33 +102,95 @@ __device__ __forceinline__ Scalars load_scalars(const AdamwScalars& s) {
   return r;
 }
 
-template <int D>
-__device__ __forceinline__ float load_f(const void* p, int64_t i) {
-  return load_as_f32(p, i, D);
+// N consecutive elements of dtype D (N a multiple of 4) as loaded, so that a
+// thread has all its loads out before it waits for the first.  Tensors may start
+// anywhere (views into flat buffers): the loads and stores are 16 bytes wide
+// (8 for four 16-bit elements) but need the alignment of one element only.
+// `left` elements are there (all N if FULL); the others read as zero and are not
+// written.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef u32x2_t u32x2_a1 __attribute__((aligned(1)));
+typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+
+template <int D, int N>
+struct Raw {
+  uint32_t v[D == kF32 ? N : N / 2];
+};
+
+template <int D, int N, bool FULL>
+__device__ __forceinline__ Raw<D, N> load_raw(const void* p, int64_t i, int64_t left) {
+  Raw<D, N> r;
+  if (FULL || left >= N) {
+    if constexpr (D == kF32) {
+#pragma unroll
+      for (int q = 0; q < N; q += 4) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(p) + i + q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.v[q + k] = x[k];
+      }
+    } else if constexpr (N == 4) {
+      const u32x2_t x = *reinterpret_cast<const u32x2_a2*>(static_cast<const uint16_t*>(p) + i);
+      r.v[0] = x[0];
+      r.v[1] = x[1];
+    } else {
+#pragma unroll
+      for (int q = 0; q < N; q += 8) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(p) + i + q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.v[q / 2 + k] = x[k];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < (D == kF32 ? N : N / 2); ++k) r.v[k] = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < left) {
+        if constexpr (D == kF32) {
+          r.v[k] = static_cast<const uint32_t*>(p)[i + k];
+        } else {
+          r.v[k >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i + k]) << (16 * (k & 1));
+        }
+      }
+  }
+  return r;
 }
 
-// Four consecutive elements as fp32 (one 16- or 8-byte load).
-template <int D>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float (&x)[4]) {
+template <int D, int N>
+__device__ __forceinline__ float raw_value(const Raw<D, N>& r, int k) {
   if constexpr (D == kF32) {
-    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    return __uint_as_float(r.v[k]);
   } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-    const uint16_t h[4] = {static_cast<uint16_t>(v.x), static_cast<uint16_t>(v.x >> 16), static_cast<uint16_t>(v.y),
-                           static_cast<uint16_t>(v.y >> 16)};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = D == kBF16 ? bf16_to_f32(h[k]) : f16_to_f32(h[k]);
+    const uint16_t h = static_cast<uint16_t>((k & 1) ? r.v[k >> 1] >> 16 : r.v[k >> 1]);
+    return D == kBF16 ? bf16_to_f32(h) : f16_to_f32(h);
   }
 }
 
-template <int D>
-__device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) {
-  if constexpr (D == kF32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+template <int D, int N, bool FULL>
+__device__ __forceinline__ void store_values(void* p, int64_t i, int64_t left, const float (&x)[N]) {
+  if (FULL || left >= N) {
+    if constexpr (D == kF32) {
+#pragma unroll
+      for (int q = 0; q < N; q += 4)
+        *reinterpret_cast<u32x4_a4*>(static_cast<float*>(p) + i + q) =
+            __builtin_bit_cast(u32x4_t, make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]));
+    } else if constexpr (N == 4) {
+      *reinterpret_cast<u32x2_a2*>(static_cast<uint16_t*>(p) + i) =
+          (u32x2_t){f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3])};
+    } else {
+#pragma unroll
+      for (int q = 0; q < N; q += 8)
+        *reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(p) + i + q) =
+            (u32x4_t){f32x2_to_bf16x2(x[q], x[q + 1]), f32x2_to_bf16x2(x[q + 2], x[q + 3]),
+                      f32x2_to_bf16x2(x[q + 4], x[q + 5]), f32x2_to_bf16x2(x[q + 6], x[q + 7])};
+    }
   } else {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-        make_uint2(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]));
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < left) store_from_f32(p, i + k, D, x[k]);
   }
 }
 
@@ -143,40 +205,46 @@ __device__ __forceinline__ void update(float& w, float g, float& m, float& v, co
   w = w - s.lr * (m * r.c1 / (sqrtf(v) * r.c2 + s.eps) + s.wd * w);
 }
 
-template <int DW, int DG>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(Adamw32Args a) {
-  const int t = find_tensor(a.t, blockIdx.x);
-  const int64_t n = a.t.size[t];
-  void* W = a.t.ptr[0][t];
-  const void* G = a.t.ptr[1][t];
-  float* M = static_cast<float*>(a.t.ptr[2][t]);
-  float* V = static_cast<float*>(a.t.ptr[3][t]);
-  const Scalars r = load_scalars(a.s);
-  const int64_t base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk32;
-  const bool aligned = ((reinterpret_cast<uintptr_t>(W) & (DW == kF32 ? 15 : 7)) |
-                        (reinterpret_cast<uintptr_t>(G) & (DG == kF32 ? 15 : 7)) |
-                        (reinterpret_cast<uintptr_t>(M) & 15) | (reinterpret_cast<uintptr_t>(V) & 15)) == 0;
+template <int DW, int DG, bool FULL>
+__device__ __forceinline__ void adamw_chunk(void* W, const void* G, void* M, void* V, int64_t base, int64_t n,
+                                            const AdamwScalars& s, const Scalars& r) {
+  Raw<DW, 4> w4[kQuads];
+  Raw<DG, 4> g4[kQuads];
+  Raw<kF32, 4> m4[kQuads], v4[kQuads];
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
     const int64_t i = base + (q * kThreads + static_cast<int>(threadIdx.x)) * 4;
-    if (aligned && i + 4 <= n) {
-      float w[4], g[4], m[4], v[4];
-      load4<DW>(W, i, w);
-      load4<DG>(G, i, g);
-      load4<kF32>(M, i, m);
-      load4<kF32>(V, i, v);
+    w4[q] = load_raw<DW, 4, FULL>(W, i, n - i);
+    g4[q] = load_raw<DG, 4, FULL>(G, i, n - i);
+    m4[q] = load_raw<kF32, 4, FULL>(M, i, n - i);
+    v4[q] = load_raw<kF32, 4, FULL>(V, i, n - i);
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) update(w[k], g[k], m[k], v[k], a.s, r);
-      store4<kF32>(M, i, m);
-      store4<kF32>(V, i, v);
-      store4<DW>(W, i, w);
-    } else {
-      for (int k = 0; k < 4 && i + k < n; ++k) {
-        float w = load_f<DW>(W, i + k);
-        update(w, load_f<DG>(G, i + k), M[i + k], V[i + k], a.s, r);
-        store_from_f32(W, i + k, DW, w);
-      }
+  for (int q = 0; q < kQuads; ++q) {
+    const int64_t i = base + (q * kThreads + static_cast<int>(threadIdx.x)) * 4;
+    float w[4], m[4], v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = raw_value(w4[q], k);
+      m[k] = raw_value(m4[q], k);
+      v[k] = raw_value(v4[q], k);
+      update(w[k], raw_value(g4[q], k), m[k], v[k], s, r);
     }
+    store_values<kF32, 4, FULL>(M, i, n - i, m);
+    store_values<kF32, 4, FULL>(V, i, n - i, v);
+    store_values<DW, 4, FULL>(W, i, n - i, w);
+  }
+}
+
+template <int DW, int DG>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Adamw32Args a) {
+  const int t = find_tensor(a.t, blockIdx.x);
+  const int64_t n = a.t.size[t], base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk32;
+  const Scalars r = load_scalars(a.s);
+  if (base + kChunk32 <= n) {
+    adamw_chunk<DW, DG, true>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
+  } else {
+    adamw_chunk<DW, DG, false>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
   }
 }
 
@@ -218,24 +286,44 @@ __device__ __forceinline__ float code_scale(uint32_t top_bits) {
   return s < 0x1p-126f ? 0.0f : s;
 }
 
-// Code of x in [0, 448] with chance h16 / 65536 (see above).
+// sqrt(x) rounded to nearest, for x zero, normal or not finite: v_sqrt_f32 is
+// off by at most one unit; s is too large if x <= s (s - 1 unit) (the square of
+// the midpoint below s, less a quarter unit squared) and too small if x > s (s +
+// 1 unit).  A third of the instructions of sqrtf(), which also scales subnormals.
+__device__ __forceinline__ float root_nearest(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
+  const float under = fmaf(-below, s, x), over = fmaf(-above, s, x);
+  const float r = under <= 0.0f ? below : s;
+  return over > 0.0f ? above : r;
+}
+
+// Code of x in [0, 448] (see above), h16 in 0..65535.  In units of the code step
+// at x (a power of two, so nothing is rounded by it) the neighbours are f and
+// f + 1, and the condition is (y - f)(y + f) > u (2 f + 1).
 __device__ __forceinline__ uint32_t root_code(float x, uint32_t h16, bool positive) {
-  const uint32_t bits = __float_as_uint(x);
-  uint32_t code;
-  float lo, step;
-  if (x < 0x1p-6f) {
-    code = static_cast<uint32_t>(x * 512.0f);
-    lo = static_cast<float>(code) * (1.0f / 512.0f);
-    step = 0x1p-9f;
-  } else {
-    code = (bits >> 20) - (120u << 3);
-    lo = __uint_as_float(bits & ~0xFFFFFu);
-    step = __uint_as_float((bits & 0x7F800000u) - (3u << 23));
+  uint32_t step = __float_as_uint(x) & 0x7F800000u;  // of the binade of x, at least 2^-6
+  step = (step > (121u << 23) ? step : 121u << 23) - (3u << 23);
+  const float y = x * __uint_as_float((254u << 23) - step);  // x / step: 8..16, or 0..8 under 2^-6
+  const float f = floorf(y);
+  const float bar = (static_cast<float>(h16) + 0.5f) * fmaf(f, 0x1p-15f, 0x1p-16f);
+  const bool up = (y - f) * (y + f) > bar || (f == 0.0f && positive);
+  return ((step - (118u << 23)) >> 20) + static_cast<uint32_t>(f) + (up ? 1u : 0u);
+}
+
+// One element of the 8-bit step: as update(), with the new moment's root r kept
+// and the quotient by v_rcp_f32 (off by one unit at most).
+__device__ __forceinline__ void update8(float& w, float g, float& m, float& v, float& root, const AdamwScalars& s,
+                                        const Scalars& r) {
+  {
+#pragma clang fp contract(off)
+    g *= r.gs;
+    m = s.b1 * m + s.ob1 * g;
+    v = s.b2 * v + (s.ob2 * g) * g;
   }
-  const float u = (static_cast<float>(h16) + 0.5f) * (1.0f / 65536.0f);
-  const float hi = lo + step;
-  const bool up = (x - lo) * (x + lo) > u * ((hi - lo) * (hi + lo)) || (code == 0 && positive);
-  return code + (up ? 1u : 0u);
+  root = root_nearest(v);
+  const float inverse = __builtin_amdgcn_rcpf(fmaf(root, r.c2, s.eps));
+  w = fmaf(-s.lr, fmaf(s.wd, w, m * r.c1 * inverse), w);
 }
 
 __device__ __forceinline__ uint32_t group_max(uint32_t x) {  // over 16 consecutive lanes
@@ -247,105 +335,100 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {  // over 16 consecut
   return x;
 }
 
-template <int DW, int DG>
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(Adamw8Args a) {
-  const int t = find_tensor(a.t, blockIdx.x);
-  const int64_t n = a.t.size[t];
-  void* W = a.t.ptr[0][t];
-  const void* G = a.t.ptr[1][t];
-  uint8_t* mc = static_cast<uint8_t*>(a.t.ptr[2][t]);
-  float* ms = static_cast<float*>(a.t.ptr[3][t]);
-  uint8_t* rc = static_cast<uint8_t*>(a.t.ptr[4][t]);
-  float* rs = static_cast<float*>(a.t.ptr[5][t]);
-  const Scalars r = load_scalars(a.s);
-  const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
-  const int64_t i = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8 + 8 * static_cast<int>(threadIdx.x);
-  const bool aligned = ((reinterpret_cast<uintptr_t>(W) & 15) | (reinterpret_cast<uintptr_t>(G) & 15) |
-                        (reinterpret_cast<uintptr_t>(mc) & 7) | (reinterpret_cast<uintptr_t>(rc) & 7)) == 0;
-  const bool whole = aligned && i + 8 <= n;
-  const bool any = i < n;
-  float w[8], g[8], m[8], v[8];
-  uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
-  if (whole) {
-    float x[4];
+// 8 code bytes.
+template <bool FULL>
+__device__ __forceinline__ u32x2_t load_codes(const void* p, int64_t i, int64_t left) {
+  const uint8_t* c = static_cast<const uint8_t*>(p) + i;
+  if (FULL || left >= 8) return *reinterpret_cast<const u32x2_a1*>(c);
+  u32x2_t r = {0, 0};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load4<DW>(W, i + 4 * h, x);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[4 * h + k] = x[k];
-      load4<DG>(G, i + 4 * h, x);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) g[4 * h + k] = x[k];
-    }
-    const uint2 a2 = *reinterpret_cast<const uint2*>(mc + i), b2 = *reinterpret_cast<const uint2*>(rc + i);
-    cm[0] = a2.x; cm[1] = a2.y; cr[0] = b2.x; cr[1] = b2.y;
+  for (int k = 0; k < 8; ++k)
+    if (k < left) r[k >> 2] |= static_cast<uint32_t>(c[k]) << (8 * (k & 3));
+  return r;
+}
+template <bool FULL>
+__device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t left, u32x2_t x) {
+  uint8_t* c = static_cast<uint8_t*>(p) + i;
+  if (FULL || left >= 8) {
+    *reinterpret_cast<u32x2_a1*>(c) = x;
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = i + k < n;
-      w[k] = in ? load_f<DW>(W, i + k) : 0.0f;
-      g[k] = in ? load_f<DG>(G, i + k) : 0.0f;
-      cm[k >> 2] |= (in ? static_cast<uint32_t>(mc[i + k]) : 0u) << (8 * (k & 3));
-      cr[k >> 2] |= (in ? static_cast<uint32_t>(rc[i + k]) : 0u) << (8 * (k & 3));
-    }
+    for (int k = 0; k < 8; ++k)
+      if (k < left) c[k] = static_cast<uint8_t>(x[k >> 2] >> (8 * (k & 3)));
   }
+}
+
+// One chunk: 8 elements a thread, 16 threads a group.
+template <int DW, int DG, bool FULL>
+__device__ __forceinline__ void adamw8_chunk(const Adamw8Args& a, int t, int64_t i, int64_t n, const Scalars& r) {
+  void* const W = a.t.ptr[0][t];
+  float* const ms = static_cast<float*>(a.t.ptr[3][t]);
+  float* const rs = static_cast<float*>(a.t.ptr[5][t]);
+  const int64_t left = n - i;  // 0 or less: nothing is there, but the group's other threads may need this one
+  const Raw<DW, 8> w8 = load_raw<DW, 8, FULL>(W, i, left);
+  const Raw<DG, 8> g8 = load_raw<DG, 8, FULL>(a.t.ptr[1][t], i, left);
+  const u32x2_t cm = load_codes<FULL>(a.t.ptr[2][t], i, left), cr = load_codes<FULL>(a.t.ptr[4][t], i, left);
+  const bool any = FULL || left > 0;
   const float sm = any ? ms[i / kGroup] : 0.0f, sr = any ? rs[i / kGroup] : 0.0f;
-  uint32_t top_m = 0, top_v = 0;
+  const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
+  float w[8], m[8], v[8], root[8], top_m = 0.0f, top_v = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t cmk = cm[k >> 2], crk = cr[k >> 2];
     const auto pm = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(cmk, true) : __builtin_amdgcn_cvt_pk_f32_fp8(cmk, false);
     const auto pr = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(crk, true) : __builtin_amdgcn_cvt_pk_f32_fp8(crk, false);
     m[k] = pm[k & 1] * sm;
-    const float root = pr[k & 1] * sr;
-    v[k] = root * root;
-    update(w[k], g[k], m[k], v[k], a.s, r);
-    if (i + k >= n) m[k] = v[k] = 0.0f;
-    const uint32_t bm = __float_as_uint(m[k]) & 0x7fffffffu, bv = __float_as_uint(v[k]) & 0x7fffffffu;
-    top_m = bm > top_m ? bm : top_m;
-    top_v = bv > top_v ? bv : top_v;
+    const float old = pr[k & 1] * sr;
+    v[k] = old * old;
+    w[k] = raw_value(w8, k);
+    update8(w[k], raw_value(g8, k), m[k], v[k], root[k], a.s, r);
   }
-  const float sm2 = code_scale(group_max(top_m));
-  const float sr2 = code_scale(__float_as_uint(sqrtf(__uint_as_float(group_max(top_v)))));
-  const float im = code_inverse(sm2), ir = code_inverse(sr2);
-  uint32_t nm[2] = {0, 0}, nr[2] = {0, 0};
+  store_values<DW, 8, FULL>(W, i, left, w);
+  // the places of a tensor's last group behind its end hold zeros (codes and
+  // gradients), which stay zeros and leave the group's largest values alone
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
-    const float x0 = im > 0.0f ? fminf(fmaxf(m[k] * im, -448.0f), 448.0f) : 0.0f;
-    const float x1 = im > 0.0f ? fminf(fmaxf(m[k + 1] * im, -448.0f), 448.0f) : 0.0f;
+    top_m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(m[k]), fabsf(m[k + 1])), top_m);
+    top_v = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[k], v[k + 1]), top_v);
+  }
+  const float sm2 = code_scale(group_max(__float_as_uint(top_m)));
+  const float sr2 = code_scale(__float_as_uint(sqrtf(__uint_as_float(group_max(__float_as_uint(top_v))))));
+  const float im = code_inverse(sm2), ir = code_inverse(sr2);
+  u32x2_t nm = {0, 0}, nr = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    // at most 448 (1 + 2^-22), which rounds to 448
     if (k & 2) {
-      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, nm[k >> 2], true);
+      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(m[k] * im, m[k + 1] * im, nm[k >> 2], true);
     } else {
-      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(x0, x1, nm[k >> 2], false);
+      nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(m[k] * im, m[k + 1] * im, nm[k >> 2], false);
     }
     const uint32_t h = mix(static_cast<uint32_t>((i + k) >> 1) + key);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float x = ir > 0.0f ? fminf(sqrtf(v[k + e]) * ir, 448.0f) : 0.0f;
-      const uint32_t c = root_code(x, e == 0 ? h & 0xffffu : h >> 16, ir > 0.0f && v[k + e] > 0.0f);
-      nr[k >> 2] |= c << (8 * ((k + e) & 3));
-    }
+    nr[k >> 2] |= root_code(fminf(root[k] * ir, 448.0f), h & 0xffffu, v[k] > 0.0f) << (8 * (k & 3));
+    nr[k >> 2] |= root_code(fminf(root[k + 1] * ir, 448.0f), h >> 16, v[k + 1] > 0.0f) << (8 * (k & 3) + 8);
   }
-  if (whole) {
-    float x[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = w[4 * h + k];
-      store4<DW>(W, i + 4 * h, x);
-    }
-    *reinterpret_cast<uint2*>(mc + i) = make_uint2(nm[0], nm[1]);
-    *reinterpret_cast<uint2*>(rc + i) = make_uint2(nr[0], nr[1]);
-  } else {
-    for (int k = 0; k < 8 && i + k < n; ++k) {
-      store_from_f32(W, i + k, DW, w[k]);
-      mc[i + k] = static_cast<uint8_t>(nm[k >> 2] >> (8 * (k & 3)));
-      rc[i + k] = static_cast<uint8_t>(nr[k >> 2] >> (8 * (k & 3)));
-    }
+  for (int q = 0; q < 2; ++q) {  // a group that is stored as zeros, or holds a NaN or an infinity
+    nm[q] = im > 0.0f ? nm[q] : 0u;
+    nr[q] = ir > 0.0f ? nr[q] : 0u;
   }
+  store_codes<FULL>(a.t.ptr[2][t], i, left, nm);
+  store_codes<FULL>(a.t.ptr[4][t], i, left, nr);
   if (any && (threadIdx.x & 15) == 0) {
     ms[i / kGroup] = sm2;
     rs[i / kGroup] = sr2;
+  }
+}
+
+template <int DW, int DG>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Adamw8Args a) {
+  const int t = find_tensor(a.t, blockIdx.x);
+  const int64_t n = a.t.size[t], base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8;
+  const Scalars r = load_scalars(a.s);
+  if (base + kChunk8 <= n) {
+    adamw8_chunk<DW, DG, true>(a, t, base + 8 * static_cast<int>(threadIdx.x), n, r);
+  } else {
+    adamw8_chunk<DW, DG, false>(a, t, base + 8 * static_cast<int>(threadIdx.x), n, r);
   }
 }
 
@@ -357,7 +440,7 @@ muon_status make_scalars(const muon_adamw_config* cfg, AdamwScalars* s) {
   if (!isfinite(cfg->lr) || !isfinite(cfg->weight_decay) || !isfinite(cfg->eps)) return MUON_ERR_INVALID_ARG;
   if (!(cfg->beta1 >= 0.0) || !(cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0) || !(cfg->beta2 < 1.0))
     return MUON_ERR_INVALID_ARG;
-  if (!(static_cast<float>(cfg->eps) > 0.0f)) return MUON_ERR_INVALID_ARG;
+  if (!(static_cast<float>(cfg->eps) >= 0x1p-126f)) return MUON_ERR_INVALID_ARG;  // its reciprocal is finite
   if (cfg->step_dev == nullptr && cfg->step < 1) return MUON_ERR_INVALID_ARG;
   memset(s, 0, sizeof(*s));
   s->lr = static_cast<float>(cfg->lr);

@@ -196,8 +196,9 @@ def step8(W, state, G, t, seed, w, hyper, scale=1.0):
                 hyper["eps"], hyper["weight_decay"], scale)
         w_new, m, v = ao.adamw(*args)
         tol = ao.adamw_tolerance(*args, w_half=HALF[w])[0]
-        # decoding adds h to m and 3 h to v: 1 h of the first and 1.5 h of the second term of 17 h
-        assert np.all(np.abs(f64(W[k]) - w_new) <= tol * 1.25), f"tensor {k}: W"
+        # decoding adds h to m and 3 h to v, so 2.5 h to the step's 17 h; the reciprocal (2 h, and the product with it h)
+        # in the place of the quotient's h adds 2 h: 21.5 h in all
+        assert np.all(np.abs(f64(W[k]) - w_new) <= tol * 21.5 / 17), f"tensor {k}: W"
         bad = ao.check_moment_codes(bytes_of(state.m_codes[k]), f64(state.m_scales[k]), m, SLACK)
         assert bad == 0, f"tensor {k}: {bad} codes of m"
         bad = ao.check_root_codes(bytes_of(state.r_codes[k]), f64(state.r_scales[k]), v,
