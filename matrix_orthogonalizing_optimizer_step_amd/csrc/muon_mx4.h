@@ -44,16 +44,28 @@ struct Mx4DequantArgs {
 hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int batch, hipStream_t s);
 
 struct Mx4GemmArgs {
-  int m, n, k, units;
+  int batch, m, n, k, units;
   int c_dtype;
   int accumulate;               // C += A B^T
+  int pieces, piece_units;      // split along k: units per piece
+  float* partial;               // pieces x batch x m x n sums, if pieces > 1
   const void* A[kMxBatch];      // codes of m x k
   const void* As[kMxBatch];     // scales
   const void* B[kMxBatch];      // codes of n x k
   const void* Bs[kMxBatch];
   void* C[kMxBatch];            // m x n, row-major
 };
-hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, int batch, hipStream_t s);
+
+// How a product of one launch (at most kMxBatch matrices) is computed.
+enum Mx4Kind : int { kMxFewRows = 0, kMxLow, kMxMid, kMxBig };
+struct Mx4Plan {
+  Mx4Kind kind;
+  int pieces, piece_units;
+  size_t bytes;                 // of partial sums
+};
+Mx4Plan mx4_plan(int batch, int m, int n, int k);
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, Mx4Kind kind, hipStream_t s);
+hipError_t launch_mx4_join(const Mx4GemmArgs& a, hipStream_t s);  // the pieces' sums into C
 
 // 2^(byte - 127), NaN for byte 255.
 __device__ __forceinline__ float e8m0_to_f32(uint32_t byte) {

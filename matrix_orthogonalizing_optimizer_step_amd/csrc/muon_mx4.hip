@@ -450,7 +450,14 @@ muon_status muon_mx4_dequantize(int batch, int rows, int cols, const void* const
 
 size_t muon_mx4_workspace_size(int batch, int m, int n, int k) {
   if (!mx4_shape_ok(batch, m, k) || !mx4_shape_ok(batch, n, k) || !operand_ok(m, k) || !operand_ok(n, k)) return 0;
-  return 256;
+  // one launch at a time uses it: the largest need is that of a whole launch or of the last one
+  const int whole = batch < kMxBatch ? batch : kMxBatch, rest = batch % kMxBatch;
+  size_t bytes = mx4_plan(whole, m, n, k).bytes;
+  if (rest > 0) {
+    const size_t last = mx4_plan(rest, m, n, k).bytes;
+    bytes = last > bytes ? last : bytes;
+  }
+  return bytes > 256 ? (bytes + 255) / 256 * 256 : 256;
 }
 
 muon_status muon_mx4_matmul(int batch, int m, int n, int k, const void* const* A_codes, const void* const* A_scales,
@@ -472,20 +479,30 @@ muon_status muon_mx4_matmul(int batch, int m, int n, int k, const void* const* A
                        mn * (c_dtype == MUON_F32 ? 4.0 : 2.0) * (accumulate ? 2.0 : 1.0);
   for (int at = 0; at < batch; at += kMxBatch) {
     const int count = batch - at < kMxBatch ? batch - at : kMxBatch;
+    const Mx4Plan plan = mx4_plan(count, m, n, k);
     Mx4GemmArgs a;
+    a.batch = count;
     a.m = m;
     a.n = n;
     a.k = k;
     a.units = static_cast<int>(mx4_units(k));
     a.c_dtype = c_dtype;
     a.accumulate = accumulate;
+    a.pieces = plan.pieces;
+    a.piece_units = plan.piece_units;
+    a.partial = static_cast<float*>(workspace);
     take(a.A, A_codes, at, count);
     take(a.As, A_scales, at, count);
     take(a.B, B_codes, at, count);
     take(a.Bs, B_scales, at, count);
     take(a.C, C, at, count);
-    if (traced_launch(s, "mx4_gemm_kernel", "mx4_matmul", 2.0 * count * mn * k, bytes * count,
-                      [&] { return launch_mx4_gemm(a, count, s); }) != hipSuccess)
+    const char* kernel = plan.kind == kMxFewRows ? "mx4_few_rows_kernel" : "mx4_tile_gemm_kernel";
+    if (traced_launch(s, kernel, "mx4_matmul", 2.0 * count * mn * k, bytes * count,
+                      [&] { return launch_mx4_gemm(a, plan.kind, s); }) != hipSuccess)
+      return MUON_ERR_HIP;
+    if (plan.pieces > 1 &&
+        traced_launch(s, "mx4_join_kernel", "mx4_join", 0.0, count * mn * (4.0 * plan.pieces + (c_dtype == MUON_F32 ? 4.0 : 2.0)),
+                      [&] { return launch_mx4_join(a, s); }) != hipSuccess)
       return MUON_ERR_HIP;
   }
   return MUON_OK;

@@ -27,61 +27,19 @@ __device__ __forceinline__ f32x16_t mfma_mx4(const uint4& a, const uint4& b, con
                                                          static_cast<int>(sb));
 }
 
-constexpr int kTile = 64;  // block tile edge: 4 waves, one 32 x 32 MFMA tile each
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-template <int DC>
-__global__ __launch_bounds__(256) void mx4_gemm_kernel(Mx4GemmArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int i0 = blockIdx.y * kTile + 32 * (wave >> 1), j0 = blockIdx.x * kTile + 32 * (wave & 1);
-  const int b = blockIdx.z;
-  const uint4* A = static_cast<const uint4*>(a.A[b]);
-  const uint4* B = static_cast<const uint4*>(a.B[b]);
-  const uint32_t* As = static_cast<const uint32_t*>(a.As[b]);
-  const uint32_t* Bs = static_cast<const uint32_t*>(a.Bs[b]);
-  const int ra = i0 + (lane & 31), rb = j0 + (lane & 31);
-  f32x16_t acc = {};
-  for (int u0 = 0; u0 < a.units; u0 += 2) {
-    const int u = u0 + (lane >> 5);
-    uint4 av[4] = {}, bv[4] = {};
-    uint32_t sa = 0, sb = 0;
-    if (u < a.units && ra < a.m) {
-      const int64_t line = static_cast<int64_t>(u) * a.m + ra;
-      for (int s = 0; s < 4; ++s) av[s] = A[line * 4 + s];
-      sa = As[line];
-    }
-    if (u < a.units && rb < a.n) {
-      const int64_t line = static_cast<int64_t>(u) * a.n + rb;
-      for (int s = 0; s < 4; ++s) bv[s] = B[line * 4 + s];
-      sb = Bs[line];
-    }
-    acc = mfma_mx4<0>(av[0], bv[0], acc, sa, sb);
-    acc = mfma_mx4<1>(av[1], bv[1], acc, sa, sb);
-    acc = mfma_mx4<2>(av[2], bv[2], acc, sa, sb);
-    acc = mfma_mx4<3>(av[3], bv[3], acc, sa, sb);
-  }
-  void* C = a.C[b];
-  const int j = j0 + (lane & 31);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int i = i0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-    if (i < a.m && j < a.n) {
-      const int64_t at = static_cast<int64_t>(i) * a.n + j;
-      const float c = a.accumulate ? load_as_f32(C, at, DC) + acc[r] : acc[r];
-      store_from_f32(C, at, DC, c);
-    }
-  }
-}
+constexpr int kCUs = 256;  // compute units of the MI355X: the plans below depend on shapes only
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles: 4 waves of 128 x 128 (4 x 4 MFMA tiles, 256 accumulators),
-// one block per compute unit.  k runs in slabs of one unit (128): the tile's
-// codes (2 x 16 KB, each one contiguous piece of memory) and scales (2 x 1 KB)
-// go straight into a ring of 4 LDS stages, three slabs ahead.  Lanes 0..31
-// take blocks 0 and 1 of the unit, lanes 32..63 blocks 2 and 3 (two MFMAs per
-// tile and slab).  Block b of row r lies in slot b ^ (r / 4 % 4) of the row's 64
-// bytes, so that 16 lanes reading one block of 16 rows touch all LDS banks
-// once; the permutation is in the global addresses of the loads, which stay
-// within a row's 64 bytes.
+// TM x TN tiles by 4 waves (WM x 4 / WM, each FM x FN MFMA tiles of 32 x 32).  k
+// runs in slabs of one unit (128): the tile's codes (each operand one
+// contiguous piece of memory) and scales go straight into a ring of 4 LDS
+// stages, three slabs ahead.  Lanes 0..31 take blocks 0 and 1 of the unit, lanes
+// 32..63 blocks 2 and 3 (two MFMAs per MFMA tile and slab).  Block b of row r
+// lies in slot b ^ (r / 4 % 4) of the row's 64 bytes, so that 16 lanes reading
+// one block of 16 rows touch all LDS banks once; the permutation is in the
+// global addresses of the loads, which stay within a row's 64 bytes.
 //
 // The fragments of a k-step are read while the previous step's MFMAs run.  The
 // barrier sits in the middle of a slab's second step: all reads of the slab are
@@ -90,15 +48,18 @@ __global__ __launch_bounds__(256) void mx4_gemm_kernel(Mx4GemmArgs a) {
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kBig = 256;                          // tile edge
 constexpr int kStages = 4;
-constexpr int kStageU4 = 2 * kBig * 4;             // uint4 of codes per stage
 constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;  // sched_group_barrier masks
-constexpr int kLoadsPerSlab = 10;                  // per wave: 4 + 4 of codes, 1 + 1 of scales
 
-struct BigStage {
-  uint4 code[kStageU4];        // A rows, then B rows, 4 slots each
-  uint32_t scale[2 * kBig];    // A rows, then B rows
+template <int TM_, int TN_, int WM_>
+struct Tile {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = 4 / WM_;
+  static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
+  static constexpr int kLoads = TM / 64 + TN / 64 + 2;  // per wave and slab: codes, and scales of A and B
+  struct Stage {
+    uint4 code[(TM + TN) * 4];   // A rows, then B rows, 4 slots each
+    uint32_t scale[TM + TN];
+  };
 };
 
 constexpr int waitcnt_imm(int vm, int lgkm) {  // vmcnt, no wait for exports, lgkmcnt
@@ -113,111 +74,123 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
                                            __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
 }
 
-// One operand's source: codes and scales of the 64 rows this wave loads.
-struct BigSource {
+// One operand's source: codes and scales from this wave's first row on.
+struct Source {
   __amdgpu_buffer_rsrc_t code, scale;
   uint32_t row;     // first row of this wave's loads
   uint32_t rows;    // rows of the matrix
 };
 
-__device__ __forceinline__ void load_operand(BigStage& st, int side, const BigSource& src, uint32_t u, int wave,
-                                             int vcode, int vscale) {
-  // u may lie behind the last unit and rows behind the last row: such addresses
-  // are behind the buffer's end (zeros) or in the next unit's rows, and what
-  // they give enters no stored element
+// This wave's ROWS (a multiple of 16) rows of unit u of one operand, to place `at`
+// of the stage.  u may lie behind the last unit and rows behind the last row:
+// such addresses are behind the buffer's end (zeros) or in the next unit's rows,
+// and what they give enters no stored element.
+template <int ROWS, class Stage>
+__device__ __forceinline__ void load_operand(Stage& st, int at, const Source& src, uint32_t u, int lane, int vcode) {
   const uint32_t line = u * src.rows + src.row;
   const int so = __builtin_amdgcn_readfirstlane(static_cast<int>(line * 64u));
-  lds_ptr_t dst = (lds_ptr_t)(st.code + (side * kBig + wave * 64) * 4);
+  lds_ptr_t dst = (lds_ptr_t)(st.code + at * 4);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 0, 0);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 1024, 0);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 2048, 0);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 3072, 0);
-  lds_ptr_t sd = (lds_ptr_t)(st.scale + side * kBig + wave * 64);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.scale, sd, 4, vscale,
-                                           __builtin_amdgcn_readfirstlane(static_cast<int>(line * 4u)), 0, 0);
+  if constexpr (ROWS > 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 1024, 0);
+  if constexpr (ROWS > 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 2048, 0);
+  if constexpr (ROWS > 48) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 3072, 0);
+  static_assert(ROWS <= 64, "one scale word per lane");
+  lds_ptr_t sd = (lds_ptr_t)(st.scale + at);
+  if (ROWS == 64 || lane < ROWS)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.scale, sd, 4, lane * 4,
+                                             __builtin_amdgcn_readfirstlane(static_cast<int>(line * 4u)), 0, 0);
 }
 
-struct Frags {
-  uint4 a[4], b[4];
-};
-struct ScaleWords {
-  uint32_t a[4], b[4];
-};
-
-// k-step s of a stage: this wave's 4 row fragments of A and of B.
-__device__ __forceinline__ void read_frag(uint4 (&f)[4], const BigStage& st, int first_row, int lane, int s) {
+// The 32-row fragments of k-step s from row `first` of a stage on.
+template <int F, class Stage>
+__device__ __forceinline__ void read_frag(uint4 (&f)[F], const Stage& st, int first, int lane, int s) {
   const int r = lane & 31, slot = (2 * (lane >> 5) + s) ^ ((r >> 2) & 3);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) f[x] = st.code[(first_row + 32 * x + r) * 4 + slot];
+  for (int x = 0; x < F; ++x) f[x] = st.code[(first + 32 * x + r) * 4 + slot];
 }
-__device__ __forceinline__ void read_scales(uint32_t (&w)[4], const BigStage& st, int first_row, int lane) {
+template <int F, class Stage>
+__device__ __forceinline__ void read_scales(uint32_t (&w)[F], const Stage& st, int first, int lane) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) w[x] = st.scale[first_row + 32 * x + (lane & 31)];
+  for (int x = 0; x < F; ++x) w[x] = st.scale[first + 32 * x + (lane & 31)];
 }
 // The upper lanes' blocks are bytes 2 and 3.
-__device__ __forceinline__ void shift_scales(uint32_t (&w)[4], int lane) {
+template <int F>
+__device__ __forceinline__ void shift_scales(uint32_t (&w)[F], int lane) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) w[x] >>= (lane >> 5) * 16;
+  for (int x = 0; x < F; ++x) w[x] >>= (lane >> 5) * 16;
 }
 
-template <int S, int Y0, int Y1>
-__device__ __forceinline__ void mfmas(f32x16_t (&acc)[4][4], const Frags& f, const ScaleWords& w) {
+template <class T>
+struct Frags {
+  uint4 a[T::FM], b[T::FN];
+};
+template <class T>
+struct ScaleWords {
+  uint32_t a[T::FM], b[T::FN];
+};
+
+template <class T, int S, int Y0, int Y1>
+__device__ __forceinline__ void mfmas(f32x16_t (&acc)[T::FN][T::FM], const Frags<T>& f, const ScaleWords<T>& w) {
 #pragma unroll
   for (int y = Y0; y < Y1; ++y)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x][y] = mfma_mx4<S>(f.b[x], f.a[y], acc[x][y], w.b[x], w.a[y]);
+    for (int x = 0; x < T::FN; ++x) acc[x][y] = mfma_mx4<S>(f.b[x], f.a[y], acc[x][y], w.b[x], w.a[y]);
 }
 
 // One slab from stage `cur`; fragments of its first step are in f0, its scales
 // in w.  Ends with those of the next slab (stage `nxt`) there.
-__device__ __forceinline__ void slab(f32x16_t (&acc)[4][4], Frags& f0, ScaleWords& w, BigStage& cur,
-                                     const BigStage& nxt, const BigSource& A, const BigSource& B, uint32_t u, int wave,
-                                     int lane, int vcode, int vscale, int ra, int rb) {
-  Frags f1;
-  read_frag(f1.b, cur, rb, lane, 1);
-  read_frag(f1.a, cur, ra, lane, 1);
-  mfmas<0, 0, 4>(acc, f0, w);
+template <class T>
+__device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0, ScaleWords<T>& w,
+                                     typename T::Stage& cur, const typename T::Stage& nxt, const Source& A,
+                                     const Source& B, uint32_t u, int wave, int lane, int vcode, int ra, int rb) {
+  constexpr int FM = T::FM, FN = T::FN;
+  Frags<T> f1;
+  read_frag<FN>(f1.b, cur, rb, lane, 1);
+  read_frag<FM>(f1.a, cur, ra, lane, 1);
+  mfmas<T, 0, 0, FM>(acc, f0, w);
+  if constexpr (FM * FN >= FM + FN) {
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
+    for (int g = 0; g < FM + FN; ++g) {
+      __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, FM * FN / (FM + FN), 0);
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
-  mfmas<1, 0, 2>(acc, f1, w);
+  mfmas<T, 1, 0, FM / 2>(acc, f1, w);
   // this wave's part of the next slab has landed (two slabs stay in flight), and
   // all its reads of this one are done
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * kLoadsPerSlab, 0));
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kLoads, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  load_operand(cur, 0, A, u + kStages, wave, vcode, vscale);
-  load_operand(cur, 1, B, u + kStages, wave, vcode, vscale);
-  ScaleWords wn;
-  read_frag(f0.b, nxt, rb, lane, 0);
-  read_frag(f0.a, nxt, ra, lane, 0);
-  read_scales(wn.b, nxt, rb, lane);
-  read_scales(wn.a, nxt, ra, lane);
-  mfmas<1, 2, 4>(acc, f1, w);
+  load_operand<T::TM / 4>(cur, wave * (T::TM / 4), A, u + kStages, lane, vcode);
+  load_operand<T::TN / 4>(cur, T::TM + wave * (T::TN / 4), B, u + kStages, lane, vcode);
+  ScaleWords<T> wn;
+  read_frag<FN>(f0.b, nxt, rb, lane, 0);
+  read_frag<FM>(f0.a, nxt, ra, lane, 0);
+  read_scales<FN>(wn.b, nxt, rb, lane);
+  read_scales<FM>(wn.a, nxt, ra, lane);
+  mfmas<T, 1, FM / 2, FM>(acc, f1, w);
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+  for (int g = 0; g < FM * FN / 2; ++g) {
     __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 2, 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedVmem, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedDsRead, (2 * (FM + FN) + FM * FN / 2 - 1) / (FM * FN / 2), 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedVmem, (T::kLoads + FM * FN / 2 - 1) / (FM * FN / 2), 0);
   }
   __builtin_amdgcn_sched_barrier(0);
-  shift_scales(wn.b, lane);
-  shift_scales(wn.a, lane);
+  shift_scales<FN>(wn.b, lane);
+  shift_scales<FM>(wn.a, lane);
   w = wn;
 }
 
 // Block id -> tile: consecutive ids go to the 8 XCDs in turn, so each XCD gets a
 // contiguous range of tiles, and tiles run down columns of 4 tile rows, so that
 // the tiles an XCD works on at one time share their rows of A and B in its L2.
-__device__ __forceinline__ void tile_of(int id, int total, int tm, int tn, int* batch, int* ti, int* tj) {
+__device__ __forceinline__ void tile_of(int id, int total, int tm, int tn, int* outer, int* ti, int* tj) {
   const int q = total >> 3, rest = total & 7, x = id & 7, at = id >> 3;
   int t = x * q + (x < rest ? x : rest) + at;
   const int per = tm * tn;
-  *batch = t / per;
-  t -= *batch * per;
+  *outer = t / per;
+  t -= *outer * per;
   constexpr int kGroup = 4;
   const int g = t / (kGroup * tn), first = g * kGroup, h = tm - first < kGroup ? tm - first : kGroup;
   t -= g * kGroup * tn;
@@ -225,6 +198,8 @@ __device__ __forceinline__ void tile_of(int id, int total, int tm, int tn, int* 
   *tj = t / h;
 }
 
+// Four consecutive elements of a row of C (those with left > 0), with what is
+// there if asked for.  vec: the place is aligned to four elements.
 template <int DC>
 __device__ __forceinline__ void store_quad(void* C, int64_t at, const float (&v)[4], int left, bool vec, int accumulate) {
   float x[4] = {v[0], v[1], v[2], v[3]};
@@ -254,90 +229,264 @@ __device__ __forceinline__ void store_quad(void* C, int64_t at, const float (&v)
   }
 }
 
-template <int DC>
-__global__ __launch_bounds__(256, 1) void mx4_gemm_big_kernel(Mx4GemmArgs a, int tm, int tn) {
-  __shared__ BigStage s0, s1, s2, s3;
+template <class T, int DC>
+__global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kernel(Mx4GemmArgs a, int tm, int tn) {
+  typedef typename T::Stage Stage;
+  constexpr int FM = T::FM, FN = T::FN;
+  __shared__ Stage s0, s1, s2, s3;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  int b, ti, tj;
-  tile_of(blockIdx.x, gridDim.x, tm, tn, &b, &ti, &tj);
-  const int i0 = ti * kBig, j0 = tj * kBig;
+  int outer, ti, tj;
+  tile_of(blockIdx.x, gridDim.x, tm, tn, &outer, &ti, &tj);
+  const int b = outer / a.pieces, piece = outer - b * a.pieces;
+  const int i0 = ti * T::TM, j0 = tj * T::TN;
+  const int ub = piece * a.piece_units, ue = ub + a.piece_units < a.units ? ub + a.piece_units : a.units;
   const uint32_t lines_a = static_cast<uint32_t>(a.units) * a.m, lines_b = static_cast<uint32_t>(a.units) * a.n;
-  const BigSource A{make_rsrc(a.A[b], lines_a * 64u), make_rsrc(a.As[b], lines_a * 4u),
-                    static_cast<uint32_t>(i0 + wave * 64), static_cast<uint32_t>(a.m)};
-  const BigSource B{make_rsrc(a.B[b], lines_b * 64u), make_rsrc(a.Bs[b], lines_b * 4u),
-                    static_cast<uint32_t>(j0 + wave * 64), static_cast<uint32_t>(a.n)};
+  const Source A{make_rsrc(a.A[b], lines_a * 64u), make_rsrc(a.As[b], lines_a * 4u),
+                 static_cast<uint32_t>(i0 + wave * (T::TM / 4)), static_cast<uint32_t>(a.m)};
+  const Source B{make_rsrc(a.B[b], lines_b * 64u), make_rsrc(a.Bs[b], lines_b * 4u),
+                 static_cast<uint32_t>(j0 + wave * (T::TN / 4)), static_cast<uint32_t>(a.n)};
   // lane l fills slot l % 4 of row l / 4 of each 16-row piece
-  const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16), vscale = lane * 4;
-  BigStage* st[kStages] = {&s0, &s1, &s2, &s3};
+  const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  Stage* st[kStages] = {&s0, &s1, &s2, &s3};
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
-    load_operand(*st[s], 0, A, s, wave, vcode, vscale);
-    load_operand(*st[s], 1, B, s, wave, vcode, vscale);
+    load_operand<T::TM / 4>(*st[s], wave * (T::TM / 4), A, ub + s, lane, vcode);
+    load_operand<T::TN / 4>(*st[s], T::TM + wave * (T::TN / 4), B, ub + s, lane, vcode);
   }
-  const int ra = 128 * (wave >> 1), rb = kBig + 128 * (wave & 1);
-  f32x16_t acc[4][4] = {};
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * kLoadsPerSlab, 0));
+  const int ra = FM * 32 * (wave / T::WN), rb = T::TM + FN * 32 * (wave % T::WN);
+  f32x16_t acc[FN][FM] = {};
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::kLoads, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  Frags f;
-  ScaleWords w;
-  read_frag(f.b, s0, rb, lane, 0);
-  read_frag(f.a, s0, ra, lane, 0);
-  read_scales(w.b, s0, rb, lane);
-  read_scales(w.a, s0, ra, lane);
-  shift_scales(w.b, lane);
-  shift_scales(w.a, lane);
-  int u = 0;
-  for (; u + kStages <= a.units; u += kStages) {
-    slab(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, vscale, ra, rb);
-    slab(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, vscale, ra, rb);
-    slab(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, vscale, ra, rb);
-    slab(acc, f, w, s3, s0, A, B, u + 3, wave, lane, vcode, vscale, ra, rb);
+  Frags<T> f;
+  ScaleWords<T> w;
+  read_frag<FN>(f.b, s0, rb, lane, 0);
+  read_frag<FM>(f.a, s0, ra, lane, 0);
+  read_scales<FN>(w.b, s0, rb, lane);
+  read_scales<FM>(w.a, s0, ra, lane);
+  shift_scales<FN>(w.b, lane);
+  shift_scales<FM>(w.a, lane);
+  int u = ub;
+  for (; u + kStages <= ue; u += kStages) {
+    slab<T>(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s3, s0, A, B, u + 3, wave, lane, vcode, ra, rb);
   }
-  if (u < a.units) slab(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, vscale, ra, rb);
-  if (u + 1 < a.units) slab(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, vscale, ra, rb);
-  if (u + 2 < a.units) slab(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, vscale, ra, rb);
+  if (u < ue) slab<T>(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
+  if (u + 1 < ue) slab<T>(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
+  if (u + 2 < ue) slab<T>(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
   // loads behind the last unit are still on their way into LDS: they end before
   // the block does
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
   // D = (B rows) x (A rows): lane l holds row l % 32 of C and, in registers
   // 4 g .. 4 g + 3, columns 8 g + 4 (l / 32) .. + 3
-  void* C = a.C[b];
-  const bool vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 ? 15u : 7u)) == 0;
+  const bool split = a.pieces > 1;
+  void* C = split ? static_cast<void*>(a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n) : a.C[b];
+  const bool vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 || split ? 15u : 7u)) == 0;
 #pragma unroll
-  for (int y = 0; y < 4; ++y) {
+  for (int y = 0; y < FM; ++y) {
     const int i = i0 + ra + 32 * y + (lane & 31);
     if (i < a.m) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < FN; ++x)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int j = j0 + (rb - kBig) + 32 * x + 8 * g + 4 * (lane >> 5);
+          const int j = j0 + (rb - T::TM) + 32 * x + 8 * g + 4 * (lane >> 5);
           const float v[4] = {acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
-          store_quad<DC>(C, static_cast<int64_t>(i) * a.n + j, v, a.n - j, vec, a.accumulate);
+          const int64_t at = static_cast<int64_t>(i) * a.n + j;
+          if (DC != kF32 && split) {
+            store_quad<kF32>(C, at, v, a.n - j, vec, 0);
+          } else {
+            store_quad<DC>(C, at, v, a.n - j, vec, split ? 0 : a.accumulate);
+          }
         }
     }
   }
 }
 
+// ---------------------------------------------------------------------------
+// The pieces of a product that was split along k, added in their order.
+// ---------------------------------------------------------------------------
+template <int DC>
+__global__ __launch_bounds__(256) void mx4_join_kernel(Mx4GemmArgs a) {
+  const int b = blockIdx.z;
+  const int64_t mn = static_cast<int64_t>(a.m) * a.n, step = static_cast<int64_t>(a.batch) * mn;
+  const float* part = a.partial + b * mn;
+  void* C = a.C[b];
+  const bool vec = (mn & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 ? 15u : 7u)) == 0;
+  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; at < mn;
+       at += static_cast<int64_t>(gridDim.x) * 1024) {
+    const int left = mn - at < 4 ? static_cast<int>(mn - at) : 4;
+    float v[4] = {};
+    for (int p = 0; p < a.pieces; ++p) {
+      if (vec) {
+        const float4 x = *reinterpret_cast<const float4*>(part + p * step + at);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) v[e] += part[p * step + at + e];
+      }
+    }
+    store_quad<DC>(C, at, v, left, vec, a.accumulate);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// At most 16 rows of A (a few tokens against a weight): the codes of B are what
+// has to be read.  A wave takes NT tiles of 16 rows of B (v_mfma_scale_f32_
+// 16x16x128_f8f6f4: a lane holds one block of one row, a unit of 16 rows is 1 KB
+// of contiguous memory) and every NW-th unit of k, straight from memory into
+// registers; the block's NW sums are added in LDS, in their order.  Rows of A
+// behind the last one repeat it and are not stored.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 16;
+constexpr int kUnitsAhead = 4;
+
+template <int NT, int NW, int DC>
+__global__ __launch_bounds__(64 * NW) void mx4_few_rows_kernel(Mx4GemmArgs a) {
+  __shared__ f32x4_t sums[NW][NT][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.z;
+  const int j0 = blockIdx.x * 16 * NT, r = lane & 15, blk = lane >> 4;
+  const uint4* A = static_cast<const uint4*>(a.A[b]) + blk;
+  const uint4* B = static_cast<const uint4*>(a.B[b]) + blk;
+  const uint8_t* As = static_cast<const uint8_t*>(a.As[b]) + blk;
+  const uint8_t* Bs = static_cast<const uint8_t*>(a.Bs[b]) + blk;
+  const int ra = r < a.m ? r : a.m - 1;
+  int rb[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) rb[t] = j0 + 16 * t + r < a.n ? j0 + 16 * t + r : a.n - 1;
+  f32x4_t acc[NT] = {};
+  for (int u0 = wave; u0 < a.units; u0 += NW * kUnitsAhead) {
+    uint4 av[kUnitsAhead], bv[kUnitsAhead][NT];
+    uint32_t sa[kUnitsAhead], sb[kUnitsAhead][NT];
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k) {
+      const int u = u0 + k * NW;
+      const bool in = u < a.units;  // a unit behind the last one counts as zeros
+      const int64_t la = static_cast<int64_t>(in ? u : u0) * a.m + ra;
+      av[k] = A[la * 4];
+      sa[k] = As[la * 4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int64_t lb = static_cast<int64_t>(in ? u : u0) * a.n + rb[t];
+        bv[k][t] = B[lb * 4];
+        sb[k][t] = Bs[lb * 4];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k) {
+      if (u0 + k * NW < a.units) {
+        const i32x8_t x = {static_cast<int>(av[k].x), static_cast<int>(av[k].y), static_cast<int>(av[k].z),
+                           static_cast<int>(av[k].w), 0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const i32x8_t y = {static_cast<int>(bv[k][t].x), static_cast<int>(bv[k][t].y), static_cast<int>(bv[k][t].z),
+                             static_cast<int>(bv[k][t].w), 0, 0, 0, 0};
+          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(y, x, acc[t], kFp4, kFp4, 0,
+                                                                    static_cast<int>(sb[k][t]), 0,
+                                                                    static_cast<int>(sa[k]));
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) sums[wave][t][lane] = acc[t];
+  __syncthreads();
+  // lane l of a tile: row l % 16 of C, columns 4 (l / 16) .. + 3
+  void* C = a.C[b];
+  const bool vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 ? 15u : 7u)) == 0;
+  for (int p = threadIdx.x; p < 64 * NT; p += 64 * NW) {
+    const int t = p >> 6, l = p & 63, i = l & 15, j = j0 + 16 * t + 4 * (l >> 4);
+    if (i >= a.m || j >= a.n) continue;
+    f32x4_t s = sums[0][t][l];
+#pragma unroll
+    for (int q = 1; q < NW; ++q) s += sums[q][t][l];
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    store_quad<DC>(C, static_cast<int64_t>(i) * a.n + j, v, a.n - j, vec, a.accumulate);
+  }
+}
+
+typedef Tile<256, 256, 2> Big;
+typedef Tile<128, 128, 2> Mid;
+typedef Tile<64, 128, 1> Low;
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Split of a product along k when its tiles do not fill the compute units:
+// pieces of at least kMinPiece units, as many as give every block slot one.
+constexpr int kMinPiece = 4;
+
+void split_k(int64_t tiles, int slots, int units, int* pieces, int* piece_units) {
+  int p = static_cast<int>(slots / tiles);
+  const int most = units / kMinPiece;
+  p = p < most ? p : most;
+  p = p < 1 ? 1 : p;
+  *piece_units = ceil_div(units, p);
+  *pieces = ceil_div(units, *piece_units);
+}
+
+template <class T>
+int64_t tiles_of(int batch, int m, int n) {
+  return static_cast<int64_t>(ceil_div(m, T::TM)) * ceil_div(n, T::TN) * batch;
+}
+
 }  // namespace
 
-hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, int batch, hipStream_t s) {
-  if (a.m > 128 && a.n > 128) {
-    const int tm = (a.m + kBig - 1) / kBig, tn = (a.n + kBig - 1) / kBig;
-    const dim3 grid(static_cast<uint32_t>(tm) * tn * batch), block(256);
-    if (a.c_dtype == kF32) {
-      hipLaunchKernelGGL(mx4_gemm_big_kernel<kF32>, grid, block, 0, s, a, tm, tn);
-    } else {
-      hipLaunchKernelGGL(mx4_gemm_big_kernel<kBF16>, grid, block, 0, s, a, tm, tn);
-    }
-    return hipGetLastError();
+Mx4Plan mx4_plan(int batch, int m, int n, int k) {
+  Mx4Plan p{kMxFewRows, 1, 0, 0};
+  const int units = static_cast<int>(mx4_units(k));
+  p.piece_units = units;
+  if (m <= kFewRows) return p;
+  if (tiles_of<Big>(batch, m, n) * 4 >= kCUs * 3) {
+    p.kind = kMxBig;
+    return p;
   }
-  const dim3 grid((a.n + kTile - 1) / kTile, (a.m + kTile - 1) / kTile, batch), block(256);
+  p.kind = m <= 64 ? kMxLow : kMxMid;
+  split_k(m <= 64 ? tiles_of<Low>(batch, m, n) : tiles_of<Mid>(batch, m, n), 2 * kCUs, units, &p.pieces, &p.piece_units);
+  if (p.pieces > 1) p.bytes = static_cast<size_t>(p.pieces) * batch * m * n * sizeof(float);
+  return p;
+}
+
+template <class T>
+static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
+  const int tm = ceil_div(a.m, T::TM), tn = ceil_div(a.n, T::TN);
+  const dim3 grid(static_cast<uint32_t>(tm) * tn * a.batch * a.pieces), block(256);
   if (a.c_dtype == kF32) {
-    hipLaunchKernelGGL(mx4_gemm_kernel<kF32>, grid, block, 0, s, a);
+    hipLaunchKernelGGL((mx4_tile_gemm_kernel<T, kF32>), grid, block, 0, s, a, tm, tn);
   } else {
-    hipLaunchKernelGGL(mx4_gemm_kernel<kBF16>, grid, block, 0, s, a);
+    hipLaunchKernelGGL((mx4_tile_gemm_kernel<T, kBF16>), grid, block, 0, s, a, tm, tn);
+  }
+}
+
+template <int NT, int NW>
+static void launch_few(const Mx4GemmArgs& a, hipStream_t s) {
+  const dim3 grid(ceil_div(a.n, 16 * NT), 1, a.batch), block(64 * NW);
+  if (a.c_dtype == kF32) {
+    hipLaunchKernelGGL((mx4_few_rows_kernel<NT, NW, kF32>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((mx4_few_rows_kernel<NT, NW, kBF16>), grid, block, 0, s, a);
+  }
+}
+
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, Mx4Kind kind, hipStream_t s) {
+  switch (kind) {
+    case kMxBig: launch_tiles<Big>(a, s); break;
+    case kMxMid: launch_tiles<Mid>(a, s); break;
+    case kMxLow: launch_tiles<Low>(a, s); break;
+    default: launch_few<1, 8>(a, s); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_join(const Mx4GemmArgs& a, hipStream_t s) {
+  const int64_t blocks = (static_cast<int64_t>(a.m) * a.n + 1023) / 1024;
+  const dim3 grid(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 1, a.batch), block(256);
+  if (a.c_dtype == kF32) {
+    hipLaunchKernelGGL(mx4_join_kernel<kF32>, grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL(mx4_join_kernel<kBF16>, grid, block, 0, s, a);
   }
   return hipGetLastError();
 }
