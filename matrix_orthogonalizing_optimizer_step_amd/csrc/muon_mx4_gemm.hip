@@ -56,6 +56,7 @@ struct Tile {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = 4 / WM_;
   static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
   static constexpr int kLoads = TM / 64 + TN / 64 + 2;  // per wave and slab: codes, and scales of A and B
+  static constexpr int kAfter = kLoads / 3;             // of them, right behind the barrier
   struct Stage {
     uint4 code[(TM + TN) * 4];   // A rows, then B rows, 4 slots each
     uint32_t scale[TM + TN];
@@ -81,24 +82,43 @@ struct Source {
   uint32_t rows;    // rows of the matrix
 };
 
-// This wave's ROWS (a multiple of 16) rows of unit u of one operand, to place `at`
-// of the stage.  u may lie behind the last unit and rows behind the last row:
-// such addresses are behind the buffer's end (zeros) or in the next unit's rows,
-// and what they give enters no stored element.
-template <int ROWS, class Stage>
-__device__ __forceinline__ void load_operand(Stage& st, int at, const Source& src, uint32_t u, int lane, int vcode) {
-  const uint32_t line = u * src.rows + src.row;
-  const int so = __builtin_amdgcn_readfirstlane(static_cast<int>(line * 64u));
-  lds_ptr_t dst = (lds_ptr_t)(st.code + at * 4);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 0, 0);
-  if constexpr (ROWS > 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 1024, 0);
-  if constexpr (ROWS > 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 2048, 0);
-  if constexpr (ROWS > 48) __builtin_amdgcn_raw_ptr_buffer_load_lds(src.code, dst, 16, vcode, so, 3072, 0);
-  static_assert(ROWS <= 64, "one scale word per lane");
-  lds_ptr_t sd = (lds_ptr_t)(st.scale + at);
-  if (ROWS == 64 || lane < ROWS)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.scale, sd, 4, lane * 4,
-                                             __builtin_amdgcn_readfirstlane(static_cast<int>(line * 4u)), 0, 0);
+// Loads FIRST .. LAST - 1 of the T::kLoads that bring this wave's share of unit u
+// into a stage: the codes of A and of B, 16 rows each, and the scales of A and
+// of B.  u may lie behind the last unit and rows behind the last row: such
+// addresses are behind the buffer's end (zeros) or in the next unit's rows, and
+// what they give enters no stored element.
+template <class T, int FIRST, int LAST>
+__device__ __forceinline__ void load_unit(typename T::Stage& st, const Source& A, const Source& B, uint32_t u, int wave,
+                                          int lane, int vcode) {
+  constexpr int RA = T::TM / 4, RB = T::TN / 4;  // rows of this wave
+  const uint32_t la = u * A.rows + A.row, lb = u * B.rows + B.row;
+  const int soa = __builtin_amdgcn_readfirstlane(static_cast<int>(la * 64u));
+  const int sob = __builtin_amdgcn_readfirstlane(static_cast<int>(lb * 64u));
+  lds_ptr_t da = (lds_ptr_t)(st.code + wave * RA * 4), db = (lds_ptr_t)(st.code + (T::TM + wave * RB) * 4);
+#define MX4_LOAD(N, R, SRC, DST, SO, OFF)                                        \
+  if constexpr (FIRST <= (N) && (N) < LAST && (OFF) < (R) * 64)                  \
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(SRC.code, DST, 16, vcode, SO, OFF, 0)
+  constexpr int NA = RA / 16, NB = RB / 16;
+  MX4_LOAD(0, RA, A, da, soa, 0);
+  MX4_LOAD(1, RA, A, da, soa, 1024);
+  MX4_LOAD(2, RA, A, da, soa, 2048);
+  MX4_LOAD(3, RA, A, da, soa, 3072);
+  MX4_LOAD(NA, RB, B, db, sob, 0);
+  MX4_LOAD(NA + 1, RB, B, db, sob, 1024);
+  MX4_LOAD(NA + 2, RB, B, db, sob, 2048);
+  MX4_LOAD(NA + 3, RB, B, db, sob, 3072);
+#undef MX4_LOAD
+  static_assert(RA <= 64 && RB <= 64 && NA + NB + 2 == T::kLoads, "loads of a unit");
+  if constexpr (FIRST <= NA + NB && NA + NB < LAST) {
+    if (RA == 64 || lane < RA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(A.scale, (lds_ptr_t)(st.scale + wave * RA), 4, lane * 4,
+                                               __builtin_amdgcn_readfirstlane(static_cast<int>(la * 4u)), 0, 0);
+  }
+  if constexpr (FIRST <= NA + NB + 1 && NA + NB + 1 < LAST) {
+    if (RB == 64 || lane < RB)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(B.scale, (lds_ptr_t)(st.scale + T::TM + wave * RB), 4, lane * 4,
+                                               __builtin_amdgcn_readfirstlane(static_cast<int>(lb * 4u)), 0, 0);
+  }
 }
 
 // The 32-row fragments of k-step s from row `first` of a stage on.
@@ -138,32 +158,46 @@ __device__ __forceinline__ void mfmas(f32x16_t (&acc)[T::FN][T::FM], const Frags
 }
 
 // One slab from stage `cur`; fragments of its first step are in f0, its scales
-// in w.  Ends with those of the next slab (stage `nxt`) there.
+// in w.  Ends with those of the next slab (stage `nxt`) there.  The loads of the
+// slab three ahead go into `prv`, the stage of the slab before, spread over the
+// MFMAs (a burst of them would hold up the wave, which issues in order): the
+// first kAfter were issued behind the last barrier.
 template <class T>
 __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0, ScaleWords<T>& w,
-                                     typename T::Stage& cur, const typename T::Stage& nxt, const Source& A,
-                                     const Source& B, uint32_t u, int wave, int lane, int vcode, int ra, int rb) {
-  constexpr int FM = T::FM, FN = T::FN;
+                                     typename T::Stage& prv, typename T::Stage& cur, const typename T::Stage& nxt,
+                                     const Source& A, const Source& B, uint32_t u, int wave, int lane, int vcode,
+                                     int ra, int rb) {
+  constexpr int FM = T::FM, FN = T::FN, kMid = T::kAfter + (T::kLoads - T::kAfter) * 2 / 3;
   Frags<T> f1;
   read_frag<FN>(f1.b, cur, rb, lane, 1);
   read_frag<FM>(f1.a, cur, ra, lane, 1);
+  load_unit<T, T::kAfter, kMid>(prv, A, B, u + kStages - 1, wave, lane, vcode);
   mfmas<T, 0, 0, FM>(acc, f0, w);
   if constexpr (FM * FN >= FM + FN) {
 #pragma unroll
     for (int g = 0; g < FM + FN; ++g) {
       __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, FM * FN / (FM + FN), 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
     }
   }
   __builtin_amdgcn_sched_barrier(0);
+  load_unit<T, kMid, T::kLoads>(prv, A, B, u + kStages - 1, wave, lane, vcode);
   mfmas<T, 1, 0, FM / 2>(acc, f1, w);
+  if constexpr (FM * FN >= FM + FN) {
+#pragma unroll
+    for (int g = 0; g < T::kLoads - kMid; ++g) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, FM * FN / 2 / (T::kLoads - kMid), 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
   // this wave's part of the next slab has landed (two slabs stay in flight), and
   // all its reads of this one are done
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kLoads, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  load_operand<T::TM / 4>(cur, wave * (T::TM / 4), A, u + kStages, lane, vcode);
-  load_operand<T::TN / 4>(cur, T::TM + wave * (T::TN / 4), B, u + kStages, lane, vcode);
+  load_unit<T, 0, T::kAfter>(cur, A, B, u + kStages, wave, lane, vcode);
   ScaleWords<T> wn;
   read_frag<FN>(f0.b, nxt, rb, lane, 0);
   read_frag<FM>(f0.a, nxt, ra, lane, 0);
@@ -174,7 +208,7 @@ __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0
   for (int g = 0; g < FM * FN / 2; ++g) {
     __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
     __builtin_amdgcn_sched_group_barrier(kSchedDsRead, (2 * (FM + FN) + FM * FN / 2 - 1) / (FM * FN / 2), 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedVmem, (T::kLoads + FM * FN / 2 - 1) / (FM * FN / 2), 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedVmem, (T::kAfter + FM * FN / 2 - 1) / (FM * FN / 2), 0);
   }
   __builtin_amdgcn_sched_barrier(0);
   shift_scales<FN>(wn.b, lane);
@@ -249,13 +283,11 @@ __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kerne
   const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
   Stage* st[kStages] = {&s0, &s1, &s2, &s3};
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    load_operand<T::TM / 4>(*st[s], wave * (T::TM / 4), A, ub + s, lane, vcode);
-    load_operand<T::TN / 4>(*st[s], T::TM + wave * (T::TN / 4), B, ub + s, lane, vcode);
-  }
+  for (int s = 0; s < kStages - 1; ++s) load_unit<T, 0, T::kLoads>(*st[s], A, B, ub + s, wave, lane, vcode);
+  load_unit<T, 0, T::kAfter>(s3, A, B, ub + 3, wave, lane, vcode);
   const int ra = FM * 32 * (wave / T::WN), rb = T::TM + FN * 32 * (wave % T::WN);
   f32x16_t acc[FN][FM] = {};
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::kLoads, 0));
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kLoads + T::kAfter, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
   Frags<T> f;
@@ -268,14 +300,14 @@ __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kerne
   shift_scales<FM>(w.a, lane);
   int u = ub;
   for (; u + kStages <= ue; u += kStages) {
-    slab<T>(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s3, s0, A, B, u + 3, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s3, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s2, s3, s0, A, B, u + 3, wave, lane, vcode, ra, rb);
   }
-  if (u < ue) slab<T>(acc, f, w, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
-  if (u + 1 < ue) slab<T>(acc, f, w, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
-  if (u + 2 < ue) slab<T>(acc, f, w, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
+  if (u < ue) slab<T>(acc, f, w, s3, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
+  if (u + 1 < ue) slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
+  if (u + 2 < ue) slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
   // loads behind the last unit are still on their way into LDS: they end before
   // the block does
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
