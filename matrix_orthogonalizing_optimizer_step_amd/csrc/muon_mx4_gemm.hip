@@ -16,6 +16,7 @@ namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the operand format field of the MFMA
 
@@ -263,6 +264,95 @@ __device__ __forceinline__ void store_quad(void* C, int64_t at, const float (&v)
   }
 }
 
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+
+// A wave's accumulators to C, 32 rows at a time through its own LDS (`stage`).
+// With D = (B rows) x (A rows) lane l holds row l % 32 of C and, in registers 4 g
+// .. 4 g + 3, columns 8 g + 4 (l / 32) .. + 3 of an MFMA tile; read back, a lane
+// has 16 bytes of a row, so that a store fills whole 128 FN-byte (bf16: 64 FN)
+// pieces of rows.  LDS holds C's type, or fp32 where C is added to: C is rounded
+// once.  Measured on 8192x7168x3584 against 8-byte stores of 32 rows at a time
+// straight from the accumulators: MEASURED.
+template <class T, int DC, bool ADD>
+__device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
+                                           int m, int n, int lane) {
+  constexpr int kSize = DC == kF32 ? 4 : 2, kHeld = ADD || DC == kF32 ? 4 : 2;  // bytes of an element of C, in LDS
+  constexpr int kCols = 32 * T::FN, kPitch = kCols * kHeld / 16 + 1;            // uint4 of a row, one against conflicts
+  constexpr int kLanes = kCols * kSize / 16, kRows = 64 / kLanes;               // lanes of a row, rows of a store
+  static_assert(32 * kPitch * 16 <= sizeof(typename T::Stage) && kLanes <= 64, "staging");
+  const int row = lane & 31, half = lane >> 5, r0 = lane / kLanes, chunk = lane % kLanes;
+  constexpr int kElems = 16 / kSize;
+  const int jc = j + chunk * kElems;
+#pragma unroll
+  for (int y = 0; y < T::FM; ++y) {
+#pragma unroll
+    for (int x = 0; x < T::FN; ++x)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float v[4] = {acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+        const int col = 32 * x + 8 * g + 4 * half;
+        if constexpr (kHeld == 4) {
+          stage[row * kPitch + col / 4] = __builtin_bit_cast(uint4, make_float4(v[0], v[1], v[2], v[3]));
+        } else {
+          reinterpret_cast<uint2*>(stage)[row * kPitch * 2 + col / 4] =
+              make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+        }
+      }
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    asm volatile("" ::: "memory");  // the wave's own writes, in order with its reads
+#pragma unroll
+    for (int q = 0; q < 32 / kRows; ++q) {
+      const int r = q * kRows + r0, ir = i + 32 * y + r;
+      if (ir < m && jc < n) {
+        char* const p = static_cast<char*>(C) + (static_cast<int64_t>(ir) * n + jc) * kSize;
+        float f[kElems];
+        uint4 h;
+        if constexpr (kHeld == 4) {
+#pragma unroll
+          for (int e = 0; e < kElems; e += 4) {
+            const float4 t = __builtin_bit_cast(float4, stage[r * kPitch + (chunk * kElems + e) / 4]);
+            f[e] = t.x; f[e + 1] = t.y; f[e + 2] = t.z; f[e + 3] = t.w;
+          }
+        } else {
+          h = stage[r * kPitch + chunk];
+        }
+        if (jc + kElems <= n) {
+          if constexpr (kHeld == 4) {
+            if constexpr (ADD) {
+              const u32x4_t c = *reinterpret_cast<const u32x4_a2*>(p);
+#pragma unroll
+              for (int e = 0; e < kElems; ++e)
+                f[e] += DC == kF32 ? __uint_as_float(c[e & 3])
+                                   : bf16_to_f32(static_cast<uint16_t>((e & 1) ? c[e >> 1] >> 16 : c[e >> 1]));
+            }
+            if constexpr (DC == kF32) {
+              *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                                          __float_as_uint(f[2]), __float_as_uint(f[3])};
+            } else {
+              *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
+                                                          f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7])};
+            }
+          } else {
+            *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){h.x, h.y, h.z, h.w};
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kElems; ++e)
+            if (jc + e < n) {
+              if constexpr (kHeld == 4) {
+                store_from_f32(p, e, DC, ADD ? load_as_f32(p, e, DC) + f[e] : f[e]);
+              } else {
+                const uint32_t w = (&h.x)[e >> 1];
+                reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>((e & 1) ? w >> 16 : w);
+              }
+            }
+        }
+      }
+    }
+    asm volatile("" ::: "memory");  // the next rows' writes stay behind these reads
+  }
+}
+
 template <class T, int DC>
 __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kernel(Mx4GemmArgs a, int tm, int tn) {
   typedef typename T::Stage Stage;
@@ -308,32 +398,19 @@ __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kerne
   if (u < ue) slab<T>(acc, f, w, s3, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
   if (u + 1 < ue) slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
   if (u + 2 < ue) slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
-  // loads behind the last unit are still on their way into LDS: they end before
-  // the block does
+  // loads behind the last unit are still on their way into LDS: they end here,
+  // and so do all waves' reads, before LDS takes the results
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-  // D = (B rows) x (A rows): lane l holds row l % 32 of C and, in registers
-  // 4 g .. 4 g + 3, columns 8 g + 4 (l / 32) .. + 3
-  const bool split = a.pieces > 1;
-  void* C = split ? static_cast<void*>(a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n) : a.C[b];
-  const bool vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 || split ? 15u : 7u)) == 0;
-#pragma unroll
-  for (int y = 0; y < FM; ++y) {
-    const int i = i0 + ra + 32 * y + (lane & 31);
-    if (i < a.m) {
-#pragma unroll
-      for (int x = 0; x < FN; ++x)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int j = j0 + (rb - T::TM) + 32 * x + 8 * g + 4 * (lane >> 5);
-          const float v[4] = {acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
-          const int64_t at = static_cast<int64_t>(i) * a.n + j;
-          if (DC != kF32 && split) {
-            store_quad<kF32>(C, at, v, a.n - j, vec, 0);
-          } else {
-            store_quad<DC>(C, at, v, a.n - j, vec, split ? 0 : a.accumulate);
-          }
-        }
-    }
+  asm volatile("s_barrier" ::: "memory");
+  const int i = i0 + ra, j = j0 + rb - T::TM;  // this wave's first row and column
+  uint4* const stage = wave == 0 ? s0.code : wave == 1 ? s1.code : wave == 2 ? s2.code : s3.code;
+  if (a.pieces > 1) {
+    float* part = a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n;
+    store_tile<T, kF32, false>(part, acc, stage, i, j, a.m, a.n, lane);
+  } else if (a.accumulate) {
+    store_tile<T, DC, true>(a.C[b], acc, stage, i, j, a.m, a.n, lane);
+  } else {
+    store_tile<T, DC, false>(a.C[b], acc, stage, i, j, a.m, a.n, lane);
   }
 }
 
