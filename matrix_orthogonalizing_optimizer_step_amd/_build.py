@@ -1,7 +1,8 @@
-"""Compile the HIP sources of the Muon library into ``libmuon.so`` (gfx950).
+"""Compile the HIP sources of the Muon library into ``libmuon.so`` (gfx950) and
+the list-marshalling extension module ``_native.so``.
 
 ``python -m matrix_orthogonalizing_optimizer_step_amd._build`` builds in
-place; the shared library sits next to this file so it travels with the
+place; the shared libraries sit next to this file so they travel with the
 source tree.
 """
 from __future__ import annotations
@@ -66,12 +67,35 @@ def sanitizer_runtime() -> str:
     return out.stdout.strip()
 
 
+NATIVE_SOURCE = os.path.join(HERE, "native", "muon_native.cpp")
+NATIVE = os.path.join(HERE, "_native.so")
+
+
+def _native_command(out: str) -> list[str]:
+    """Host compiler line of the extension module (torch's headers and ABI, no device code)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-DTORCH_API_INCLUDE_EXTENSION_H",
+            *[f"-isystem{p}" for p in include_paths()], f"-isystem{sysconfig.get_paths()['include']}",
+            NATIVE_SOURCE, "-o", out, *[f"-L{p}" for p in library_paths()], "-lc10", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python"]
+
+
 def build(verbose: bool = False, csrc: str = CSRC, lib: str = LIB, defines=(), sanitize: bool = False) -> str:
     """Always recompiles (one process per source, in parallel); writes the
     library (default libmuon.so next to this file) atomically and returns its
     path.  ``csrc``, ``lib`` and ``defines`` (-D flags) build a variant;
     ``sanitize`` instruments the host code (see SANITIZE_COMPILE)."""
     objdir = tempfile.mkdtemp(prefix="muon_build_")
+    native = None
+    if lib == LIB:  # a variant of the library uses the same extension module
+        native = _run(_native_command(NATIVE + ".tmp"), verbose)
     try:
         objs, procs = [], []
         for src in SOURCES:
@@ -86,6 +110,9 @@ def build(verbose: bool = False, csrc: str = CSRC, lib: str = LIB, defines=(), s
         _finish(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *(SANITIZE_LINK if sanitize else []),
                       "-o", tmp, *objs], verbose), "link", verbose)
         os.replace(tmp, lib)
+        if native is not None:
+            _finish(native, os.path.basename(NATIVE_SOURCE), verbose)
+            os.replace(NATIVE + ".tmp", NATIVE)
     finally:
         shutil.rmtree(objdir, ignore_errors=True)
     return lib

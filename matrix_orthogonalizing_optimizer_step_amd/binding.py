@@ -6,11 +6,15 @@ functions keep the C names: ``ns_orthogonalize``, ``gram_ns_orthogonalize``
 and ``muon_step`` take lists of same-shape device tensors (one per matrix of
 the batch).  There is no fallback: if the library is missing or a call
 fails, an exception is raised.
+
+The entry points that take lists of parameters or one layer's matrices (the
+AdamW steps, the microscaled 4-bit code and product) go through the extension
+module ``_native``, which checks the tensors and calls the same C ABI at the
+cost of a launch.
 """
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
 from collections import OrderedDict
 from dataclasses import dataclass
@@ -63,11 +67,22 @@ class _GraspState(ctypes.Structure):
 
 
 _lib = None
+_native = None
+
+
+def _load_native():
+    """The extension module (raises ImportError if it has not been built)."""
+    try:
+        from . import _native as module
+    except ImportError as e:
+        raise ImportError(f"_native.so is missing or does not fit this PyTorch ({e}): build it with "
+                          "`python -m matrix_orthogonalizing_optimizer_step_amd._build`") from e
+    return module
 
 
 def load_library():
     """Load libmuon.so once; raises ImportError if it has not been built."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -119,6 +134,8 @@ def load_library():
         getattr(lib, name).argtypes = [i32, i32, i32, vp, vp, vp, vp]
         getattr(lib, name).restype = i32
     sizes, acfg = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_AdamWConfig)
+    names = ("muon_adamw_step", "muon_adamw8_step", "muon_mx4_quantize", "muon_mx4_dequantize",
+             "muon_mx4_workspace_size", "muon_mx4_matmul")
     lib.muon_adamw_config_init.argtypes = [acfg]
     lib.muon_adamw_config_init.restype = None
     lib.muon_adamw_step.argtypes = [i32, sizes, vp, i32, vp, vp, vp, i32, acfg, vp]
@@ -133,6 +150,10 @@ def load_library():
     lib.muon_mx4_workspace_size.restype = sz
     lib.muon_mx4_matmul.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
     lib.muon_mx4_matmul.restype = i32
+    native = _load_native()
+    native.bind_library({name: ctypes.cast(getattr(lib, name), vp).value for name in names},
+                        torch._C._cuda_getCurrentRawStream)
+    _native = native
     _lib = lib
     return lib
 
@@ -635,93 +656,23 @@ class AdamW8State:
         return decode(self.m_codes, self.m_scales), [r * r for r in decode(self.r_codes, self.r_scales)]
 
 
-_numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
-_get_device, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
-_dtype = operator.attrgetter("dtype")
+def _on_stream(stream, tensors):
+    """The context in which ``stream`` (a torch stream or a raw handle) is the current stream of the tensors' device."""
+    device = tensors[0].device
+    if getattr(stream, "device", device) != device:
+        raise ValueError("stream must be a stream of the tensors' device")
+    return torch.cuda.stream(_stream_obj(stream, device))
 
 
-def _list_of(tensors, name: str, sizes, device: int, dtypes):
-    """Data pointers of a list of contiguous device tensors that share one of
-    ``dtypes`` and have the given sizes."""
-    if len(tensors) != len(sizes):
-        raise ValueError(f"{name}: one tensor per tensor of W is needed")
-    types = set(map(_dtype, tensors))
-    if len(types) != 1 or not types <= dtypes:
-        raise ValueError(f"{name}: all tensors must share one dtype of {sorted(str(d) for d in dtypes)}")
-    if set(map(_get_device, tensors)) != {device}:
-        raise ValueError(f"{name}: all tensors must be on the device of W")
-    if tuple(map(_numel, tensors)) != sizes:
-        raise ValueError(f"{name}: wrong number of elements")
-    if not all(map(_contiguous, tensors)):
-        raise ValueError(f"{name}: tensors must be contiguous")
-    return tuple(map(_data_ptr, tensors))
-
-
-def _host_pointers(ptrs):
-    """A host array of device pointers (read by the library during the call)."""
-    return (ctypes.c_void_p * len(ptrs))(*ptrs)
-
-
-class _Same:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_same = _Same()
-
-
-def _on(index: int):
-    """The context in which device ``index`` is the current one."""
-    return _same if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-
-def _raw_stream(stream, index: int) -> int:
-    """The handle of ``stream`` (None = device ``index``'s current stream)."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-
-
-_W_TYPES, _F32, _F8 = {torch.float32, torch.bfloat16}, {torch.float32}, {torch.float8_e4m3fn}
-_G_TYPES = set(_DT)
-
-
-def _adamw_call(entry: str, W, lists, G, config, stream):
-    """Checks and call of both AdamW steps: ``lists`` = (name, tensors, sizes or None for W's, dtypes) of the state."""
-    lib = load_library()
-    if len(W) == 0:
-        raise ValueError("W: empty list")
-    sizes = tuple(map(_numel, W))
-    device = W[0].get_device()
-    if device < 0:
-        raise ValueError("W: tensors must be device tensors")
-    pw = _list_of(W, "W", sizes, device, _W_TYPES)
-    pg = _list_of(G, "G", sizes, device, _G_TYPES)
-    ps = [_list_of(t, name, n or sizes, device, types) for name, t, n, types in lists]
-    used = [p for q in (pw, pg, *ps) for p in q if p]
-    if len(set(used)) != len(used):
-        raise ValueError("W, G and the state must be tensors of their own: one of them is in the lists twice")
-    lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed = config
-    c = _AdamWConfig(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 0, None, None,
-                     int(seed) & 0xFFFFFFFF)
-    if isinstance(step, torch.Tensor):
-        if step.numel() != 1 or step.dtype != torch.int64 or step.get_device() != device:
-            raise ValueError("step: a tensor must be one int64 on the device of W")
-        c.step_dev = step.data_ptr()
-    else:
-        c.step = int(step)
-    if grad_scale is not None:
-        if not isinstance(grad_scale, torch.Tensor) or grad_scale.numel() != 1 or grad_scale.dtype != torch.float32 \
-                or grad_scale.get_device() != device:
-            raise ValueError("grad_scale must be None or one float32 on the device of W")
-        c.grad_scale = grad_scale.data_ptr()
-    arrays = [_host_pointers(p) for p in ps]  # held until the call returns
-    state = arrays if entry == "muon_adamw_step" else [ctypes.byref(_AdamW8State(*map(ctypes.addressof, arrays)))]
-    n = len(sizes)
-    with _on(device):
-        _check(getattr(lib, entry)(n, (ctypes.c_int64 * n)(*sizes), _host_pointers(pw), _DT[W[0].dtype], *state,
-                                   _host_pointers(pg), _DT[G[0].dtype], ctypes.byref(c), _raw_stream(stream, device)))
+def _call(entry: str, stream, tensors, *args):
+    """Calls an entry of the extension module on ``stream`` (None = the current stream of the tensors' device)."""
+    if _native is None:
+        load_library()
+    f = getattr(_native, entry)
+    if stream is None:
+        return f(*args)
+    with _on_stream(stream, tensors):
+        return f(*args)
 
 
 def adamw_step(W, M, V, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -732,19 +683,15 @@ def adamw_step(W, M, V, G, step, lr: float, beta1: float = 0.9, beta2: float = 0
     W: float32 or bfloat16, M and V: float32, G: float32, bfloat16 or float16 (one dtype per list).  ``step`` counts
     from 1; as a one-element int64 device tensor it is read by the kernel, so that a captured graph can advance it.
     ``grad_scale``: None or a one-element float32 device tensor the gradients are multiplied with."""
-    _adamw_call("muon_adamw_step", W, (("M", M, None, _F32), ("V", V, None, _F32)), G,
-                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, 0), stream)
+    _check(_call("adamw_step", stream, W, W, M, V, G, step, lr, beta1, beta2, eps, weight_decay, grad_scale))
 
 
 def adamw8_step(W, state: AdamW8State, G, step, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                 eps: float = 1e-8, weight_decay: float = 0.0, grad_scale=None, seed: int = 0, stream=None):
     """adamw_step with the moments in 8 bits: W and the state are updated in place.  ``seed`` with ``step`` fixes the
     random roundings of the second moment's codes."""
-    groups = tuple([(w.numel() + GRID - 1) // GRID for w in W])
-    _adamw_call("muon_adamw8_step", W,
-                (("m_codes", state.m_codes, None, _F8), ("m_scales", state.m_scales, groups, _F32),
-                 ("r_codes", state.r_codes, None, _F8), ("r_scales", state.r_scales, groups, _F32)), G,
-                (lr, beta1, beta2, eps, weight_decay, step, grad_scale, seed), stream)
+    _check(_call("adamw8_step", stream, W, W, state.m_codes, state.m_scales, state.r_codes, state.r_scales, G, step, lr,
+                 beta1, beta2, eps, weight_decay, grad_scale, seed & 0xFFFFFFFF))
 
 
 # ---------------------------------------------------------------------------
@@ -763,123 +710,58 @@ class MX4:
         return self.codes[0].shape[1]
 
     @classmethod
-    def empty(cls, batch: int, rows: int, cols: int, device, stream=None):
+    def empty(cls, batch: int, rows: int, cols: int, device):
         """Uninitialised buffers for the code of ``batch`` rows x cols matrices."""
         units = _nb(cols)
-        split = batch * units * rows * 64  # all codes first, so that every matrix's codes are 16-byte aligned
-        flat = _allocate((batch * units * rows * 68,), torch.uint8, device, stream)
-        codes = torch.as_strided(flat, (batch, units, rows, 64), (units * rows * 64, rows * 64, 64, 1))
-        scales = torch.as_strided(flat, (batch, units, rows, 4), (units * rows * 4, rows * 4, 4, 1), split)
-        return cls(list(codes.unbind(0)), list(scales.unbind(0)), int(cols))
-
-
-def _allocate(shape, dtype, device, stream):
-    """torch.empty whose memory belongs to ``stream`` (None = the current stream)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_stream_obj(stream, torch.device(device))):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _mx4_check(q, name: str):
-    """(batch, rows, cols, device index) of a code, and the data pointers of its codes and scales."""
-    if len(q.codes) == 0 or len(q.codes) != len(q.scales):
-        raise ValueError(f"{name}: codes and scales must hold one tensor per matrix")
-    shape, device, cols = tuple(q.codes[0].shape), q.codes[0].get_device(), q.cols
-    if len(shape) != 3 or cols < 1 or shape[0] != _nb(cols) or shape[1] < 1 or shape[2] != 64:
-        raise ValueError(f"{name}: codes must be (ceil(cols / 128), rows, 64)")
-    if device < 0:
-        raise ValueError(f"{name}: codes must be device tensors")
-    pointers = []
-    for tensors, want, align in ((q.codes, shape, 16), (q.scales, (shape[0], shape[1], 4), 4)):
-        ptrs = []
-        for t in tensors:
-            p = t.data_ptr()
-            if t.dtype != torch.uint8 or t.get_device() != device or t.shape != want:
-                raise ValueError(f"{name}: all codes and scales must be uint8 of one shape and device")
-            if not t.is_contiguous() or p % align:
-                raise ValueError(f"{name}: codes and scales must be contiguous, codes 16-byte and scales 4-byte aligned")
-            ptrs.append(p)
-        pointers.append(ptrs)
-    return (len(q.codes), shape[1], cols, device), pointers
-
-
-def _matrices(tensors, name: str):
-    """_batch, with the device index and the data pointers: ((batch, rows, cols, device), dtype, pointers)."""
-    rows, cols, dt = _batch(tensors, name)
-    return (len(tensors), rows, cols, tensors[0].get_device()), dt, [t.data_ptr() for t in tensors]
+        return cls([torch.empty(units, rows, 64, dtype=torch.uint8, device=device) for _ in range(batch)],
+                   [torch.empty(units, rows, 4, dtype=torch.uint8, device=device) for _ in range(batch)], int(cols))
 
 
 def mx4_quantize(X, transpose=False, out=None, stream=None):
     """The microscaled 4-bit code of the matrices ``X`` (float32, bfloat16 or float16) along their rows, or with
     ``transpose=True`` that of their transposes (along the columns), or with ``transpose="both"`` the pair of both from
     one read.  ``out``: an MX4 (or a pair) of the right shape to write into."""
-    lib = load_library()
-    (batch, rows, cols, device), dt, px = _matrices(X, "X")
-    if transpose not in (False, True, "both"):
+    both = transpose == "both"
+    if not both and transpose is not False and transpose is not True:
         raise ValueError('transpose must be False, True or "both"')
-    want = ((rows, cols),) if transpose is False else ((cols, rows),) if transpose is True else ((rows, cols), (cols, rows))
-    made = [MX4.empty(batch, r, c, X[0].device, stream) for r, c in want] if out is None else \
-        list(out) if transpose == "both" else [out]
-    checked = [_mx4_check(q, "out") for q in made]
-    if [c[0] for c in checked] != [(batch, r, c, device) for r, c in want]:
-        raise ValueError("out must have the shape, batch and device of the result")
-    none = [None, None]
-    along = [_host_pointers(p) for p in checked[0][1]] if transpose is not True else none
-    across = [_host_pointers(p) for p in checked[-1][1]] if transpose is not False else none
-    with _on(device):
-        _check(lib.muon_mx4_quantize(batch, rows, cols, _host_pointers(px), dt, *along, *across,
-                                     _raw_stream(stream, device)))
+    given = None
+    if out is not None:
+        given = [(q.codes, q.scales, q.cols) for q in (out if both else (out,))]
+        if len(given) != (2 if both else 1):
+            raise ValueError("out must be a pair of codes")
+    status, made = _call("mx4_quantize", stream, X, X, transpose is not True, transpose is not False, given)
+    if status:
+        _check(status)
     if out is not None:
         return out
-    return tuple(made) if transpose == "both" else made[0]
+    if both:
+        rows, cols = X[0].shape
+        return MX4(*made[0], cols), MX4(*made[1], rows)
+    return MX4(*made[0], X[0].shape[0 if transpose else 1])
 
 
 def mx4_dequantize(q: MX4, dtype=torch.float32, out=None, stream=None):
-    """The values of a code as float32 or bfloat16 matrices."""
-    lib = load_library()
-    shape, (pc, ps) = _mx4_check(q, "q")
-    batch, rows, cols, device = shape
-    if dtype not in _DT:
-        raise ValueError("dtype must be float32 or bfloat16")
-    Y = list(_allocate((batch, rows, cols), dtype, q.codes[0].device, stream).unbind(0)) if out is None else out
-    got, dt, py = _matrices(Y, "out")
-    if got != shape or dt != _DT[dtype]:
-        raise ValueError("out must have the shape, batch, dtype and device of the result")
-    with _on(device):
-        _check(lib.muon_mx4_dequantize(batch, rows, cols, _host_pointers(pc), _host_pointers(ps), _host_pointers(py), dt,
-                                       _raw_stream(stream, device)))
+    """The values of a code as float32 or bfloat16 matrices (``out``: matrices to write into, of either type)."""
+    status, Y = _call("mx4_dequantize", stream, q.codes, q.codes, q.scales, q.cols, dtype, out)
+    if status:
+        _check(status)
     return Y
 
 
 def mx4_matmul(A: MX4, B: MX4, dtype=torch.bfloat16, out=None, accumulate: bool = False, workspace=None, stream=None):
-    """C = A B^T of every pair of coded matrices (A: m x k, B: n x k), as float32 or bfloat16 m x n matrices; with
-    ``accumulate`` C += A B^T into ``out``."""
-    lib = load_library()
-    (batch, m, k, device), pa = _mx4_check(A, "A")
-    (b2, n, k2, device2), pb = _mx4_check(B, "B")
-    if b2 != batch or k2 != k or device2 != device:
-        raise ValueError("A and B must share the batch, the row length and the device")
-    if accumulate and out is None:
-        raise ValueError("accumulate needs out")
-    if out is None:
-        if dtype not in _DT:
-            raise ValueError("dtype must be float32 or bfloat16")
-        C = list(_allocate((batch, m, n), dtype, A.codes[0].device, stream).unbind(0))
-    else:
-        C = out
-    got, cdt, pc = _matrices(C, "out")
-    if got != (batch, m, n, device):
-        raise ValueError("out must have one m x n matrix per pair, on the same device")
-    need = lib.muon_mx4_workspace_size(batch, m, n, k)
-    if need == 0:
-        raise MuonError(1, "invalid arguments for the workspace size")
-    with _on(device):
-        if workspace is None:
-            # from the allocator at every call: its memory is reused in the stream's order, and under capture it
-            # belongs to the graph, so two graphs never share it
-            workspace = _allocate((need,), torch.uint8, A.codes[0].device, stream)
-        _check(lib.muon_mx4_matmul(batch, m, n, k, *map(_host_pointers, (*pa, *pb, pc)), cdt, 1 if accumulate else 0,
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _raw_stream(stream, device)))
+    """C = A B^T of every pair of coded matrices (A: m x k, B: n x k), as new float32 or bfloat16 m x n matrices or into
+    ``out``; with ``accumulate`` C += A B^T there.  ``workspace``: a device tensor of muon_mx4_workspace_size() bytes;
+    without one the call takes its scratch from torch's allocator."""
+    status, C = _call("mx4_matmul", stream, A.codes, A.codes, A.scales, B.codes, B.scales, A.cols, B.cols, dtype, out,
+                      accumulate, workspace)
+    if status:
+        _check(status)
     return C
+
+
+def mx4_workspace_size(batch: int, m: int, n: int, k: int) -> int:
+    """Bytes of workspace mx4_matmul needs (see muon_mx4_workspace_size in include/muon.h)."""
+    n = load_library().muon_mx4_workspace_size(batch, m, n, k)
+    if n == 0:
+        raise MuonError(1, "invalid arguments for the workspace size")
+    return int(n)

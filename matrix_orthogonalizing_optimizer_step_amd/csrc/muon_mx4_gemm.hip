@@ -272,7 +272,7 @@ typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 // has 16 bytes of a row, so that a store fills whole 128 FN-byte (bf16: 64 FN)
 // pieces of rows.  LDS holds C's type, or fp32 where C is added to: C is rounded
 // once.  Measured on 8192x7168x3584 against 8-byte stores of 32 rows at a time
-// straight from the accumulators: MEASURED.
+// straight from the accumulators: 138 -> 122 us.
 template <class T, int DC, bool ADD>
 __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
                                            int m, int n, int lane) {
@@ -451,7 +451,7 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4GemmArgs a) {
 // behind the last one repeat it and are not stored.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;
-constexpr int kUnitsAhead = 4;
+constexpr int kUnitsAhead = 2;
 
 template <int NT, int NW, int DC>
 __global__ __launch_bounds__(64 * NW) void mx4_few_rows_kernel(Mx4GemmArgs a) {
@@ -523,38 +523,56 @@ typedef Tile<64, 128, 1> Low;
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Split of a product along k when its tiles do not fill the compute units:
-// pieces of at least kMinPiece units, as many as give every block slot one.
-constexpr int kMinPiece = 4;
-
-void split_k(int64_t tiles, int slots, int units, int* pieces, int* piece_units) {
-  int p = static_cast<int>(slots / tiles);
-  const int most = units / kMinPiece;
-  p = p < most ? p : most;
-  p = p < 1 ? 1 : p;
-  *piece_units = ceil_div(units, p);
-  *pieces = ceil_div(units, *piece_units);
-}
-
 template <class T>
 int64_t tiles_of(int batch, int m, int n) {
   return static_cast<int64_t>(ceil_div(m, T::TM)) * ceil_div(n, T::TN) * batch;
 }
 
+// Pieces along k of a product in 64 x 128 tiles that leave compute units idle:
+// the fewest microseconds of a slab a unit (measured 0.26, one block on a compute
+// unit) plus, for more than one piece, the joining launch (4.5) and the partial
+// sums' way through memory (8 bytes an element and piece at 6 TB/s).
+void split_k(int64_t tiles, int units, double elements, Mx4Plan* p) {
+  constexpr int kMinUnits = 4;  // of a piece
+  double best = 0.0;
+  for (int q = 1; q * tiles <= kCUs && (q == 1 || units / q >= kMinUnits); ++q) {
+    const double us = ceil_div(units, q) * 0.26 + (q > 1 ? 4.5 + q * elements * 8.0 / 6e6 : 0.0);
+    if (q == 1 || us < best) {
+      best = us;
+      p->piece_units = ceil_div(units, q);
+      p->pieces = ceil_div(units, p->piece_units);
+    }
+  }
+}
+
 }  // namespace
 
+// Which kernel, by the tiles there are for 256 compute units (times on bf16 C):
+//   at most 16 rows of A   B's codes are read once, straight into registers.
+//                          16x18944x3584: 10.1 us, 64 x 128 tiles 11.3
+//   256 x 256 tiles        where their last round leaves at most a third of the
+//                          compute units idle: 4096x4096x2048 (256 tiles) 29 us,
+//                          128 x 128 36; 2048x4096x8192 (128 tiles) 49 and 45
+//   64 x 128 tiles         for at most 384 of them, split along k if they are
+//                          few: 512x3584x3584 (224) 11.0 us, 128 x 128 13.4;
+//                          256x18944x3584 (592) 23.7 and 21.0
+//   128 x 128 tiles        otherwise.
 Mx4Plan mx4_plan(int batch, int m, int n, int k) {
-  Mx4Plan p{kMxFewRows, 1, 0, 0};
   const int units = static_cast<int>(mx4_units(k));
-  p.piece_units = units;
+  Mx4Plan p{kMxFewRows, 1, units, 0};
   if (m <= kFewRows) return p;
-  if (tiles_of<Big>(batch, m, n) * 4 >= kCUs * 3) {
+  const int64_t big = tiles_of<Big>(batch, m, n), low = tiles_of<Low>(batch, m, n);
+  const int64_t rounds = (big + kCUs - 1) / kCUs;
+  if (big * 3 >= rounds * kCUs * 2) {
     p.kind = kMxBig;
-    return p;
+  } else if (low * 2 <= kCUs * 3) {
+    p.kind = kMxLow;
+    const double elements = static_cast<double>(batch) * m * n;
+    split_k(low, units, elements, &p);
+    if (p.pieces > 1) p.bytes = static_cast<size_t>(p.pieces) * batch * m * n * sizeof(float);
+  } else {
+    p.kind = kMxMid;
   }
-  p.kind = m <= 64 ? kMxLow : kMxMid;
-  split_k(m <= 64 ? tiles_of<Low>(batch, m, n) : tiles_of<Mid>(batch, m, n), 2 * kCUs, units, &p.pieces, &p.piece_units);
-  if (p.pieces > 1) p.bytes = static_cast<size_t>(p.pieces) * batch * m * n * sizeof(float);
   return p;
 }
 
@@ -584,7 +602,15 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, Mx4Kind kind, hipStream_t s) {
     case kMxBig: launch_tiles<Big>(a, s); break;
     case kMxMid: launch_tiles<Mid>(a, s); break;
     case kMxLow: launch_tiles<Low>(a, s); break;
-    default: launch_few<1, 8>(a, s); break;
+    default:
+      // 16 waves a block where 8 leave compute units idle or with few loads in
+      // flight and k is long: 1x3584x18944 10.1 -> 8.0 us, 1x18944x3584 8.2 -> 9.3
+      if (a.units >= 64 && ceil_div(a.n, 16) * a.batch <= kCUs) {
+        launch_few<1, 16>(a, s);
+      } else {
+        launch_few<1, 8>(a, s);
+      }
+      break;
   }
   return hipGetLastError();
 }

@@ -145,18 +145,10 @@ def test_adamw_binding_refusals():
         mu.adamw_step([], [], [], [], 1, 1e-3)
     with pytest.raises(ValueError, match="device tensors"):
         mu.adamw_step([z], [z], [z], [z], 1, 1e-3)
-    with pytest.raises(ValueError, match="one tensor per tensor"):
-        bd._list_of([z, z], "G", (4,), -1, {torch.float32})
-    with pytest.raises(ValueError, match="dtype"):
-        bd._list_of([z, z.double()], "G", (4, 4), -1, {torch.float32})
-    with pytest.raises(ValueError, match="dtype"):
-        bd._list_of([z.half()], "M", (4,), -1, {torch.float32})
-    with pytest.raises(ValueError, match="device of W"):
-        bd._list_of([z], "G", (4,), 0, {torch.float32})
-    with pytest.raises(ValueError, match="number of elements"):
-        bd._list_of([z], "G", (5,), -1, {torch.float32})
-    with pytest.raises(ValueError, match="contiguous"):
-        bd._list_of([torch.zeros(4, 4).t()], "G", (16,), -1, {torch.float32})
+    with pytest.raises(ValueError, match="list of tensors"):
+        mu.adamw_step(z, z, z, z, 1, 1e-3)
+    with pytest.raises(ValueError, match="list of tensors"):
+        mu.adamw_step([1.0], [z], [z], [z], 1, 1e-3)
 
 
 def test_mx4_refusals_before_any_device_work():

@@ -136,11 +136,11 @@ def test_adamw_zero_gradient_and_state():
 def test_adamw_refuses_a_tensor_twice():
     a, b = torch.zeros(8, device=DEV), torch.zeros(8, device=DEV)
     z = lambda: torch.zeros(8, device=DEV)  # noqa: E731
-    with pytest.raises(ValueError, match="twice"):
+    with pytest.raises(ValueError, match="overlaps"):
         mu.adamw_step([a, a], [z(), z()], [z(), z()], [z(), z()], 1, 1e-3)
-    with pytest.raises(ValueError, match="twice"):
+    with pytest.raises(ValueError, match="overlaps"):
         mu.adamw_step([a], [b], [b], [z()], 1, 1e-3)
-    with pytest.raises(ValueError, match="twice"):
+    with pytest.raises(ValueError, match="overlaps"):
         mu.adamw_step([a], [z()], [z()], [a], 1, 1e-3)
     with pytest.raises(ValueError, match="step"):
         mu.adamw_step([a], [z()], [z()], [z()], torch.ones(2, dtype=torch.int64, device=DEV), 1e-3)
@@ -149,6 +149,32 @@ def test_adamw_refuses_a_tensor_twice():
     with pytest.raises(mu.MuonError):
         mu.adamw_step([a], [z()], [z()], [z()], 0, 1e-3)
     assert not a.any()
+
+
+def test_adamw_checks_every_list():
+    z = lambda n=8, dt=torch.float32: torch.zeros(n, dtype=dt, device=DEV)  # noqa: E731
+    call = lambda W=None, M=None, V=None, G=None: mu.adamw_step(  # noqa: E731
+        W or [z(), z(5)], M or [z(), z(5)], V or [z(), z(5)], G or [z(), z(5)], 1, 1e-3)
+    call()
+    for kw, what in [(dict(G=[z()]), "one tensor per tensor"), (dict(M=[z()]), "one tensor per tensor"),
+                     (dict(W=[z(), z(5, torch.bfloat16)]), "dtype"), (dict(G=[z(), z(5, torch.float16)]), "dtype"),
+                     (dict(M=[z(8, torch.bfloat16), z(5, torch.bfloat16)]), "dtype"),
+                     (dict(W=[z(8, torch.float16), z(5, torch.float16)]), "dtype"),
+                     (dict(G=[z(8, torch.float64), z(5, torch.float64)]), "dtype"), (dict(V=[z(), z(6)]), "number"),
+                     (dict(G=[z(), torch.zeros(5)]), "device of W"), (dict(G=[z(), z(10)[::2]]), "contiguous")]:
+        with pytest.raises(ValueError, match=what):
+            call(**kw)
+    both = z(16)
+    with pytest.raises(ValueError, match="overlaps"):  # views that share elements
+        call(W=[both[:8], both[7:12]])
+    G = [z(), z(5)]
+    call(W=[both[:8], both[8:13]], G=G)                # neighbours, and gradients read only
+    same = z()
+    mu.adamw_step([z(), z()], [z(), z()], [z(), z()], [same, same], 1, 1e-3)
+    s = mu.AdamW8State.zeros([z(), z(300)])
+    s.m_scales[1] = z(2)
+    with pytest.raises(ValueError, match="number"):
+        mu.adamw8_step([z(), z(300)], s, [z(), z(300)], 1, 1e-3)
 
 
 # --- 8-bit moments -------------------------------------------------------------------------------------------------

@@ -230,7 +230,8 @@ def test_product_of_a_matrix_with_itself():
 
 def test_product_is_reproducible_with_a_given_workspace():
     A, B = random_code(1, 300, 5000, 17), random_code(1, 260, 5000, 18)
-    need = mu.load_library().muon_mx4_workspace_size(1, 300, 260, 5000)
+    need = mu.mx4_workspace_size(1, 300, 260, 5000)
+    assert need > 256  # split along k
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # contents on entry are ignored
     a = mu.mx4_matmul(A, B, torch.float32, workspace=ws)[0]
     b = mu.mx4_matmul(A, B, torch.float32)[0]
@@ -263,6 +264,17 @@ def test_mx4_refusals_on_the_device():
     codes = torch.zeros(1 * 4 * 64 + 8, dtype=torch.uint8, device=DEV)[8:].view(1, 4, 64)
     with pytest.raises(ValueError, match="aligned"):
         mu.mx4_matmul(mu.MX4([codes], A.scales, 100), B)
+    two, twoB = random_code(2, 4, 100, 19), random_code(2, 5, 100, 20)
+    C = torch.zeros(4, 5, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        mu.mx4_matmul(two, twoB, out=[C, C])
+    with pytest.raises(ValueError, match="overlaps"):
+        q = mu.MX4.empty(1, 4, 100, DEV)
+        mu.mx4_quantize([torch.zeros(4, 100, device=DEV)] * 2, out=mu.MX4(q.codes * 2, q.scales * 2, 100))
+    with pytest.raises(ValueError, match="stream"):
+        mu.mx4_matmul(A, B, stream=type("S", (), {"cuda_stream": 0, "device": torch.device("cuda:1")})())
+    with pytest.raises(ValueError, match="empty"):
+        mu.mx4_quantize([torch.zeros(0, 5, device=DEV)])
 
 
 # --- graphs, streams -----------------------------------------------------------------------------------------------
