@@ -31,6 +31,9 @@ __device__ __forceinline__ float half_of(uint32_t w, int upper) {
 // Scale as the converters take it: its exponent field is the scale byte.
 __device__ __forceinline__ float scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// (A macro: a template parameter would drop the pointer type's alignment.)
+#define LOAD_VEC(p) (NT ? __builtin_nontemporal_load(p) : *(p))
+
 // Two e2m1 codes of (lo, hi) / scale into byte S of w (nearest even, saturating).
 template <int S>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, float lo, float hi, float scale) {
@@ -57,85 +60,86 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t x) {  // of non-negative fl
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;  // quad permutations, reversal within 8 lanes
 
 // ---------------------------------------------------------------------------
-// Codes along rows: a thread takes 8 consecutive elements, 4 threads a block of
-// 32, 16 a unit; a wave takes 4 rows, a block 16, and kUnitsPerThread units one
-// after the other with all loads out first.
+// Rows of X to or from rows of units: a thread takes 16 bytes of a row of X (8
+// 16-bit elements, 4 fp32), so that a wave's access is 1 KB without gaps, for
+// kUnitsPerThread units one after the other with all loads out first.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
-constexpr int kRowsPerBlock = 16, kUnitsPerThread = 4;
+constexpr int kUnitsPerThread = 4;
 
 template <int D>
-struct Raw8 {
-  u32x4_t v[D == kF32 ? 2 : 1];
+struct Span {
+  static constexpr int kElems = D == kF32 ? 4 : 8;  // of a thread and unit
+  static constexpr int kLanes = kMxUnit / kElems;   // threads of a row
+  static constexpr int kRows = kThreads / kLanes;   // rows of a block
 };
 
-template <int D>
-__device__ __forceinline__ Raw8<D> load8(const void* X, int64_t at, int left) {
-  Raw8<D> r;
-  if (left >= 8) {
+template <int D, bool NT>
+__device__ __forceinline__ u32x4_t load_span(const void* X, int64_t at, int left) {
+  constexpr int E = Span<D>::kElems;
+  if (left >= E) {
     if constexpr (D == kF32) {
-      const u32x4_a4* p = reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at);
-      r.v[0] = p[0];
-      r.v[1] = p[1];
+      return LOAD_VEC(reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at));
     } else {
-      r.v[0] = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(X) + at);
+      return LOAD_VEC(reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(X) + at));
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < (D == kF32 ? 2 : 1); ++e) r.v[e] = (u32x4_t){0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) {
-        if constexpr (D == kF32) {
-          r.v[e >> 2][e & 3] = static_cast<const uint32_t*>(X)[at + e];
-        } else {
-          r.v[0][e >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(X)[at + e]) << (16 * (e & 1));
-        }
-      }
   }
+  u32x4_t r = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (e < left) {
+      if constexpr (D == kF32) {
+        r[e] = static_cast<const uint32_t*>(X)[at + e];
+      } else {
+        r[e >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(X)[at + e]) << (16 * (e & 1));
+      }
+    }
   return r;
 }
 
-template <int D>
-__device__ __forceinline__ void expand8(const Raw8<D>& r, float (&x)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (D == kF32) {
-      x[e] = __uint_as_float(r.v[e >> 2][e & 3]);
-    } else {
-      x[e] = half_of<D>(r.v[0][e >> 1], e & 1);
-    }
-  }
-}
-
-template <int D>
+// Codes along rows.  A block of 32 is that of 4 (fp32: 8) neighbouring threads.
+template <int D, bool NT>
 __global__ __launch_bounds__(kThreads) void mx4_rows_kernel(Mx4QuantArgs a, int units) {
-  const int b = blockIdx.z, o = threadIdx.x & 15;
-  const int r = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x >> 4);
-  if (r >= a.rows) return;  // all 16 threads of a row together
+  typedef Span<D> S;
+  constexpr int E = S::kElems;
+  const int b = blockIdx.z, o = threadIdx.x % S::kLanes;
+  const int r = blockIdx.x * S::kRows + static_cast<int>(threadIdx.x) / S::kLanes;
+  if (r >= a.rows) return;  // all threads of a row together
   const int u0 = blockIdx.y * kUnitsPerThread;
   const void* X = a.X[b];
-  uint32_t* codes = static_cast<uint32_t*>(a.codes[b]);
+  uint8_t* codes = static_cast<uint8_t*>(a.codes[b]);
   uint8_t* scales = static_cast<uint8_t*>(a.scales[b]);
-  Raw8<D> raw[kUnitsPerThread];
+  u32x4_t raw[kUnitsPerThread];
 #pragma unroll
   for (int k = 0; k < kUnitsPerThread; ++k) {
-    const int c = (u0 + k) * kMxUnit + 8 * o;
-    raw[k] = load8<D>(X, static_cast<int64_t>(r) * a.cols + c, a.cols - c);
+    const int c = (u0 + k) * kMxUnit + E * o;
+    raw[k] = load_span<D, NT>(X, static_cast<int64_t>(r) * a.cols + c, a.cols - c);
   }
 #pragma unroll
   for (int k = 0; k < kUnitsPerThread; ++k) {
-    float x[8];
-    expand8<D>(raw[k], x);
-    uint32_t top = __float_as_uint(top3(top3(x[0], x[1], x[2]), x[3], top3(top3(x[4], x[5], x[6]), x[7], 0.0f)));
+    float x[8] = {};
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = D == kF32 ? __uint_as_float(raw[k][e & 3]) : half_of<D>(raw[k][e >> 1], e & 1);
+    float most = top3(top3(x[0], x[1], x[2]), x[3], 0.0f);
+    if constexpr (E == 8) most = top3(top3(x[4], x[5], x[6]), x[7], most);
+    uint32_t top = __float_as_uint(most);
     top = dpp_max<kXor1>(top);
     top = dpp_max<kXor2>(top);
+    if constexpr (E == 4) top = dpp_max<kHalfMirror>(top);
     const uint32_t byte = mx4_scale_byte(top);
-    const uint32_t w = code8(x, scale_operand(byte));
+    const float scale = scale_operand(byte);
+    uint32_t w = code_pair<1>(code_pair<0>(0, x[0], x[1], scale), x[2], x[3], scale);
+    if constexpr (E == 8) w = code_pair<3>(code_pair<2>(w, x[4], x[5], scale), x[6], x[7], scale);
+    w = byte == 255u ? 0u : w;
     if (u0 + k < units) {
       const int64_t line = static_cast<int64_t>(u0 + k) * a.rows + r;
-      codes[line * 16 + o] = byte == 255u ? 0u : w;
-      if ((o & 3) == 0) scales[line * 4 + (o >> 2)] = static_cast<uint8_t>(byte);
+      uint8_t* const c = codes + line * 64 + o * (E / 2);
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint32_t*>(c) = w;
+      } else {
+        *reinterpret_cast<uint16_t*>(c) = static_cast<uint16_t>(w);
+      }
+      if (o % (kMxBlock / E) == 0) scales[line * 4 + o * E / kMxBlock] = static_cast<uint8_t>(byte);
     }
   }
 }
@@ -150,14 +154,14 @@ __global__ __launch_bounds__(kThreads) void mx4_rows_kernel(Mx4QuantArgs a, int 
 constexpr int kTileThreads = 128;
 constexpr int kColPitch = 80;  // bytes of a column's codes in LDS: 64, and 16 against bank conflicts
 
-template <int D, bool FULL>
+template <int D, bool FULL, bool NT>
 __device__ __forceinline__ void load_tile(const void* X, int64_t at, int64_t pitch, int rows_left, int cols_left,
                                           float (&x)[32][4]) {
   if constexpr (FULL) {
     if constexpr (D == kF32) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at + e * pitch);
+        const u32x4_t v = LOAD_VEC(reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(X) + at + e * pitch));
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[e][c] = __uint_as_float(v[c]);
       }
@@ -165,7 +169,7 @@ __device__ __forceinline__ void load_tile(const void* X, int64_t at, int64_t pit
       u32x2_t v[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        v[e] = *reinterpret_cast<const u32x2_a2*>(static_cast<const uint16_t*>(X) + at + e * pitch);
+        v[e] = LOAD_VEC(reinterpret_cast<const u32x2_a2*>(static_cast<const uint16_t*>(X) + at + e * pitch));
 #pragma unroll
       for (int e = 0; e < 32; ++e)
 #pragma unroll
@@ -180,7 +184,7 @@ __device__ __forceinline__ void load_tile(const void* X, int64_t at, int64_t pit
   }
 }
 
-template <int D, bool ROWS>
+template <int D, bool ROWS, bool NT>
 __global__ __launch_bounds__(kTileThreads) void mx4_tile_kernel(Mx4QuantArgs a) {
   __shared__ __align__(16) uint8_t col_code[128 * kColPitch];
   __shared__ __align__(16) uint8_t row_code[ROWS ? 128 * 64 : 16];
@@ -192,9 +196,9 @@ __global__ __launch_bounds__(kTileThreads) void mx4_tile_kernel(Mx4QuantArgs a) 
   const int64_t at = static_cast<int64_t>(i) * a.cols + j;
   float x[32][4];
   if (i0 + 128 <= a.rows && j0 + 128 <= a.cols) {
-    load_tile<D, true>(a.X[b], at, a.cols, 32, 4, x);
+    load_tile<D, true, NT>(a.X[b], at, a.cols, 32, 4, x);
   } else {
-    load_tile<D, false>(a.X[b], at, a.cols, a.rows - i, a.cols - j, x);
+    load_tile<D, false, NT>(a.X[b], at, a.cols, a.rows - i, a.cols - j, x);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -263,70 +267,88 @@ __global__ __launch_bounds__(kTileThreads) void mx4_tile_kernel(Mx4QuantArgs a) 
   }
 }
 
-// ---------------------------------------------------------------------------
-// Values of the code, row-major: threads as in mx4_rows_kernel.
-// ---------------------------------------------------------------------------
+// Values of the code, row-major.  The stores pass the caches by: the values are
+// four or eight times the codes (3 x 3584x18944 fp32: 190 -> 155 us).
 template <int D>
 __global__ __launch_bounds__(kThreads) void mx4_values_kernel(Mx4DequantArgs a, int units) {
-  const int b = blockIdx.z, o = threadIdx.x & 15;
-  const int r = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x >> 4);
+  typedef Span<D> V;
+  const int b = blockIdx.z, o = threadIdx.x % V::kLanes;
+  const int r = blockIdx.x * V::kRows + static_cast<int>(threadIdx.x) / V::kLanes;
   if (r >= a.rows) return;
   const int u0 = blockIdx.y * kUnitsPerThread;
-  const uint32_t* codes = static_cast<const uint32_t*>(a.codes[b]);
+  const uint8_t* codes = static_cast<const uint8_t*>(a.codes[b]);
   const uint8_t* scales = static_cast<const uint8_t*>(a.scales[b]);
-  void* Y = a.Y[b];
   uint32_t code[kUnitsPerThread], byte[kUnitsPerThread];
 #pragma unroll
   for (int k = 0; k < kUnitsPerThread; ++k) {
     const int u = u0 + k < units ? u0 + k : units - 1;
     const int64_t line = static_cast<int64_t>(u) * a.rows + r;
-    code[k] = codes[line * 16 + o];
-    byte[k] = scales[line * 4 + (o >> 2)];
+    const uint8_t* c = codes + line * 64 + o * (V::kElems / 2);
+    code[k] = D == kF32 ? *reinterpret_cast<const uint16_t*>(c) : *reinterpret_cast<const uint32_t*>(c);
+    byte[k] = scales[line * 4 + o * V::kElems / kMxBlock];
   }
 #pragma unroll
   for (int k = 0; k < kUnitsPerThread; ++k) {
-    const int c = (u0 + k) * kMxUnit + 8 * o, left = a.cols - c;
+    const int c = (u0 + k) * kMxUnit + V::kElems * o, left = a.cols - c;
     const float s = e8m0_to_f32(byte[k]);
+    float y[8];
     const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 0);
     const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 1);
-    const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 2);
-    const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 3);
-    const float y[8] = {p0[0] * s, p0[1] * s, p1[0] * s, p1[1] * s, p2[0] * s, p2[1] * s, p3[0] * s, p3[1] * s};
-    const int64_t at = static_cast<int64_t>(r) * a.cols + c;
-    if (left >= 8) {
+    y[0] = p0[0] * s; y[1] = p0[1] * s; y[2] = p1[0] * s; y[3] = p1[1] * s;
+    if constexpr (D != kF32) {
+      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 2);
+      const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[k], 1.0f, 3);
+      y[4] = p2[0] * s; y[5] = p2[1] * s; y[6] = p3[0] * s; y[7] = p3[1] * s;
+    }
+    char* const p = static_cast<char*>(a.Y[b]) + (static_cast<int64_t>(r) * a.cols + c) * (D == kF32 ? 4 : 2);
+    if (left >= V::kElems) {
       if constexpr (D == kF32) {
-        u32x4_a4* p = reinterpret_cast<u32x4_a4*>(static_cast<float*>(Y) + at);
-        p[0] = __builtin_bit_cast(u32x4_t, make_float4(y[0], y[1], y[2], y[3]));
-        p[1] = __builtin_bit_cast(u32x4_t, make_float4(y[4], y[5], y[6], y[7]));
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, make_float4(y[0], y[1], y[2], y[3])),
+                                    reinterpret_cast<u32x4_a4*>(p));
       } else {
-        *reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(Y) + at) =
-            (u32x4_t){f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]), f32x2_to_bf16x2(y[4], y[5]),
-                      f32x2_to_bf16x2(y[6], y[7])};
+        __builtin_nontemporal_store(((u32x4_t){f32x2_to_bf16x2(y[0], y[1]), f32x2_to_bf16x2(y[2], y[3]),
+                                               f32x2_to_bf16x2(y[4], y[5]), f32x2_to_bf16x2(y[6], y[7])}),
+                                    reinterpret_cast<u32x4_a2*>(p));
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < left) store_from_f32(Y, at + e, D, y[e]);
+      for (int e = 0; e < V::kElems; ++e)
+        if (e < left) store_from_f32(p, e, D, y[e]);
     }
   }
 }
 
-dim3 row_grid(int rows, int units, int batch) {
-  return dim3((rows + kRowsPerBlock - 1) / kRowsPerBlock, (units + kUnitsPerThread - 1) / kUnitsPerThread, batch);
+dim3 row_grid(int rows, int per_block, int units, int batch) {
+  return dim3((rows + per_block - 1) / per_block, (units + kUnitsPerThread - 1) / kUnitsPerThread, batch);
 }
 
-template <int D>
+template <int D, bool NT>
 void quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) {
   if (a.codes_t[0] == nullptr) {
     const int units = static_cast<int>(mx4_units(a.cols));
-    hipLaunchKernelGGL(mx4_rows_kernel<D>, row_grid(a.rows, units, batch), dim3(kThreads), 0, s, a, units);
+    hipLaunchKernelGGL((mx4_rows_kernel<D, NT>), row_grid(a.rows, Span<D>::kRows, units, batch), dim3(kThreads), 0, s, a,
+                       units);
     return;
   }
   const dim3 grid(static_cast<uint32_t>(mx4_units(a.cols)), static_cast<uint32_t>(mx4_units(a.rows)), batch);
   if (a.codes[0] != nullptr) {
-    hipLaunchKernelGGL((mx4_tile_kernel<D, true>), grid, dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL((mx4_tile_kernel<D, true, NT>), grid, dim3(kTileThreads), 0, s, a);
   } else {
-    hipLaunchKernelGGL((mx4_tile_kernel<D, false>), grid, dim3(kTileThreads), 0, s, a);
+    hipLaunchKernelGGL((mx4_tile_kernel<D, false, NT>), grid, dim3(kTileThreads), 0, s, a);
+  }
+}
+
+// Inputs larger than the 256 MB cache are read past it: 3 x 3584x18944 fp32 both
+// ways 204 -> 174 us, bf16 120 -> 103; 8192x3584 bf16, still cached, 17 -> 20 us.
+constexpr double kStreamBytes = 256.0 * (1 << 20);
+
+template <int D>
+void quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) {
+  const double bytes = static_cast<double>(a.rows) * a.cols * batch * (D == kF32 ? 4 : 2);
+  if (bytes > kStreamBytes) {
+    quantize<D, true>(a, batch, s);
+  } else {
+    quantize<D, false>(a, batch, s);
   }
 }
 
@@ -343,11 +365,12 @@ hipError_t launch_mx4_quantize(const Mx4QuantArgs& a, int batch, hipStream_t s) 
 
 hipError_t launch_mx4_dequantize(const Mx4DequantArgs& a, int batch, hipStream_t s) {
   const int units = static_cast<int>(mx4_units(a.cols));
-  const dim3 grid = row_grid(a.rows, units, batch), block(kThreads);
   if (a.y_dtype == kF32) {
-    hipLaunchKernelGGL(mx4_values_kernel<kF32>, grid, block, 0, s, a, units);
+    hipLaunchKernelGGL(mx4_values_kernel<kF32>, row_grid(a.rows, Span<kF32>::kRows, units, batch), dim3(kThreads), 0, s,
+                       a, units);
   } else {
-    hipLaunchKernelGGL(mx4_values_kernel<kBF16>, grid, block, 0, s, a, units);
+    hipLaunchKernelGGL(mx4_values_kernel<kBF16>, row_grid(a.rows, Span<kBF16>::kRows, units, batch), dim3(kThreads), 0,
+                       s, a, units);
   }
   return hipGetLastError();
 }
