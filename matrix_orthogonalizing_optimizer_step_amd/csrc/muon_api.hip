@@ -1041,9 +1041,9 @@ muon_status group8_codec(bool dequantize, int batch, int rows, int k, void* cons
 // ---------------------------------------------------------------------------
 }  // namespace
 
-hipError_t muon::traced_launch(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
-                               const std::function<hipError_t()>& launch) {
-  return traced(s, kernel, role, flops, bytes, launch);
+hipError_t muon::traced_call(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
+                             hipError_t (*launch)(const void*), const void* context) {
+  return traced(s, kernel, role, flops, bytes, [&] { return launch(context); });
 }
 
 // Scratch memory of muon_step_fixed_scratch, for callers that cannot

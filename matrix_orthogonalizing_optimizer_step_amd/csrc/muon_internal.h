@@ -4,8 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <functional>
-
 namespace muon {
 
 // Every workspace dimension is padded to a multiple of this, so the GEMM
@@ -104,8 +102,13 @@ int gemm_tile(int op);  // block tile edge of the GEMM kernel used for an operan
 
 // Runs `launch`, bracketed by the launch trace's events if the trace is on
 // (muon_trace_enable), with the launch's kernel, role and algorithmic work.
+hipError_t traced_call(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
+                       hipError_t (*launch)(const void*), const void* context);
+template <class F>
 hipError_t traced_launch(hipStream_t s, const char* kernel, const char* role, double flops, double bytes,
-                         const std::function<hipError_t()>& launch);
+                         const F& launch) {
+  return traced_call(s, kernel, role, flops, bytes, [](const void* f) { return (*static_cast<const F*>(f))(); }, &launch);
+}
 
 struct NormArgs {
   const void* const* M;   // user matrices

@@ -68,57 +68,61 @@ constexpr int waitcnt_imm(int vm, int lgkm) {  // vmcnt, no wait for exports, lg
   return (vm & 15) | (((vm >> 4) & 3) << 14) | (7 << 4) | ((lgkm & 15) << 8);
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t u = reinterpret_cast<uint64_t>(base);
+// A buffer resource of `bytes` bytes at `base` + `offset` (all block-uniform).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t offset, uint32_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(base) + offset;
   const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u & 0xffffffffu)));
   const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32)));
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), static_cast<short>(0),
                                            __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
 }
 
-// One operand's source: codes and scales from this wave's first row on.
+// One operand's source, seen from this lane.
 struct Source {
-  __amdgpu_buffer_rsrc_t code, scale;
-  uint32_t row;     // first row of this wave's loads
-  uint32_t rows;    // rows of the matrix
+  const void* code;
+  const void* scale;
+  int vcode, vscale;     // byte offsets of this lane's first loads from a unit's first row
+  uint32_t rows, lines;  // rows of the matrix; units x rows
 };
 
 // Loads FIRST .. LAST - 1 of the T::kLoads that bring this wave's share of unit u
 // into a stage: the codes of A and of B, 16 rows each, and the scales of A and
-// of B.  u may lie behind the last unit and rows behind the last row: such
-// addresses are behind the buffer's end (zeros) or in the next unit's rows, and
-// what they give enters no stored element.
+// of B.  Behind the last unit the last one is read again.  The resource starts at
+// the unit and ends with the matrix, so every load is checked against the
+// matrix's end: rows behind the last row read the next unit's, or zeros behind
+// the last unit.  Neither enters a stored element.
 template <class T, int FIRST, int LAST>
-__device__ __forceinline__ void load_unit(typename T::Stage& st, const Source& A, const Source& B, uint32_t u, int wave,
-                                          int lane, int vcode) {
+__device__ __forceinline__ void load_unit(typename T::Stage& st, const Source& A, const Source& B, int u, int last,
+                                          int wave, int lane) {
   constexpr int RA = T::TM / 4, RB = T::TN / 4;  // rows of this wave
-  const uint32_t la = u * A.rows + A.row, lb = u * B.rows + B.row;
-  const int soa = __builtin_amdgcn_readfirstlane(static_cast<int>(la * 64u));
-  const int sob = __builtin_amdgcn_readfirstlane(static_cast<int>(lb * 64u));
+  const uint32_t unit = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(u < last ? u : last));
+  const uint32_t la = unit * A.rows, lb = unit * B.rows;
+  const __amdgpu_buffer_rsrc_t ca = make_rsrc(A.code, la * 64u, (A.lines - la) * 64u);
+  const __amdgpu_buffer_rsrc_t cb = make_rsrc(B.code, lb * 64u, (B.lines - lb) * 64u);
   lds_ptr_t da = (lds_ptr_t)(st.code + wave * RA * 4), db = (lds_ptr_t)(st.code + (T::TM + wave * RB) * 4);
-#define MX4_LOAD(N, R, SRC, DST, SO, OFF)                                        \
-  if constexpr (FIRST <= (N) && (N) < LAST && (OFF) < (R) * 64)                  \
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(SRC.code, DST, 16, vcode, SO, OFF, 0)
+#define MX4_LOAD(N, R, RSRC, DST, VOFF, OFF)                    \
+  if constexpr (FIRST <= (N) && (N) < LAST && (OFF) < (R) * 64) \
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(RSRC, DST, 16, VOFF, 0, OFF, 0)
   constexpr int NA = RA / 16, NB = RB / 16;
-  MX4_LOAD(0, RA, A, da, soa, 0);
-  MX4_LOAD(1, RA, A, da, soa, 1024);
-  MX4_LOAD(2, RA, A, da, soa, 2048);
-  MX4_LOAD(3, RA, A, da, soa, 3072);
-  MX4_LOAD(NA, RB, B, db, sob, 0);
-  MX4_LOAD(NA + 1, RB, B, db, sob, 1024);
-  MX4_LOAD(NA + 2, RB, B, db, sob, 2048);
-  MX4_LOAD(NA + 3, RB, B, db, sob, 3072);
+  MX4_LOAD(0, RA, ca, da, A.vcode, 0);
+  MX4_LOAD(1, RA, ca, da, A.vcode, 1024);
+  MX4_LOAD(2, RA, ca, da, A.vcode, 2048);
+  MX4_LOAD(3, RA, ca, da, A.vcode, 3072);
+  MX4_LOAD(NA, RB, cb, db, B.vcode, 0);
+  MX4_LOAD(NA + 1, RB, cb, db, B.vcode, 1024);
+  MX4_LOAD(NA + 2, RB, cb, db, B.vcode, 2048);
+  MX4_LOAD(NA + 3, RB, cb, db, B.vcode, 3072);
 #undef MX4_LOAD
   static_assert(RA <= 64 && RB <= 64 && NA + NB + 2 == T::kLoads, "loads of a unit");
   if constexpr (FIRST <= NA + NB && NA + NB < LAST) {
     if (RA == 64 || lane < RA)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(A.scale, (lds_ptr_t)(st.scale + wave * RA), 4, lane * 4,
-                                               __builtin_amdgcn_readfirstlane(static_cast<int>(la * 4u)), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(A.scale, la * 4u, (A.lines - la) * 4u),
+                                               (lds_ptr_t)(st.scale + wave * RA), 4, A.vscale, 0, 0, 0);
   }
   if constexpr (FIRST <= NA + NB + 1 && NA + NB + 1 < LAST) {
     if (RB == 64 || lane < RB)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(B.scale, (lds_ptr_t)(st.scale + T::TM + wave * RB), 4, lane * 4,
-                                               __builtin_amdgcn_readfirstlane(static_cast<int>(lb * 4u)), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(B.scale, lb * 4u, (B.lines - lb) * 4u),
+                                               (lds_ptr_t)(st.scale + T::TM + wave * RB), 4, B.vscale, 0, 0, 0);
   }
 }
 
@@ -166,13 +170,13 @@ __device__ __forceinline__ void mfmas(f32x16_t (&acc)[T::FN][T::FM], const Frags
 template <class T>
 __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0, ScaleWords<T>& w,
                                      typename T::Stage& prv, typename T::Stage& cur, const typename T::Stage& nxt,
-                                     const Source& A, const Source& B, uint32_t u, int wave, int lane, int vcode,
-                                     int ra, int rb) {
+                                     const Source& A, const Source& B, int u, int last, int wave, int lane, int ra,
+                                     int rb) {
   constexpr int FM = T::FM, FN = T::FN, kMid = T::kAfter + (T::kLoads - T::kAfter) * 2 / 3;
   Frags<T> f1;
   read_frag<FN>(f1.b, cur, rb, lane, 1);
   read_frag<FM>(f1.a, cur, ra, lane, 1);
-  load_unit<T, T::kAfter, kMid>(prv, A, B, u + kStages - 1, wave, lane, vcode);
+  load_unit<T, T::kAfter, kMid>(prv, A, B, u + kStages - 1, last, wave, lane);
   mfmas<T, 0, 0, FM>(acc, f0, w);
   if constexpr (FM * FN >= FM + FN) {
 #pragma unroll
@@ -183,7 +187,7 @@ __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0
     }
   }
   __builtin_amdgcn_sched_barrier(0);
-  load_unit<T, kMid, T::kLoads>(prv, A, B, u + kStages - 1, wave, lane, vcode);
+  load_unit<T, kMid, T::kLoads>(prv, A, B, u + kStages - 1, last, wave, lane);
   mfmas<T, 1, 0, FM / 2>(acc, f1, w);
   if constexpr (FM * FN >= FM + FN) {
 #pragma unroll
@@ -198,7 +202,7 @@ __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kLoads, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
-  load_unit<T, 0, T::kAfter>(cur, A, B, u + kStages, wave, lane, vcode);
+  load_unit<T, 0, T::kAfter>(cur, A, B, u + kStages, last, wave, lane);
   ScaleWords<T> wn;
   read_frag<FN>(f0.b, nxt, rb, lane, 0);
   read_frag<FM>(f0.a, nxt, ra, lane, 0);
@@ -364,17 +368,18 @@ __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kerne
   const int b = outer / a.pieces, piece = outer - b * a.pieces;
   const int i0 = ti * T::TM, j0 = tj * T::TN;
   const int ub = piece * a.piece_units, ue = ub + a.piece_units < a.units ? ub + a.piece_units : a.units;
-  const uint32_t lines_a = static_cast<uint32_t>(a.units) * a.m, lines_b = static_cast<uint32_t>(a.units) * a.n;
-  const Source A{make_rsrc(a.A[b], lines_a * 64u), make_rsrc(a.As[b], lines_a * 4u),
-                 static_cast<uint32_t>(i0 + wave * (T::TM / 4)), static_cast<uint32_t>(a.m)};
-  const Source B{make_rsrc(a.B[b], lines_b * 64u), make_rsrc(a.Bs[b], lines_b * 4u),
-                 static_cast<uint32_t>(j0 + wave * (T::TN / 4)), static_cast<uint32_t>(a.n)};
   // lane l fills slot l % 4 of row l / 4 of each 16-row piece
   const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  const int fa = i0 + wave * (T::TM / 4), fb = j0 + wave * (T::TN / 4);  // first rows of this wave's loads
+  const Source A{a.A[b], a.As[b], fa * 64 + vcode, (fa + lane) * 4, static_cast<uint32_t>(a.m),
+                 static_cast<uint32_t>(a.units) * a.m};
+  const Source B{a.B[b], a.Bs[b], fb * 64 + vcode, (fb + lane) * 4, static_cast<uint32_t>(a.n),
+                 static_cast<uint32_t>(a.units) * a.n};
+  const int last = a.units - 1;
   Stage* st[kStages] = {&s0, &s1, &s2, &s3};
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load_unit<T, 0, T::kLoads>(*st[s], A, B, ub + s, wave, lane, vcode);
-  load_unit<T, 0, T::kAfter>(s3, A, B, ub + 3, wave, lane, vcode);
+  for (int s = 0; s < kStages - 1; ++s) load_unit<T, 0, T::kLoads>(*st[s], A, B, ub + s, last, wave, lane);
+  load_unit<T, 0, T::kAfter>(s3, A, B, ub + 3, last, wave, lane);
   const int ra = FM * 32 * (wave / T::WN), rb = T::TM + FN * 32 * (wave % T::WN);
   f32x16_t acc[FN][FM] = {};
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kLoads + T::kAfter, 0));
@@ -390,14 +395,14 @@ __global__ __launch_bounds__(256, T::TM == 256 ? 1 : 2) void mx4_tile_gemm_kerne
   shift_scales<FM>(w.a, lane);
   int u = ub;
   for (; u + kStages <= ue; u += kStages) {
-    slab<T>(acc, f, w, s3, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
-    slab<T>(acc, f, w, s2, s3, s0, A, B, u + 3, wave, lane, vcode, ra, rb);
+    slab<T>(acc, f, w, s3, s0, s1, A, B, u, last, wave, lane, ra, rb);
+    slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, last, wave, lane, ra, rb);
+    slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, last, wave, lane, ra, rb);
+    slab<T>(acc, f, w, s2, s3, s0, A, B, u + 3, last, wave, lane, ra, rb);
   }
-  if (u < ue) slab<T>(acc, f, w, s3, s0, s1, A, B, u, wave, lane, vcode, ra, rb);
-  if (u + 1 < ue) slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, wave, lane, vcode, ra, rb);
-  if (u + 2 < ue) slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, wave, lane, vcode, ra, rb);
+  if (u < ue) slab<T>(acc, f, w, s3, s0, s1, A, B, u, last, wave, lane, ra, rb);
+  if (u + 1 < ue) slab<T>(acc, f, w, s0, s1, s2, A, B, u + 1, last, wave, lane, ra, rb);
+  if (u + 2 < ue) slab<T>(acc, f, w, s1, s2, s3, A, B, u + 2, last, wave, lane, ra, rb);
   // loads behind the last unit are still on their way into LDS: they end here,
   // and so do all waves' reads, before LDS takes the results
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
