@@ -12,6 +12,14 @@
 // block per chunk, and a block finds its tensor in the chunk starts that travel
 // with the kernel arguments, as the pointers do (no table in memory, so nothing
 // has to be copied to the device first and a captured graph holds everything).
+//
+// Both kernels are bound by memory: an element is read and written once, 28
+// bytes with fp32 W and G and 32-bit states, 10.1 with bf16 and 8-bit ones,
+// against some 25 and 75 instructions.  What counts is bytes in flight: a thread
+// issues all loads of its 16 (8) elements before it uses one, and the chip holds
+// thousands of such blocks.  Measured on 235M parameters: 32-bit states 5.83 TB/s
+// (bf16 W and G, 886 us) and 5.90 (fp32, 1114 us), 8-bit states 5.38 (442 us) and
+// 5.49 (690 us); a large copy reaches 4.8 and an addition in place 6.0.
 #include <math.h>
 #include <string.h>
 
@@ -40,7 +48,8 @@ struct AdamwScalars {
 
 // The tensors of one launch, up to K of them with P pointers each.  Two sizes of
 // the kernel arguments: as many tensors as keep them within the 4 KB that a
-// launch takes, and kFew for short lists, whose 0.5 KB the host copies sooner.
+// launch takes, and kFew for short lists, whose 0.5 KB the host copies sooner
+// (a call on one norm 4.87 -> 4.65 us).
 constexpr int kFew = 8;
 constexpr int many_tensors(int pointers) { return 3840 / (8 * pointers + 12); }
 
@@ -284,8 +293,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs<kPtrs32, K> a
 // divide by eps alone.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
-  // xor-shift and multiply rounds; the constants are the odd numbers next to
-  // 2^32 times the golden ratio's inverse and 2^32 times (e - 2)
+  // xor-shift and multiply rounds; the constants are odd numbers near 2^32 times
+  // the golden ratio's inverse and 2^32 times (e - 2)
   x ^= x >> 16;
   x *= 0x9E3779B1u;
   x ^= x >> 15;
@@ -306,7 +315,8 @@ __device__ __forceinline__ float code_scale(uint32_t top_bits) {
 // sqrt(x) rounded to nearest, for x zero, normal or not finite: v_sqrt_f32 is
 // off by at most one unit; s is too large if x <= s (s - 1 unit) (the square of
 // the midpoint below s, less a quarter unit squared) and too small if x > s (s +
-// 1 unit).  A third of the instructions of sqrtf(), which also scales subnormals.
+// 1 unit).  sqrtf() also scales subnormals, which an element's v needs not: its
+// code is that of a zero then, or the smallest.
 __device__ __forceinline__ float root_nearest(float x) {
   const float s = __builtin_amdgcn_sqrtf(x);
   const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
