@@ -247,6 +247,64 @@ def test_adamw8_against_oracle(w, g, sizes, offset):
             assert not whole[:offset * e].any() and not whole[(offset + x.numel()) * e:].any()
 
 
+def test_adamw8_many_tensors():
+    """A list over several launches: the roundings go by the place in the whole list."""
+    sizes = [(53 * i) % 397 for i in range(150)]
+    W, M, V, G = make(sizes, "f32", "f32", 25)
+    step8(W, state_of(M, V), G, 6, 12, "f32", HYPER)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_adamw_past_2_31_elements(eight):
+    """One tensor of 2^31 + 1003 elements: both ends are stepped, what has no gradient and no decay stays."""
+    n = 2 ** 31 + 1003
+    W = [torch.ones(n, dtype=torch.bfloat16, device=DEV)]
+    G = [torch.zeros(n, dtype=torch.bfloat16, device=DEV)]
+    ends = torch.cat((torch.arange(3000), torch.arange(n - 3000, n))).to(DEV)
+    G[0][ends] = torch.randn(6000, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(torch.bfloat16)
+    hyper = dict(lr=0.03, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
+    if eight:
+        state = mu.AdamW8State.zeros(W)
+        mu.adamw8_step(W, state, G, 1, **hyper)
+    else:
+        M, V = [torch.zeros(n, device=DEV)], [torch.zeros(n, device=DEV)]
+        mu.adamw_step(W, M, V, G, 1, **hyper)
+    g = f64(G[0][ends])
+    one, zero = np.ones(6000), np.zeros(6000)
+    args = (one, zero, zero, g, 1, 0.03, 0.9, 0.999, 1e-8, 0.0)
+    w, m, v = ao.adamw(*args)
+    tol = ao.adamw_tolerance(*args, w_half=2.0 ** -8)
+    assert np.all(np.abs(f64(W[0][ends]) - w) <= tol[0] * 21.5 / 17)
+    if not eight:
+        assert np.all(np.abs(f64(M[0][ends]) - m) <= tol[1]) and np.all(np.abs(f64(V[0][ends]) - v) <= tol[2])
+    for part in (slice(3000, 2 ** 30), slice(2 ** 30, n - 3000)):
+        assert bool((W[0][part] == 1).all())
+        if eight:
+            assert not state.m_codes[0][part].view(torch.uint8).any() and not state.r_codes[0][part].view(torch.uint8).any()
+        else:
+            assert not M[0][part].any() and not V[0][part].any()
+
+
+def test_adamw8_tiny_gradients():
+    """Gradients down to fp32's subnormal squares: no division by zero, no NaN, W within the bounds of eps."""
+    n = 512
+    W = [torch.ones(n, device=DEV)]
+    G = [torch.logspace(-44, 0, n, device=DEV, dtype=torch.float64).float()]
+    state = mu.AdamW8State.zeros(W)
+    for t in (1, 2, 3):
+        mu.adamw8_step(W, state, G, t, 0.01)
+    m, v = state.values()
+    assert torch.isfinite(W[0]).all() and torch.isfinite(m[0]).all() and torch.isfinite(v[0]).all()
+    # For a constant gradient m_hat / sqrt(v_hat) is at most 1 before rounding.  Coding m changes it by a factor of at most
+    # 2 (the smallest magnitude that is not stored as 0 is half the smallest code), coding the root divides it by at most
+    # 2 (it goes to its lower neighbour, and never to 0), so a step's quotient grows by at most 4: 1, 4 and 16 times lr.
+    assert ((1 - W[0]).abs() <= 0.01 * (1 + 4 + 16)).all()
+    # Over 2^-6 of its group's code range (1e-3 of the last group's largest gradient is 0.448 of 448) m loses at most
+    # 1/16 and the root gains at most 1/8 a step: at least 1, 0.83 and 0.69 times lr.
+    big = G[0] > 1e-3
+    assert ((1 - W[0])[big] > 0.01 * (1 + 0.83 + 0.69)).all()
+
+
 def test_adamw8_several_steps_from_zero():
     W, _, _, _ = make((4096 + 77, 300), "f32", "f32", 22)
     state = mu.AdamW8State.zeros(W)

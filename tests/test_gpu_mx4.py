@@ -165,7 +165,10 @@ def check_product(C, A, B, dtype, C0=None, exact=False):
 SHAPES = [(1, 1, 1, 1), (1, 5, 7, 33), (2, 31, 65, 127), (1, 64, 64, 128), (1, 65, 129, 129), (3, 130, 70, 257),
           (1, 257, 300, 1000), (1, 1, 4096, 7001), (1, 3, 300, 640), (2, 16, 513, 2050), (1, 300, 1, 640),
           (1, 17, 1000, 31), (1, 512, 512, 512), (1, 129, 2049, 384), (1, 33, 40, 9000), (4, 20, 96, 1200),
-          (1, 700, 520, 1153)]
+          (1, 700, 520, 1153),
+          (1, 5, 700, 8300), (19, 3, 40, 300), (17, 20, 50, 600),  # 16 waves a block; more matrices than one launch takes
+          (1, 1030, 3001, 400), (2, 700, 2100, 150),               # 128 x 128 tiles, ragged
+          (1, 4100, 2900, 300), (1, 3333, 4003, 129)]              # 256 x 256 tiles, ragged
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -314,6 +317,72 @@ def test_two_products_at_once_on_two_streams():
     got = [[mu.mx4_matmul(A, B, torch.float32, stream=s)[0] for s in streams] for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for pair in got for x in pair)
+
+
+def test_two_captured_products_replayed_at_once():
+    """Two graphs of products that are split along k, each with its own scratch, replayed side by side."""
+    sets = []
+    for i in range(2):
+        A, B = random_code(1, 260, 6000, 30 + i), random_code(1, 300, 6000, 40 + i)
+        C = [torch.zeros(260, 300, device=DEV)]
+        mu.mx4_matmul(A, B, out=C)
+        want = C[0].clone()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mu.mx4_matmul(A, B, out=C)
+        sets.append((g, C, want, torch.cuda.Stream(), A, B))
+    for _ in range(4):
+        for g, C, *_ in sets:
+            C[0].zero_()
+        torch.cuda.synchronize()
+        for g, C, want, s, A, B in sets:
+            with torch.cuda.stream(s):
+                g.replay()
+        mu.mx4_matmul(sets[0][4], sets[0][5], torch.float32)  # eager work beside them
+        torch.cuda.synchronize()
+        for g, C, want, *_ in sets:
+            assert torch.equal(C[0], want)
+
+
+def test_code_of_more_matrices_than_one_launch_takes():
+    X = matrices(35, 9, 70, "bf16", 25)
+    q, t = mu.mx4_quantize(X, transpose="both")
+    same_code(q, [f64(x) for x in X])
+    same_code(t, [f64(x).T for x in X])
+    for y, c, s in zip(mu.mx4_dequantize(q), q.codes, q.scales):
+        assert np.array_equal(f64(y), xo.decode(c.cpu().numpy(), s.cpu().numpy(), 70))
+
+
+def test_code_and_values_past_2_31_elements():
+    """66000 x 32768 bf16 (2.16e9 elements): the last rows' codes in both orientations, and their values."""
+    rows, cols = 66000, 32768
+    X = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    X[-300:] = torch.randn(300, cols, device=DEV, generator=torch.Generator(DEV).manual_seed(3)).to(torch.bfloat16)
+    q, t = mu.mx4_quantize([X], transpose="both")
+    # the last whole unit of 128 rows and what follows start at row 515 * 128 = 65920 of 66000
+    tail = mu.MX4([q.codes[0][:, -80:].contiguous()], [q.scales[0][:, -80:].contiguous()], cols)
+    same_code(tail, [f64(X[-80:])])
+    wc, ws = xo.quantize(f64(X[65920:]).T)
+    assert np.array_equal(t.codes[0][515:].cpu().numpy(), wc) and np.array_equal(t.scales[0][515:].cpu().numpy(), ws)
+    assert not q.codes[0][:, :65700].any() and not t.codes[0][:513].any()
+    only = mu.mx4_quantize([X])
+    assert torch.equal(only.codes[0], q.codes[0]) and torch.equal(only.scales[0], q.scales[0])
+    del only, t
+    Y = mu.mx4_dequantize(q, torch.bfloat16)[0]
+    assert np.array_equal(f64(Y[-80:]), xo.decode(tail.codes[0].cpu().numpy(), tail.scales[0].cpu().numpy(), cols))
+    assert not Y[:65700].any()
+
+
+def test_product_past_2_31_elements():
+    """50000 x 50000 results (2.5e9): rows at the start, in the middle and at the end."""
+    A, B = random_code(1, 50000, 100, 26, 127, 127), random_code(1, 50000, 100, 27, 127, 127)
+    b64 = decoded(B)[0]
+    C = mu.mx4_matmul(A, B, torch.bfloat16)[0]
+    a64 = decoded(A)[0]
+    for i in (0, 1, 255, 256, 42949, 42950, 49997, 49999):
+        want = f64(torch.from_numpy((a64[i] @ b64.T).astype(np.float32)).to(torch.bfloat16))
+        assert np.array_equal(f64(C[i]), want), i
 
 
 def test_mx4_launches_are_traced():
