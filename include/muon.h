@@ -346,8 +346,9 @@ muon_status muon_group8_dequantize(int batch, int rows, int k, const void *const
  * call only: such lists are long and their gradients move, so the pointers
  * travel as kernel arguments (one launch per 87 tensors) instead of in an array
  * in device memory.  They must be distinct, and no two of the buffers may overlap.
- * Buffers need the alignment of their element type only.  Errors as for muon_step; MUON_ERR_INVALID_ARG also for lr, eps
- * or weight_decay not finite in fp32, eps < 2^-126, betas outside [0, 1) or step < 1.
+ * Buffers need the alignment of their element type only.  Errors as for muon_step;
+ * MUON_ERR_INVALID_ARG also for lr, eps or weight_decay not finite in fp32, eps <
+ * 2^-126, betas outside [0, 1) or step < 1.
  *
  * muon_adamw_config:
  *   lr, beta1, beta2, eps, weight_decay   defaults 1e-3, 0.9, 0.999, 1e-8, 0
@@ -421,7 +422,8 @@ muon_status muon_adamw8_step(int tensors, const int64_t *sizes, void *const *W, 
  * 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 = sign).  The conversion is exact arithmetic.
  *
  * Layout: a row of k elements is ceil(k / 128) units of four blocks, filled up
- * with zeros (codes and scale bytes).  For a matrix of `rows` rows
+ * with zeros (codes and scale bytes; the product relies on them).  For a matrix
+ * of `rows` rows
  *   codes   uint8 [units][rows][64], element 2 i in the low, 2 i + 1 in the
  *           high half of byte i of its unit; 16-byte aligned
  *   scales  uint8 [units][rows][4]; 4-byte aligned.

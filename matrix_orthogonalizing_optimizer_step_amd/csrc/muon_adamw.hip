@@ -13,15 +13,20 @@
 // with the kernel arguments, as the pointers do (no table in memory, so nothing
 // has to be copied to the device first and a captured graph holds everything).
 //
-// Both kernels are bound by memory: an element is read and written once, 28
-// bytes with fp32 W and G and 32-bit states, 10.1 with bf16 and 8-bit ones,
-// against some 25 and 75 instructions.  What counts is bytes in flight: a thread
-// issues all loads of its 16 (8) elements before it uses one, and the chip holds
-// thousands of such blocks.  Measured on 235M parameters: 32-bit states 5.83 TB/s
-// (bf16 W and G, 886 us) and 5.90 (fp32, 1114 us), 8-bit states 5.38 (442 us) and
-// 5.49 (690 us); a large copy reaches 4.8 and an addition in place 6.0.
+// With 32-bit states memory bounds the step: an element is read and written once,
+// 28 bytes with fp32 W and G, against some 25 instructions.  What counts is bytes
+// in flight: a thread issues all loads of its 16 elements before it uses one, and
+// the chip holds thousands of such blocks.  With 8-bit states it is 10.1 bytes
+// (bf16 W and G) against 58 vector instructions, 3 of them at a quarter of the rate:
+// for 235M parameters some 395 us of memory beside 400 us of instructions, so both
+// count (with 71 instructions 439 us, with 58 428, then with accesses past the
+// caches 384).  Measured on 235M parameters: 32-bit states 5.83 TB/s (bf16 W and
+// G, 886 us) and 5.90 (fp32, 1114 us), 8-bit states 6.2 (384 us) and 5.70 (665 us);
+// a large copy reaches 4.8 and an addition in place 6.0.
 #include <math.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "../../include/muon.h"
 #include "muon_convert.h"
@@ -39,6 +44,7 @@ constexpr int kChunk8 = kThreads * 8;                  // elements per block, 8-
 struct AdamwScalars {
   float lr, wd, eps, b1, ob1, b2, ob2;
   float c1, c2;              // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) for the host's t
+  float lr1, wd1;            // lr c1, wd / c1
   double beta1, beta2;
   int64_t step;
   const int64_t* step_dev;   // t in device memory, or null
@@ -100,15 +106,18 @@ __device__ __forceinline__ double int_power(double b, int64_t t) {
 
 // The scalars with a step number or a gradient scale from device memory.
 struct Scalars {
-  float c1, c2, gs;
+  float c1, c2, lr1, wd1, gs;
   int64_t step;
 };
 __device__ __forceinline__ Scalars load_scalars(const AdamwScalars& s) {
-  Scalars r{s.c1, s.c2, 1.0f, s.step};
+  Scalars r{s.c1, s.c2, s.lr1, s.wd1, 1.0f, s.step};
   if (s.step_dev != nullptr) {
     const int64_t t = *s.step_dev;
     r.step = t < 1 ? 1 : t;
-    r.c1 = static_cast<float>(1.0 / (1.0 - int_power(s.beta1, r.step)));
+    const double left = 1.0 - int_power(s.beta1, r.step);
+    r.c1 = static_cast<float>(1.0 / left);
+    r.lr1 = static_cast<float>(s.lr / left);
+    r.wd1 = static_cast<float>(s.wd * left);
     r.c2 = static_cast<float>(1.0 / sqrt(1.0 - int_power(s.beta2, r.step)));
   }
   if (s.grad_scale != nullptr) r.gs = *s.grad_scale;
@@ -302,82 +311,106 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// 1 / s, or 0 where the group is stored as zeros (s zero or not finite).
-__device__ __forceinline__ float code_inverse(float s) { return s > 0.0f && s < INFINITY ? 1.0f / s : 0.0f; }
+// The two halves of mix(x) as 2^32 u = 65536 (half + 1/2), lower half first.
+__device__ __forceinline__ void mix_chances(uint32_t x, float* lo, float* hi) {
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0xB7E15163u;
+  *lo = static_cast<float>((x << 16 | 0x8000u) ^ (x & 0xFFFF0000u));
+  *hi = static_cast<float>((x & 0xFFFF0000u) | 0x8000u);
+}
 
-// The scale of a group from the bits of its largest magnitude (NaN counts as
-// largest).  A scale under 2^-126 is taken as 0.
-__device__ __forceinline__ float code_scale(uint32_t top_bits) {
-  const float s = __uint_as_float(top_bits) * (1.0f / 448.0f);
+// 1 / s rounded to nearest, or 0 where the group is stored as zeros (s zero or
+// not finite).  v_rcp_f32 is off by one unit at most and one Newton step ends
+// the error (checked for every s from 2^-126 on).
+__device__ __forceinline__ float code_inverse(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return s > 0.0f && s < INFINITY ? fmaf(fmaf(-s, r, 1.0f), r, r) : 0.0f;
+}
+
+// The scale of a group from its largest magnitude.  A scale under 2^-126 is
+// taken as 0.
+__device__ __forceinline__ float code_scale(float top) {
+  const float s = top * (1.0f / 448.0f);
   return s < 0x1p-126f ? 0.0f : s;
 }
 
-// sqrt(x) rounded to nearest, for x zero, normal or not finite: v_sqrt_f32 is
-// off by at most one unit; s is too large if x <= s (s - 1 unit) (the square of
-// the midpoint below s, less a quarter unit squared) and too small if x > s (s +
-// 1 unit).  sqrtf() also scales subnormals, which an element's v needs not: its
-// code is that of a zero then, or the smallest.
+// sqrt(x) rounded to nearest, for x zero or finite and at least 2^-102: s = x / sqrt(x) by v_rsq_f32 and one Newton step with the residual x - s^2, which
+// fmaf gives exactly (checked for every x).  Smaller ones: under 2^-51 (1 + 2^-23).
+// Infinity and NaN: NaN.
 __device__ __forceinline__ float root_nearest(float x) {
-  const float s = __builtin_amdgcn_sqrtf(x);
-  const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
-  const float under = fmaf(-below, s, x), over = fmaf(-above, s, x);
-  const float r = under <= 0.0f ? below : s;
-  return over > 0.0f ? above : r;
+  const uint32_t bits = __float_as_uint(x);
+  const float r = __builtin_amdgcn_rsqf(__uint_as_float(bits > 0x00800000u ? bits : 0x00800000u));
+  const float s = x * r;
+  return fmaf(fmaf(-s, s, x), 0.5f * r, s);
 }
 
-// Code of x in [0, 448] (see above), h16 in 0..65535.  In units of the code step
-// at x (a power of two, so nothing is rounded by it) the neighbours are f and
-// f + 1, and the condition is (y - f)(y + f) > u (2 f + 1).
-__device__ __forceinline__ uint32_t root_code(float x, uint32_t h16, bool positive) {
-  uint32_t step = __float_as_uint(x) & 0x7F800000u;  // of the binade of x, at least 2^-6
-  step = (step > (121u << 23) ? step : 121u << 23) - (3u << 23);
-  const float y = x * __uint_as_float((254u << 23) - step);  // x / step: 8..16, or 0..8 under 2^-6
+// The value of the code of x in [0, 448 (1 + 2^-22)] (see above), given 2^32 u.
+// In units of the code step at x (a power of two, so nothing is
+// rounded by it) the neighbours are f and f + 1, and the condition is (y - f)
+// (y + f) > u (2 f + 1).  Of 14 units of 32, the largest code, 14 (1 + 2^-22) is
+// 14 for every u: (y - f)(y + f) < 2^-13 < 29 * 2^-17.
+__device__ __forceinline__ float root_code_value(float x, float u32, bool positive) {
+  const uint32_t binade = __float_as_uint(x) & 0x7F800000u;
+  const uint32_t b = binade > (121u << 23) ? binade : 121u << 23;  // of x, at least 2^-6; the step is 1/8 of it
+  const float y = x * __uint_as_float((257u << 23) - b);           // x / step: 8..16, or 0..8 under 2^-6
   const float f = floorf(y);
-  const float bar = (static_cast<float>(h16) + 0.5f) * fmaf(f, 0x1p-15f, 0x1p-16f);
-  const bool up = (y - f) * (y + f) > bar || (f == 0.0f && positive);
-  return ((step - (118u << 23)) >> 20) + static_cast<uint32_t>(f) + (up ? 1u : 0u);
+  const float bar = u32 * fmaf(f, 0x1p-31f, 0x1p-32f);
+  const bool up = ((y - f) * (y + f) > bar) | ((f == 0.0f) & positive);
+  const float step = __uint_as_float(b - (3u << 23));
+  return fmaf(f, step, up ? step : 0.0f);
 }
 
-// One element of the 8-bit step: as update(), with the new moment's root r kept
-// and the quotient by v_rcp_f32 (off by one unit at most).
-__device__ __forceinline__ void update8(float& w, float g, float& m, float& v, float& root, const AdamwScalars& s,
-                                        const Scalars& r) {
-  {
+// One element's moments as in update(); its weight, with the root of the new v,
+// by W - (lr c1) (m / (root c2 + eps) + (wd / c1) W), the quotient by v_rcp_f32
+// (off by one unit at most).
+__device__ __forceinline__ void moments8(float g, float& m, float& v, const AdamwScalars& s) {
 #pragma clang fp contract(off)
-    g *= r.gs;
-    m = s.b1 * m + s.ob1 * g;
-    v = s.b2 * v + (s.ob2 * g) * g;
-  }
-  root = root_nearest(v);
+  m = s.b1 * m + s.ob1 * g;
+  v = s.b2 * v + (s.ob2 * g) * g;
+}
+__device__ __forceinline__ float weight8(float w, float m, float root, const AdamwScalars& s, const Scalars& r) {
   const float inverse = __builtin_amdgcn_rcpf(fmaf(root, r.c2, s.eps));
-  w = fmaf(-s.lr, fmaf(s.wd, w, m * r.c1 * inverse), w);
+  return fmaf(-r.lr1, fmaf(r.wd1, w, m * inverse), w);
 }
 
-__device__ __forceinline__ uint32_t group_max(uint32_t x) {  // over 16 consecutive lanes
+// Largest magnitude of 16 threads' 8 values each (a DPP row), compared as unsigned
+// integers across the threads: a NaN's bits count as the largest.
+__device__ __forceinline__ float group_max(const float (&v)[8]) {
+  float top = 0.0f;
 #pragma unroll
-  for (int d = 1; d < 16; d <<= 1) {
-    const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), d));
+  for (int k = 0; k < 8; k += 2)
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(v[k]), fabsf(v[k + 1])), top);
+  uint32_t x = __float_as_uint(top);
+  const auto rotate_max = [&](auto turn) {
+    const uint32_t y = static_cast<uint32_t>(
+        __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x120 + decltype(turn)::value, 0xf, 0xf, true));
     x = x > y ? x : y;
-  }
-  return x;
+  };
+  rotate_max(std::integral_constant<int, 1>());
+  rotate_max(std::integral_constant<int, 2>());
+  rotate_max(std::integral_constant<int, 4>());
+  rotate_max(std::integral_constant<int, 8>());
+  return __uint_as_float(x);
 }
 
 // 8 code bytes.
-template <bool FULL>
+template <bool FULL, bool NT>
 __device__ __forceinline__ u32x2_t load_codes(const void* p, int64_t i, int64_t left) {
   const uint8_t* c = static_cast<const uint8_t*>(p) + i;
-  if (FULL || left >= 8) return *reinterpret_cast<const u32x2_a1*>(c);
+  if (FULL || left >= 8) return LOAD_VEC(reinterpret_cast<const u32x2_a1*>(c));
   u32x2_t r = {0, 0};
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (k < left) r[k >> 2] |= static_cast<uint32_t>(c[k]) << (8 * (k & 3));
   return r;
 }
-template <bool FULL>
+template <bool FULL, bool NT>
 __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t left, u32x2_t x) {
   uint8_t* c = static_cast<uint8_t*>(p) + i;
   if (FULL || left >= 8) {
-    *reinterpret_cast<u32x2_a1*>(c) = x;
+    STORE_VEC(reinterpret_cast<u32x2_a1*>(c), x);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -385,20 +418,32 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t left, u3
   }
 }
 
-// One chunk: 8 elements a thread, 16 threads a group.
-template <int DW, int DG, bool FULL, int K>
-__device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int t, int64_t i, int64_t n, const Scalars& r) {
-  void* const W = a.t.ptr[0][t];
-  float* const ms = static_cast<float*>(a.t.ptr[3][t]);
-  float* const rs = static_cast<float*>(a.t.ptr[5][t]);
-  const int64_t left = n - i;  // 0 or less: nothing is there, but the group's other threads may need this one
-  const Raw<DW, 8> w8 = load_raw<DW, 8, FULL>(W, i, left);
-  const Raw<DG, 8> g8 = load_raw<DG, 8, FULL>(a.t.ptr[1][t], i, left);
-  const u32x2_t cm = load_codes<FULL>(a.t.ptr[2][t], i, left), cr = load_codes<FULL>(a.t.ptr[4][t], i, left);
+// One chunk, from element `base` on: 8 elements a thread, 16 threads a group.  NT
+// leaves the caches alone for what a wave takes in whole cache lines: 8 fp32
+// elements a thread come in two halves of 16 bytes, and these stay cached.
+template <int DW, int DG, bool FULL, bool NT, int K>
+__device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int t, int64_t base, int64_t n, const Scalars& r) {
+  // the block's pointers are scalars and a thread's offset has 32 bits
+  const int i = 8 * static_cast<int>(threadIdx.x), group = static_cast<int>(threadIdx.x) >> 4;
+  char* const W = static_cast<char*>(a.t.ptr[0][t]) + base * (DW == kF32 ? 4 : 2);
+  const char* const G = static_cast<const char*>(a.t.ptr[1][t]) + base * (DG == kF32 ? 4 : 2);
+  char* const mc = static_cast<char*>(a.t.ptr[2][t]) + base;
+  char* const rc = static_cast<char*>(a.t.ptr[4][t]) + base;
+  float* const ms = static_cast<float*>(a.t.ptr[3][t]) + base / kGroup;
+  float* const rs = static_cast<float*>(a.t.ptr[5][t]) + base / kGroup;
+  const int64_t left = n - base - i;  // 0 or less: nothing is there, but the group's other threads may need this one
+  const Raw<DW, 8> w8 = load_raw<DW, 8, FULL, NT && DW != kF32>(W, i, left);
+  const Raw<DG, 8> g8 = load_raw<DG, 8, FULL, NT && DG != kF32>(G, i, left);
+  const u32x2_t cm = load_codes<FULL, NT>(mc, i, left), cr = load_codes<FULL, NT>(rc, i, left);
   const bool any = FULL || left > 0;
-  const float sm = any ? ms[i / kGroup] : 0.0f, sr = any ? rs[i / kGroup] : 0.0f;
-  const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
-  float w[8], m[8], v[8], root[8], top_m = 0.0f, top_v = 0.0f;
+  const float sm = any ? ms[group] : 0.0f, sr = any ? rs[group] : 0.0f;
+  float g[8], m[8], v[8], root[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = raw_value(g8, k);
+  if (a.s.grad_scale != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] *= r.gs;
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t cmk = cm[k >> 2], crk = cr[k >> 2];
@@ -407,55 +452,67 @@ __device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int 
     m[k] = pm[k & 1] * sm;
     const float old = pr[k & 1] * sr;
     v[k] = old * old;
-    w[k] = raw_value(w8, k);
-    update8(w[k], raw_value(g8, k), m[k], v[k], root[k], a.s, r);
+    moments8(g[k], m[k], v[k], a.s);
+    root[k] = root_nearest(v[k]);
   }
-  store_values<DW, 8, FULL>(W, i, left, w);
   // the places of a tensor's last group behind its end hold zeros (codes and
   // gradients), which stay zeros and leave the group's largest values alone
+  const float group_m = group_max(m);
+  float group_root = group_max(root);
+  // In a group whose largest root is 2^-33 or more, one under 2^-51 (1 + 2^-23) gets
+  // the smallest code whatever it is exactly: 448 * 2^-18 is under the code step
+  // 2^-9.  Smaller roots, infinities and NaN take the general function.
+  if (!((group_root >= 0x1p-33f && group_root < INFINITY) || group_root == 0.0f)) {
 #pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    top_m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(m[k]), fabsf(m[k + 1])), top_m);
-    top_v = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[k], v[k + 1]), top_v);
+    for (int k = 0; k < 8; ++k) root[k] = sqrtf(v[k]);
+    group_root = group_max(root);
   }
-  const float sm2 = code_scale(group_max(__float_as_uint(top_m)));
-  const float sr2 = code_scale(__float_as_uint(sqrtf(__uint_as_float(group_max(__float_as_uint(top_v))))));
+  float w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = weight8(raw_value(w8, k), m[k], root[k], a.s, r);
+  store_values<DW, 8, FULL, NT && DW != kF32>(W, i, left, w);
+  const float sm2 = code_scale(group_m), sr2 = code_scale(group_root);
   const float im = code_inverse(sm2), ir = code_inverse(sr2);
+  const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
+  const uint32_t pair = (static_cast<uint32_t>(base >> 1) + key) + 4 * threadIdx.x;
   u32x2_t nm = {0, 0}, nr = {0, 0};
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
-    // at most 448 (1 + 2^-22), which rounds to 448
+    float u0, u1;
+    mix_chances(pair + k / 2, &u0, &u1);
+    const float lo = root_code_value(root[k] * ir, u0, v[k] > 0.0f);
+    const float hi = root_code_value(root[k + 1] * ir, u1, v[k + 1] > 0.0f);
+    // m: at most 448 (1 + 2^-22), which rounds to 448
     if (k & 2) {
       nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(m[k] * im, m[k + 1] * im, nm[k >> 2], true);
+      nr[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, nr[k >> 2], true);
     } else {
       nm[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(m[k] * im, m[k + 1] * im, nm[k >> 2], false);
+      nr[k >> 2] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, nr[k >> 2], false);
     }
-    const uint32_t h = mix(static_cast<uint32_t>((i + k) >> 1) + key);
-    nr[k >> 2] |= root_code(fminf(root[k] * ir, 448.0f), h & 0xffffu, v[k] > 0.0f) << (8 * (k & 3));
-    nr[k >> 2] |= root_code(fminf(root[k + 1] * ir, 448.0f), h >> 16, v[k + 1] > 0.0f) << (8 * (k & 3) + 8);
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {  // a group that is stored as zeros, or holds a NaN or an infinity
     nm[q] = im > 0.0f ? nm[q] : 0u;
     nr[q] = ir > 0.0f ? nr[q] : 0u;
   }
-  store_codes<FULL>(a.t.ptr[2][t], i, left, nm);
-  store_codes<FULL>(a.t.ptr[4][t], i, left, nr);
+  store_codes<FULL, NT>(mc, i, left, nm);
+  store_codes<FULL, NT>(rc, i, left, nr);
   if (any && (threadIdx.x & 15) == 0) {
-    ms[i / kGroup] = sm2;
-    rs[i / kGroup] = sr2;
+    ms[group] = sm2;
+    rs[group] = sr2;
   }
 }
 
-template <int DW, int DG, bool, int K>
+template <int DW, int DG, bool NT, int K>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(AdamwArgs<kPtrs8, K> a) {
   const int t = find_tensor(a.t, blockIdx.x);
   const int64_t n = a.t.size[t], base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8;
   const Scalars r = load_scalars(a.s);
   if (base + kChunk8 <= n) {
-    adamw8_chunk<DW, DG, true>(a, t, base + 8 * static_cast<int>(threadIdx.x), n, r);
+    adamw8_chunk<DW, DG, true, NT>(a, t, base, n, r);
   } else {
-    adamw8_chunk<DW, DG, false>(a, t, base + 8 * static_cast<int>(threadIdx.x), n, r);
+    adamw8_chunk<DW, DG, false, NT>(a, t, base, n, r);
   }
 }
 
@@ -485,7 +542,10 @@ muon_status make_scalars(const muon_adamw_config* cfg, AdamwScalars* s) {
   s->grad_scale = cfg->grad_scale;
   s->seed = cfg->seed;
   if (cfg->step_dev == nullptr) {
-    s->c1 = static_cast<float>(1.0 / (1.0 - pow(cfg->beta1, static_cast<double>(cfg->step))));
+    const double left = 1.0 - pow(cfg->beta1, static_cast<double>(cfg->step));
+    s->c1 = static_cast<float>(1.0 / left);
+    s->lr1 = static_cast<float>(s->lr / left);
+    s->wd1 = static_cast<float>(s->wd * left);
     s->c2 = static_cast<float>(1.0 / sqrt(1.0 - pow(cfg->beta2, static_cast<double>(cfg->step))));
   }
   return MUON_OK;
@@ -552,7 +612,17 @@ uint32_t fill_lists(Lists<P, K>* t, int tensors, const int64_t* sizes, const voi
 // A call that moves more than this passes the caches by (32-bit states).
 // Measured on bf16 W and G: 5.2 GB 5.43 -> 5.80 TB/s (fp32: 5.47 -> 5.90), 0.55 GB
 // 6.65 -> 5.91 TB/s when its tensors are still in the 256 MB cache from before.
-constexpr double kStreamBytes = 1 << 30;
+// 8-bit states (the codes and the 16-bit buffers): bf16 W and G 2.4 GB 423 -> 404 us,
+// 0.64 GB 113 -> 110, 0.48 GB 78 -> 82; fp32 W and G 3.8 GB 687 -> 664; fp32 W and
+// bf16 G 0.89 GB 162 -> 133, 0.44 GB 65 -> 70.  With fp32 W and G past them as well
+// 692 instead of 664 us.
+constexpr double kStreamBytes = 1 << 30, kStreamBytes8 = 1 << 29;
+
+double total_bytes(int tensors, const int64_t* sizes, double element) {
+  double bytes = 0.0;
+  for (int i = 0; i < tensors; ++i) bytes += static_cast<double>(sizes[i]) * element;
+  return bytes;
+}
 
 double element_bytes(muon_dtype w, muon_dtype g, double state_bytes) {
   return (w == MUON_F32 ? 8.0 : 4.0) + (g == MUON_F32 ? 4.0 : 2.0) + state_bytes;
@@ -583,9 +653,7 @@ template <int K>
 muon_status run32(const AdamwScalars& scalars, int tensors, const int64_t* sizes, const void* const* const* arrays,
                   muon_dtype w, muon_dtype g, hipStream_t s) {
   const double element = element_bytes(w, g, 16.0);
-  double bytes = 0.0;
-  for (int i = 0; i < tensors; ++i) bytes += static_cast<double>(sizes[i]) * element;
-  const bool stream = bytes > kStreamBytes;
+  const bool stream = total_bytes(tensors, sizes, element) > kStreamBytes;
   return run_lists<kPtrs32, K>(scalars, tensors, sizes, arrays, kChunk32, element, "adamw_kernel", "adamw", s,
                                [&](const AdamwArgs<kPtrs32, K>& a, uint32_t blocks) {
                                  if (stream) {
@@ -599,9 +667,15 @@ muon_status run32(const AdamwScalars& scalars, int tensors, const int64_t* sizes
 template <int K>
 muon_status run8(const AdamwScalars& scalars, int tensors, const int64_t* sizes, const void* const* const* arrays,
                  muon_dtype w, muon_dtype g, hipStream_t s) {
-  return run_lists<kPtrs8, K>(scalars, tensors, sizes, arrays, kChunk8, element_bytes(w, g, 4.0 + 16.0 / kGroup),
-                              "adamw8_kernel", "adamw8", s, [&](const AdamwArgs<kPtrs8, K>& a, uint32_t blocks) {
-                                ADAMW_TYPES(adamw8_kernel, false, K, a, blocks, w, g, s);
+  const double element = element_bytes(w, g, 4.0 + 16.0 / kGroup);
+  const bool stream = total_bytes(tensors, sizes, element) > kStreamBytes8;
+  return run_lists<kPtrs8, K>(scalars, tensors, sizes, arrays, kChunk8, element, "adamw8_kernel", "adamw8", s,
+                              [&](const AdamwArgs<kPtrs8, K>& a, uint32_t blocks) {
+                                if (stream) {
+                                  ADAMW_TYPES(adamw8_kernel, true, K, a, blocks, w, g, s);
+                                } else {
+                                  ADAMW_TYPES(adamw8_kernel, false, K, a, blocks, w, g, s);
+                                }
                               });
 }
 

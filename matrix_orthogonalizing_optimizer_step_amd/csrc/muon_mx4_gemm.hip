@@ -554,13 +554,13 @@ void split_k(int64_t tiles, int units, double elements, Mx4Plan* p) {
 
 // Which kernel, by the tiles there are for 256 compute units (times on bf16 C):
 //   at most 16 rows of A   B's codes are read once, straight into registers.
-//                          16x18944x3584: 10.1 us, 64 x 128 tiles 11.3
+//                          16x18944x3584: 9.3 us, 64 x 128 tiles 10.2
 //   256 x 256 tiles        where their last round leaves at most a third of the
-//                          compute units idle: 4096x4096x2048 (256 tiles) 29 us,
-//                          128 x 128 36; 2048x4096x8192 (128 tiles) 49 and 45
+//                          compute units idle: 4096x4096x2048 (256 tiles) 25.9 us,
+//                          128 x 128 28.3; 2048x4096x8192 (128 tiles) 46.9 and 42.1
 //   64 x 128 tiles         for at most 384 of them, split along k if they are
-//                          few: 512x3584x3584 (224) 11.0 us, 128 x 128 13.4;
-//                          256x18944x3584 (592) 23.7 and 21.0
+//                          few: 512x3584x3584 (224) 9.6 us, 128 x 128 11.4;
+//                          256x18944x3584 (592) 22.0 and 19.0
 //   128 x 128 tiles        otherwise.
 Mx4Plan mx4_plan(int batch, int m, int n, int k) {
   const int units = static_cast<int>(mx4_units(k));

@@ -305,6 +305,60 @@ def test_adamw8_tiny_gradients():
     assert ((1 - W[0])[big] > 0.01 * (1 + 0.83 + 0.69)).all()
 
 
+def test_adamw8_codes_of_tiny_second_moments():
+    """Groups whose second moments are subnormal, as a whole or beside large ones, and around the largest root of 2^-33
+    from which on the kernel takes its short root: codes of exactly the fp32 moments."""
+    rng = np.random.default_rng(31)
+    spread = [(-20.5, -17.6), (-19.0, -18.9), (-20.0, -12.0), (-20.0, -3.0), (-9.0, -8.3), (-10.0, -8.43), (-18.0, -8.42),
+              (-3.0, 0.0)]
+    mag = np.concatenate([10.0 ** rng.uniform(lo, hi, 128) for lo, hi in spread])
+    mag[::11] = 0.0
+    g = (mag * rng.choice([-1.0, 1.0], mag.size)).astype(np.float32)
+    W, G = [torch.ones(g.size, device=DEV)], [torch.from_numpy(g).to(DEV)]
+    state = mu.AdamW8State.zeros(W)
+    mu.adamw8_step(W, state, G, 1, 0.01, seed=77)
+    m = np.float32(1 - 0.9) * g
+    v = (np.float32(1 - 0.999) * g) * g
+    assert v.dtype == np.float32 and (v[:256] < 2.0 ** -126).all() and v[:256].any()
+    assert ao.check_moment_codes(bytes_of(state.m_codes[0]), f64(state.m_scales[0]), m.astype(np.float64), SLACK) == 0
+    bad = ao.check_root_codes(bytes_of(state.r_codes[0]), f64(state.r_scales[0]), v.astype(np.float64),
+                              ao.chances(g.size, 77, 1, 0), SLACK)
+    assert bad == 0, f"{bad} codes of the root of v"
+
+
+@pytest.mark.parametrize("w", ["f32", "bf16"])
+@pytest.mark.parametrize("g", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("eight", [False, True])
+def test_adamw_large_calls_compute_the_same(w, g, eight):
+    """A tensor beside one so large that the call leaves the caches alone: bit for bit what it is in a call of its own."""
+    W, M, V, G = make((70001, 4096), w, g, 32)
+    n = 100_000_000  # over 1 GB is moved with 32-bit and with 8-bit states
+
+    def run(extra):
+        P, Q = [x.clone() for x in W], list(G)
+        if extra:
+            P.append(torch.zeros(n, dtype=DT[w], device=DEV))
+            Q.append(torch.zeros(n, dtype=DT[g], device=DEV))
+        if eight:
+            s = state_of(M, V)
+            big = mu.AdamW8State.zeros(P[2:])
+            for a in ("m_codes", "m_scales", "r_codes", "r_scales"):
+                setattr(s, a, list(getattr(s, a)) + list(getattr(big, a)))
+            mu.adamw8_step(P, s, Q, 5, seed=4, **HYPER)
+            out = P[:2] + s.m_codes[:2] + s.m_scales[:2] + s.r_codes[:2] + s.r_scales[:2]
+        else:
+            A, B = [x.clone() for x in M], [x.clone() for x in V]
+            if extra:
+                A.append(torch.zeros(n, device=DEV))
+                B.append(torch.zeros(n, device=DEV))
+            mu.adamw_step(P, A, B, Q, 5, **HYPER)
+            out = P[:2] + A[:2] + B[:2]
+        assert not extra or not P[2].any()
+        return [x.view(torch.uint8).cpu() for x in out]
+
+    assert all(torch.equal(a, b) for a, b in zip(run(False), run(True)))
+
+
 def test_adamw8_several_steps_from_zero():
     W, _, _, _ = make((4096 + 77, 300), "f32", "f32", 22)
     state = mu.AdamW8State.zeros(W)
