@@ -53,6 +53,22 @@ def test_code_bit_for_bit(dtype, batch, rows, cols):
                 assert np.array_equal(f64(y), xo.decode(c.cpu().numpy(), s.cpu().numpy(), shape[1]))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cols", [2, 3, 4, 5, 6, 7, 32, 125, 130, 131, 253])
+def test_code_of_edge_tiles(dtype, cols):
+    """Every number of columns over a thread's four, rows that end anywhere in a tile, and a NaN and an infinity in the
+    last row and column, which belong to their own blocks only."""
+    for rows in (1, 33, 95, 129, 161):
+        X = matrices(1, rows, cols, dtype, 6)
+        for bad in (None, float("nan"), float("-inf")):
+            if bad is not None:
+                X[0][-1, -1] = bad
+            q, t = mu.mx4_quantize(X, transpose="both")
+            same_code(q, [f64(X[0])])
+            same_code(t, [f64(X[0]).T])
+            same_code(mu.mx4_quantize(X, transpose=True), [f64(X[0]).T])
+
+
 def test_code_of_every_bf16_value():
     """All finite bf16 values as elements of blocks whose largest magnitude is 7.9375 2^e: every rounding border and
     subnormal input, in both orientations."""
