@@ -20,7 +20,17 @@
 // (bf16 W and G) against 58 vector instructions, 3 of them at a quarter of the rate:
 // for 235M parameters some 395 us of memory beside 400 us of instructions, so both
 // count (with 71 instructions 439 us, with 58 428, then with accesses past the
-// caches 384).  Measured on 235M parameters: 32-bit states 5.83 TB/s (bf16 W and
+// caches 384).
+//
+// Accesses go past the caches: a training step lies between two calls, so nothing
+// of the call before is left there.  With cold caches that is as fast or faster at
+// almost every size, in us past / through them: 32-bit states, fp32 W and G 1M
+// elements 10.2 / 12.0, 12M 62.5 / 66.8, 24M 121 / 121, 96M 479 / 503 (24M with bf16
+// G 114 / 110); 8-bit states, bf16 W and G 1M 8.9 / 9.4, 24M 48.0 / 51.5, 96M 168 /
+// 180.  Called again and again on 0.55 GB, which then stay in the 256 MB cache in
+// part, the 32-bit step would be 12 % faster through them.
+//
+// Measured on 235M parameters: 32-bit states 5.83 TB/s (bf16 W and
 // G, 886 us) and 5.90 (fp32, 1114 us), 8-bit states 6.2 (384 us) and 5.70 (665 us);
 // a large copy reaches 4.8 and an addition in place 6.0.
 #include <math.h>
@@ -238,7 +248,7 @@ __device__ __forceinline__ void update(float& w, float g, float& m, float& v, co
   w = w - s.lr * (m * r.c1 / (sqrtf(v) * r.c2 + s.eps) + s.wd * w);
 }
 
-template <int DW, int DG, bool FULL, bool NT>
+template <int DW, int DG, bool FULL>
 __device__ __forceinline__ void adamw_chunk(void* W, const void* G, void* M, void* V, int64_t base, int64_t n,
                                             const AdamwScalars& s, const Scalars& r) {
   Raw<DW, 4> w4[kQuads];
@@ -247,10 +257,10 @@ __device__ __forceinline__ void adamw_chunk(void* W, const void* G, void* M, voi
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
     const int64_t i = base + (q * kThreads + static_cast<int>(threadIdx.x)) * 4;
-    w4[q] = load_raw<DW, 4, FULL, NT>(W, i, n - i);
-    g4[q] = load_raw<DG, 4, FULL, NT>(G, i, n - i);
-    m4[q] = load_raw<kF32, 4, FULL, NT>(M, i, n - i);
-    v4[q] = load_raw<kF32, 4, FULL, NT>(V, i, n - i);
+    w4[q] = load_raw<DW, 4, FULL, true>(W, i, n - i);
+    g4[q] = load_raw<DG, 4, FULL, true>(G, i, n - i);
+    m4[q] = load_raw<kF32, 4, FULL, true>(M, i, n - i);
+    v4[q] = load_raw<kF32, 4, FULL, true>(V, i, n - i);
   }
 #pragma unroll
   for (int q = 0; q < kQuads; ++q) {
@@ -263,23 +273,21 @@ __device__ __forceinline__ void adamw_chunk(void* W, const void* G, void* M, voi
       v[k] = raw_value(v4[q], k);
       update(w[k], raw_value(g4[q], k), m[k], v[k], s, r);
     }
-    store_values<kF32, 4, FULL, NT>(M, i, n - i, m);
-    store_values<kF32, 4, FULL, NT>(V, i, n - i, v);
-    store_values<DW, 4, FULL, NT>(W, i, n - i, w);
+    store_values<kF32, 4, FULL, true>(M, i, n - i, m);
+    store_values<kF32, 4, FULL, true>(V, i, n - i, v);
+    store_values<DW, 4, FULL, true>(W, i, n - i, w);
   }
 }
 
-// NT: accesses that leave the caches alone, for calls that stream far more than
-// the caches hold.
-template <int DW, int DG, bool NT, int K>
+template <int DW, int DG, int K>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwArgs<kPtrs32, K> a) {
   const int t = find_tensor(a.t, blockIdx.x);
   const int64_t n = a.t.size[t], base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk32;
   const Scalars r = load_scalars(a.s);
   if (base + kChunk32 <= n) {
-    adamw_chunk<DW, DG, true, NT>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
+    adamw_chunk<DW, DG, true>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
   } else {
-    adamw_chunk<DW, DG, false, NT>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
+    adamw_chunk<DW, DG, false>(a.t.ptr[0][t], a.t.ptr[1][t], a.t.ptr[2][t], a.t.ptr[3][t], base, n, a.s, r);
   }
 }
 
@@ -396,21 +404,21 @@ __device__ __forceinline__ float group_max(const float (&v)[8]) {
 }
 
 // 8 code bytes.
-template <bool FULL, bool NT>
+template <bool FULL>
 __device__ __forceinline__ u32x2_t load_codes(const void* p, int64_t i, int64_t left) {
   const uint8_t* c = static_cast<const uint8_t*>(p) + i;
-  if (FULL || left >= 8) return LOAD_VEC(reinterpret_cast<const u32x2_a1*>(c));
+  if (FULL || left >= 8) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_a1*>(c));
   u32x2_t r = {0, 0};
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (k < left) r[k >> 2] |= static_cast<uint32_t>(c[k]) << (8 * (k & 3));
   return r;
 }
-template <bool FULL, bool NT>
+template <bool FULL>
 __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t left, u32x2_t x) {
   uint8_t* c = static_cast<uint8_t*>(p) + i;
   if (FULL || left >= 8) {
-    STORE_VEC(reinterpret_cast<u32x2_a1*>(c), x);
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x2_a1*>(c));
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -418,10 +426,10 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t left, u3
   }
 }
 
-// One chunk, from element `base` on: 8 elements a thread, 16 threads a group.  NT
-// leaves the caches alone for what a wave takes in whole cache lines: 8 fp32
-// elements a thread come in two halves of 16 bytes, and these stay cached.
-template <int DW, int DG, bool FULL, bool NT, int K>
+// One chunk, from element `base` on: 8 elements a thread, 16 threads a group.  Of
+// fp32 a thread has two halves of 16 bytes, so that two loads share each cache line,
+// and W and G in fp32 go through the caches (235M elements 664 us, past them 692).
+template <int DW, int DG, bool FULL, int K>
 __device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int t, int64_t base, int64_t n, const Scalars& r) {
   // the block's pointers are scalars and a thread's offset has 32 bits
   const int i = 8 * static_cast<int>(threadIdx.x), group = static_cast<int>(threadIdx.x) >> 4;
@@ -432,9 +440,9 @@ __device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int 
   float* const ms = static_cast<float*>(a.t.ptr[3][t]) + base / kGroup;
   float* const rs = static_cast<float*>(a.t.ptr[5][t]) + base / kGroup;
   const int64_t left = n - base - i;  // 0 or less: nothing is there, but the group's other threads may need this one
-  const Raw<DW, 8> w8 = load_raw<DW, 8, FULL, NT && DW != kF32>(W, i, left);
-  const Raw<DG, 8> g8 = load_raw<DG, 8, FULL, NT && DG != kF32>(G, i, left);
-  const u32x2_t cm = load_codes<FULL, NT>(mc, i, left), cr = load_codes<FULL, NT>(rc, i, left);
+  const Raw<DW, 8> w8 = load_raw<DW, 8, FULL, DW != kF32>(W, i, left);
+  const Raw<DG, 8> g8 = load_raw<DG, 8, FULL, DG != kF32>(G, i, left);
+  const u32x2_t cm = load_codes<FULL>(mc, i, left), cr = load_codes<FULL>(rc, i, left);
   const bool any = FULL || left > 0;
   const float sm = any ? ms[group] : 0.0f, sr = any ? rs[group] : 0.0f;
   float g[8], m[8], v[8], root[8];
@@ -470,7 +478,7 @@ __device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int 
   float w[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) w[k] = weight8(raw_value(w8, k), m[k], root[k], a.s, r);
-  store_values<DW, 8, FULL, NT && DW != kF32>(W, i, left, w);
+  store_values<DW, 8, FULL, DW != kF32>(W, i, left, w);
   const float sm2 = code_scale(group_m), sr2 = code_scale(group_root);
   const float im = code_inverse(sm2), ir = code_inverse(sr2);
   const uint32_t key = mix(a.s.seed + mix(static_cast<uint32_t>(r.step) + mix(static_cast<uint32_t>(a.t.first + t))));
@@ -496,23 +504,23 @@ __device__ __forceinline__ void adamw8_chunk(const AdamwArgs<kPtrs8, K>& a, int 
     nm[q] = im > 0.0f ? nm[q] : 0u;
     nr[q] = ir > 0.0f ? nr[q] : 0u;
   }
-  store_codes<FULL, NT>(mc, i, left, nm);
-  store_codes<FULL, NT>(rc, i, left, nr);
+  store_codes<FULL>(mc, i, left, nm);
+  store_codes<FULL>(rc, i, left, nr);
   if (any && (threadIdx.x & 15) == 0) {
     ms[group] = sm2;
     rs[group] = sr2;
   }
 }
 
-template <int DW, int DG, bool NT, int K>
+template <int DW, int DG, int K>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(AdamwArgs<kPtrs8, K> a) {
   const int t = find_tensor(a.t, blockIdx.x);
   const int64_t n = a.t.size[t], base = static_cast<int64_t>(blockIdx.x - a.t.start[t]) * kChunk8;
   const Scalars r = load_scalars(a.s);
   if (base + kChunk8 <= n) {
-    adamw8_chunk<DW, DG, true, NT>(a, t, base, n, r);
+    adamw8_chunk<DW, DG, true>(a, t, base, n, r);
   } else {
-    adamw8_chunk<DW, DG, false, NT>(a, t, base, n, r);
+    adamw8_chunk<DW, DG, false>(a, t, base, n, r);
   }
 }
 
@@ -594,35 +602,20 @@ uint32_t fill_lists(Lists<P, K>* t, int tensors, const int64_t* sizes, const voi
   return blocks;
 }
 
-// Launches of `kernel<DW, DG, NT, K>` over the list.
-#define ADAMW_TYPES(kernel, NT, K, args, blocks, w, g, s)                                                     \
-  do {                                                                                                        \
-    const dim3 grid_(blocks), block_(kThreads);                                                               \
-    if ((w) == MUON_F32) {                                                                                    \
-      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kF32, kF32, NT, K>), grid_, block_, 0, s, args);        \
-      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kF32, kBF16, NT, K>), grid_, block_, 0, s, args); \
-      else hipLaunchKernelGGL((kernel<kF32, kF16, NT, K>), grid_, block_, 0, s, args);                        \
-    } else {                                                                                                  \
-      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kBF16, kF32, NT, K>), grid_, block_, 0, s, args);       \
-      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kBF16, kBF16, NT, K>), grid_, block_, 0, s, args);\
-      else hipLaunchKernelGGL((kernel<kBF16, kF16, NT, K>), grid_, block_, 0, s, args);                       \
-    }                                                                                                         \
+// A launch of `kernel<DW, DG, K>`.
+#define ADAMW_TYPES(kernel, K, args, blocks, w, g, s)                                                     \
+  do {                                                                                                    \
+    const dim3 grid_(blocks), block_(kThreads);                                                           \
+    if ((w) == MUON_F32) {                                                                                \
+      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kF32, kF32, K>), grid_, block_, 0, s, args);        \
+      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kF32, kBF16, K>), grid_, block_, 0, s, args); \
+      else hipLaunchKernelGGL((kernel<kF32, kF16, K>), grid_, block_, 0, s, args);                        \
+    } else {                                                                                              \
+      if ((g) == MUON_F32) hipLaunchKernelGGL((kernel<kBF16, kF32, K>), grid_, block_, 0, s, args);       \
+      else if ((g) == MUON_BF16) hipLaunchKernelGGL((kernel<kBF16, kBF16, K>), grid_, block_, 0, s, args);\
+      else hipLaunchKernelGGL((kernel<kBF16, kF16, K>), grid_, block_, 0, s, args);                       \
+    }                                                                                                     \
   } while (0)
-
-// A call that moves more than this passes the caches by (32-bit states).
-// Measured on bf16 W and G: 5.2 GB 5.43 -> 5.80 TB/s (fp32: 5.47 -> 5.90), 0.55 GB
-// 6.65 -> 5.91 TB/s when its tensors are still in the 256 MB cache from before.
-// 8-bit states (the codes and the 16-bit buffers): bf16 W and G 2.4 GB 423 -> 404 us,
-// 0.64 GB 113 -> 110, 0.48 GB 78 -> 82; fp32 W and G 3.8 GB 687 -> 664; fp32 W and
-// bf16 G 0.89 GB 162 -> 133, 0.44 GB 65 -> 70.  With fp32 W and G past them as well
-// 692 instead of 664 us.
-constexpr double kStreamBytes = 1 << 30, kStreamBytes8 = 1 << 29;
-
-double total_bytes(int tensors, const int64_t* sizes, double element) {
-  double bytes = 0.0;
-  for (int i = 0; i < tensors; ++i) bytes += static_cast<double>(sizes[i]) * element;
-  return bytes;
-}
 
 double element_bytes(muon_dtype w, muon_dtype g, double state_bytes) {
   return (w == MUON_F32 ? 8.0 : 4.0) + (g == MUON_F32 ? 4.0 : 2.0) + state_bytes;
@@ -652,30 +645,18 @@ muon_status run_lists(const AdamwScalars& scalars, int tensors, const int64_t* s
 template <int K>
 muon_status run32(const AdamwScalars& scalars, int tensors, const int64_t* sizes, const void* const* const* arrays,
                   muon_dtype w, muon_dtype g, hipStream_t s) {
-  const double element = element_bytes(w, g, 16.0);
-  const bool stream = total_bytes(tensors, sizes, element) > kStreamBytes;
-  return run_lists<kPtrs32, K>(scalars, tensors, sizes, arrays, kChunk32, element, "adamw_kernel", "adamw", s,
-                               [&](const AdamwArgs<kPtrs32, K>& a, uint32_t blocks) {
-                                 if (stream) {
-                                   ADAMW_TYPES(adamw_kernel, true, K, a, blocks, w, g, s);
-                                 } else {
-                                   ADAMW_TYPES(adamw_kernel, false, K, a, blocks, w, g, s);
-                                 }
+  return run_lists<kPtrs32, K>(scalars, tensors, sizes, arrays, kChunk32, element_bytes(w, g, 16.0), "adamw_kernel",
+                               "adamw", s, [&](const AdamwArgs<kPtrs32, K>& a, uint32_t blocks) {
+                                 ADAMW_TYPES(adamw_kernel, K, a, blocks, w, g, s);
                                });
 }
 
 template <int K>
 muon_status run8(const AdamwScalars& scalars, int tensors, const int64_t* sizes, const void* const* const* arrays,
                  muon_dtype w, muon_dtype g, hipStream_t s) {
-  const double element = element_bytes(w, g, 4.0 + 16.0 / kGroup);
-  const bool stream = total_bytes(tensors, sizes, element) > kStreamBytes8;
-  return run_lists<kPtrs8, K>(scalars, tensors, sizes, arrays, kChunk8, element, "adamw8_kernel", "adamw8", s,
-                              [&](const AdamwArgs<kPtrs8, K>& a, uint32_t blocks) {
-                                if (stream) {
-                                  ADAMW_TYPES(adamw8_kernel, true, K, a, blocks, w, g, s);
-                                } else {
-                                  ADAMW_TYPES(adamw8_kernel, false, K, a, blocks, w, g, s);
-                                }
+  return run_lists<kPtrs8, K>(scalars, tensors, sizes, arrays, kChunk8, element_bytes(w, g, 4.0 + 16.0 / kGroup),
+                              "adamw8_kernel", "adamw8", s, [&](const AdamwArgs<kPtrs8, K>& a, uint32_t blocks) {
+                                ADAMW_TYPES(adamw8_kernel, K, a, blocks, w, g, s);
                               });
 }
 

@@ -100,18 +100,18 @@ __device__ __forceinline__ void load_unit(typename T::Stage& st, const Source& A
   const __amdgpu_buffer_rsrc_t ca = make_rsrc(A.code, la * 64u, (A.lines - la) * 64u);
   const __amdgpu_buffer_rsrc_t cb = make_rsrc(B.code, lb * 64u, (B.lines - lb) * 64u);
   lds_ptr_t da = (lds_ptr_t)(st.code + wave * RA * 4), db = (lds_ptr_t)(st.code + (T::TM + wave * RB) * 4);
-#define MX4_LOAD(N, R, RSRC, DST, VOFF, OFF)                    \
-  if constexpr (FIRST <= (N) && (N) < LAST && (OFF) < (R) * 64) \
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(RSRC, DST, 16, VOFF, 0, OFF, 0)
+#define MX4_LOAD(N, R, RSRC, DST, VOFF, PIECE)                            \
+  if constexpr (FIRST <= (N) && (N) < LAST && (PIECE) * 1024 < (R) * 64)  \
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(RSRC, DST, 16, VOFF, 0, (PIECE) * 1024, 0)
   constexpr int NA = RA / 16, NB = RB / 16;
   MX4_LOAD(0, RA, ca, da, A.vcode, 0);
-  MX4_LOAD(1, RA, ca, da, A.vcode, 1024);
-  MX4_LOAD(2, RA, ca, da, A.vcode, 2048);
-  MX4_LOAD(3, RA, ca, da, A.vcode, 3072);
+  MX4_LOAD(1, RA, ca, da, A.vcode, 1);
+  MX4_LOAD(2, RA, ca, da, A.vcode, 2);
+  MX4_LOAD(3, RA, ca, da, A.vcode, 3);
   MX4_LOAD(NA, RB, cb, db, B.vcode, 0);
-  MX4_LOAD(NA + 1, RB, cb, db, B.vcode, 1024);
-  MX4_LOAD(NA + 2, RB, cb, db, B.vcode, 2048);
-  MX4_LOAD(NA + 3, RB, cb, db, B.vcode, 3072);
+  MX4_LOAD(NA + 1, RB, cb, db, B.vcode, 1);
+  MX4_LOAD(NA + 2, RB, cb, db, B.vcode, 2);
+  MX4_LOAD(NA + 3, RB, cb, db, B.vcode, 3);
 #undef MX4_LOAD
   static_assert(RA <= 64 && RB <= 64 && NA + NB + 2 == T::kLoads, "loads of a unit");
   if constexpr (FIRST <= NA + NB && NA + NB < LAST) {

@@ -330,9 +330,9 @@ def test_adamw8_codes_of_tiny_second_moments():
 @pytest.mark.parametrize("g", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("eight", [False, True])
 def test_adamw_large_calls_compute_the_same(w, g, eight):
-    """A tensor beside one so large that the call leaves the caches alone: bit for bit what it is in a call of its own."""
+    """A tensor beside a large one: bit for bit what it is in a call of its own."""
     W, M, V, G = make((70001, 4096), w, g, 32)
-    n = 100_000_000  # over 1 GB is moved with 32-bit and with 8-bit states
+    n = 100_000_000
 
     def run(extra):
         P, Q = [x.clone() for x in W], list(G)
