@@ -326,6 +326,65 @@ def test_adamw8_codes_of_tiny_second_moments():
     assert bad == 0, f"{bad} codes of the root of v"
 
 
+def moments32(s, g, t):
+    """The fp32 moments of a step as the library rounds them (one rounding for each product and sum), subnormals
+    kept."""
+    b1, b2, o1, o2 = (np.float32(x) for x in (s["beta1"], s["beta2"], 1 - s["beta1"], 1 - s["beta2"]))
+    m, v = b1 * s["m"] + o1 * g, b2 * s["v"] + (o2 * g) * g
+    assert m.dtype == np.float32 and v.dtype == np.float32
+    return m, v
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 1e-20, 1e-15, 1e-10, 1e-8])
+def test_adamw_weights_of_tiny_second_moments(eight, beta2, eps):
+    """Second moments that are subnormal, alone in their group or beside large ones, with every kind of eps: W is the
+    step on exactly the fp32 moments.
+
+    Half a step is h = 2^-24.  Of the step's quotient: c1 and its product 2 h; of the denominator the root 1.5 h (nearest
+    from 2^-102 on and wherever eps lets it be seen; otherwise another 2^-25 of the denominator), c2 and its product 2 h,
+    eps and the sum 2 h; the quotient by v_rcp_f32 2 h and its product h (nearest: h); lr and its product 2 h: at most
+    13 h.  Decay: wd, lr and their products with the sum 5 h.  The result's own rounding h."""
+    rng = np.random.default_rng(33)
+    spread = [(-23.0, -17.0), (-22.5, -19.0), (-21.0, -3.0), (-24.0, 0.0), (-18.5, -15.0), (-3.0, 0.0)]
+    mag = np.concatenate([10.0 ** rng.uniform(lo, hi, 256) for lo, hi in spread])
+    mag[::13] = 0.0
+    mag[5::128][::2] = 1.0  # every second group has a large neighbour
+    lr, wd = 0.01, 0.1
+    hyper = dict(lr=lr, beta1=0.9, beta2=beta2, eps=eps, weight_decay=wd)
+    w0 = np.where(np.arange(mag.size) % 2 == 0, 0.0, rng.standard_normal(mag.size)).astype(np.float32)
+    W = [torch.from_numpy(w0).to(DEV)]
+    zero = np.zeros(mag.size, dtype=np.float32)
+    M, V, state = [torch.zeros_like(W[0])], [torch.zeros_like(W[0])], mu.AdamW8State.zeros(W)
+    s = dict(beta1=0.9, beta2=beta2, m=zero, v=zero)
+    h = 2.0 ** -24
+    for t in (1, 2, 3):
+        g = (mag * rng.choice([-1.0, 1.0], mag.size) * rng.uniform(0.5, 2.0, mag.size)).astype(np.float32)
+        G, w_old = [torch.from_numpy(g).to(DEV)], f64(W[0])
+        m, v = moments32(s, g, t)
+        if eight:
+            mu.adamw8_step(W, state, G, t, seed=5, **hyper)
+        else:
+            mu.adamw_step(W, M, V, G, t, **hyper)
+            assert np.array_equal(M[0].cpu().numpy(), m) and np.array_equal(V[0].cpu().numpy(), v)
+        assert t > 1 or ((v > 0) & (v < 2.0 ** -126)).sum() > 100
+        step = lr * (m / (1 - 0.9 ** t)) / (np.sqrt(v.astype(np.float64)) / np.sqrt(1 - beta2 ** t) + eps)
+        want = w_old - step - lr * wd * w_old
+        bound = 13 * h * np.abs(step) + 5 * h * lr * wd * np.abs(w_old) + 2 * h * np.abs(want) + 2.0 ** -149
+        off = np.abs(f64(W[0]) - want)
+        assert np.all(off <= bound), f"t = {t}: {np.sum(off > bound)} weights, worst {np.max(off / bound):.3g} bounds"
+        if eight:
+            assert ao.check_moment_codes(bytes_of(state.m_codes[0]), f64(state.m_scales[0]), m.astype(np.float64), SLACK) == 0
+            assert ao.check_root_codes(bytes_of(state.r_codes[0]), f64(state.r_scales[0]), v.astype(np.float64),
+                                       ao.chances(g.size, 5, t, 0), SLACK) == 0
+            codes = [c[0].float().cpu().numpy() * np.repeat(x[0].cpu().numpy(), 128)
+                     for c, x in ((state.m_codes, state.m_scales), (state.r_codes, state.r_scales))]
+            s.update(m=codes[0], v=codes[1] * codes[1])
+        else:
+            s.update(m=m, v=v)
+
+
 @pytest.mark.parametrize("w", ["f32", "bf16"])
 @pytest.mark.parametrize("g", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("eight", [False, True])
