@@ -398,7 +398,8 @@ muon_status muon_adamw_step(int tensors, const int64_t *sizes, void *const *W, m
  *   state     HOST arrays of device pointers, updated in place: codes of
  *             sizes[j] bytes, scales of ceil(sizes[j] / 128) floats.  The first
  *             step of a run passes zeros.  One launch per 64 tensors.
- * Everything else as for muon_adamw_step.
+ * Everything else as for muon_adamw_step; MUON_ERR_INVALID_ARG also where lr / (1 -
+ * beta1) is not finite in fp32 or eps is over 2^126.
  */
 typedef struct muon_adamw8_state {
   void *const *m_codes;

@@ -720,6 +720,9 @@ muon_status muon_adamw8_step(int tensors, const int64_t* sizes, void* const* W, 
   AdamwScalars scalars;
   st = make_scalars(cfg, &scalars);
   if (st != MUON_OK) return st;
+  // weight8's quotients in fp32: lr c1, largest at t = 1, and 1 / eps in the normal range
+  if (!isfinite(static_cast<float>(scalars.lr / (1.0 - cfg->beta1))) || !(scalars.eps <= 0x1p126f))
+    return MUON_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   return tensors <= kFew ? run8<kFew>(scalars, tensors, sizes, arrays, w_dtype, g_dtype, s)
                          : run8<many_tensors(kPtrs8)>(scalars, tensors, sizes, arrays, w_dtype, g_dtype, s);

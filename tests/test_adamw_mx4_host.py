@@ -139,6 +139,19 @@ def test_empty_tensors_need_no_device():
     assert _adamw(mu.load_library(), tensors=3, sizes=(0, 0, 0), W=none[0], M=none[1], V=none[2], G=none[3]) == (0, 0)
 
 
+def test_adamw8_refuses_what_its_quotients_cannot_hold():
+    """The 8-bit step works with lr / (1 - beta1^t) and 1 / (c2 root + eps) in fp32: values whose quotients overflow (at
+    t = 1, the largest) or fall under the normal range are refused there; the 32-bit step has neither quotient."""
+    lib = mu.load_library()
+    none = [ptrs(None, None, None) for _ in range(4)]
+    empty = dict(tensors=1, sizes=(0,), W=none[0], M=none[1], V=none[2], G=none[3])
+    for kw in (dict(lr=1e38), dict(lr=3.4e38), dict(lr=-1e38), dict(lr=1e30, beta1=1 - 2.0 ** -40), dict(eps=1e38),
+               dict(eps=2.0 ** 126 * 1.001)):
+        assert _adamw(lib, **empty, **kw) == (0, 1), kw
+    for kw in (dict(lr=3e37), dict(lr=3.4e38, beta1=0.0), dict(lr=1e20, beta1=1 - 2.0 ** -40), dict(eps=2.0 ** 126)):
+        assert _adamw(lib, **empty, **kw) == (0, 0), kw
+
+
 def test_adamw_binding_refusals():
     z = torch.zeros(4)
     with pytest.raises(ValueError, match="empty list"):
