@@ -10,7 +10,8 @@ fails, an exception is raised.
 The entry points that take lists of parameters or one layer's matrices (the
 AdamW steps, the microscaled 4-bit code and product) go through the extension
 module ``_native``, which checks the tensors and calls the same C ABI at the
-cost of a launch.
+cost of a launch.  It is loaded at the first of them: the other calls need the
+library alone.
 """
 from __future__ import annotations
 
@@ -68,21 +69,57 @@ class _GraspState(ctypes.Structure):
 
 _lib = None
 _native = None
+_LIST_CALLS = ("muon_adamw_step", "muon_adamw8_step", "muon_mx4_quantize", "muon_mx4_dequantize",
+               "muon_mx4_workspace_size", "muon_mx4_matmul")
+
+
+def _require_list_calls(lib):
+    missing = [name for name in _LIST_CALLS if not hasattr(lib, name)]
+    if missing:
+        raise ImportError(f"{LIB_PATH} has no {missing[0]}: it is an older build of the library")
 
 
 def _load_native():
-    """The extension module (raises ImportError if it has not been built)."""
+    """The extension module, bound to the library; only the calls that go through it need it (raises ImportError if it
+    has not been built or the library lacks those calls)."""
+    global _native
+    if _native is not None:
+        return _native
+    lib = load_library()
+    _require_list_calls(lib)
     try:
         from . import _native as module
     except ImportError as e:
         raise ImportError(f"_native.so is missing or does not fit this PyTorch ({e}): build it with "
                           "`python -m matrix_orthogonalizing_optimizer_step_amd._build`") from e
+    module.bind_library({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _LIST_CALLS},
+                        torch._C._cuda_getCurrentRawStream)
+    _native = module
     return module
+
+
+def _declare_list_calls(lib):
+    vp, i32 = ctypes.c_void_p, ctypes.c_int
+    sizes, acfg = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_AdamWConfig)
+    lib.muon_adamw_config_init.argtypes = [acfg]
+    lib.muon_adamw_config_init.restype = None
+    lib.muon_adamw_step.argtypes = [i32, sizes, vp, i32, vp, vp, vp, i32, acfg, vp]
+    lib.muon_adamw_step.restype = i32
+    lib.muon_adamw8_step.argtypes = [i32, sizes, vp, i32, ctypes.POINTER(_AdamW8State), vp, i32, acfg, vp]
+    lib.muon_adamw8_step.restype = i32
+    lib.muon_mx4_quantize.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp]
+    lib.muon_mx4_quantize.restype = i32
+    lib.muon_mx4_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, vp]
+    lib.muon_mx4_dequantize.restype = i32
+    lib.muon_mx4_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.muon_mx4_workspace_size.restype = ctypes.c_size_t
+    lib.muon_mx4_matmul.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.muon_mx4_matmul.restype = i32
 
 
 def load_library():
     """Load libmuon.so once; raises ImportError if it has not been built."""
-    global _lib, _native
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -133,27 +170,8 @@ def load_library():
     for name in ("muon_group8_quantize", "muon_group8_dequantize"):
         getattr(lib, name).argtypes = [i32, i32, i32, vp, vp, vp, vp]
         getattr(lib, name).restype = i32
-    sizes, acfg = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_AdamWConfig)
-    names = ("muon_adamw_step", "muon_adamw8_step", "muon_mx4_quantize", "muon_mx4_dequantize",
-             "muon_mx4_workspace_size", "muon_mx4_matmul")
-    lib.muon_adamw_config_init.argtypes = [acfg]
-    lib.muon_adamw_config_init.restype = None
-    lib.muon_adamw_step.argtypes = [i32, sizes, vp, i32, vp, vp, vp, i32, acfg, vp]
-    lib.muon_adamw_step.restype = i32
-    lib.muon_adamw8_step.argtypes = [i32, sizes, vp, i32, ctypes.POINTER(_AdamW8State), vp, i32, acfg, vp]
-    lib.muon_adamw8_step.restype = i32
-    lib.muon_mx4_quantize.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp]
-    lib.muon_mx4_quantize.restype = i32
-    lib.muon_mx4_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, vp]
-    lib.muon_mx4_dequantize.restype = i32
-    lib.muon_mx4_workspace_size.argtypes = [i32, i32, i32, i32]
-    lib.muon_mx4_workspace_size.restype = sz
-    lib.muon_mx4_matmul.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, sz, vp]
-    lib.muon_mx4_matmul.restype = i32
-    native = _load_native()
-    native.bind_library({name: ctypes.cast(getattr(lib, name), vp).value for name in names},
-                        torch._C._cuda_getCurrentRawStream)
-    _native = native
+    if all(hasattr(lib, name) for name in _LIST_CALLS):  # an older build is fine for the other calls
+        _declare_list_calls(lib)
     _lib = lib
     return lib
 
@@ -666,9 +684,7 @@ def _on_stream(stream, tensors):
 
 def _call(entry: str, stream, tensors, *args):
     """Calls an entry of the extension module on ``stream`` (None = the current stream of the tensors' device)."""
-    if _native is None:
-        load_library()
-    f = getattr(_native, entry)
+    f = getattr(_native or _load_native(), entry)
     if stream is None:
         return f(*args)
     with _on_stream(stream, tensors):
@@ -761,7 +777,9 @@ def mx4_matmul(A: MX4, B: MX4, dtype=torch.bfloat16, out=None, accumulate: bool 
 
 def mx4_workspace_size(batch: int, m: int, n: int, k: int) -> int:
     """Bytes of workspace mx4_matmul needs (see muon_mx4_workspace_size in include/muon.h)."""
-    n = load_library().muon_mx4_workspace_size(batch, m, n, k)
+    lib = load_library()
+    _require_list_calls(lib)
+    n = lib.muon_mx4_workspace_size(batch, m, n, k)
     if n == 0:
         raise MuonError(1, "invalid arguments for the workspace size")
     return int(n)
