@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import os
 import shutil
+import signal
 import subprocess
 import sys
 import tempfile
@@ -39,7 +40,8 @@ def hipcc() -> str:
 def _run(cmd: list[str], verbose: bool) -> subprocess.Popen:
     if verbose:
         print(" ".join(cmd), flush=True)
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    # a process group of its own: a compiler driver's passes end with it
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, start_new_session=True)
 
 
 def _finish(proc: subprocess.Popen, what: str, verbose: bool) -> None:
@@ -47,7 +49,7 @@ def _finish(proc: subprocess.Popen, what: str, verbose: bool) -> None:
     noise = "is not a recognized feature for this target"
     msgs = "\n".join(l for l in out.splitlines() if noise not in l)
     if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {what} ({proc.returncode}):\n{msgs}")
+        raise RuntimeError(f"{os.path.basename(proc.args[0])} failed on {what} ({proc.returncode}):\n{msgs}")
     if verbose and msgs.strip():
         print(msgs, file=sys.stderr)
 
@@ -71,14 +73,19 @@ NATIVE_SOURCE = os.path.join(HERE, "native", "muon_native.cpp")
 NATIVE = os.path.join(HERE, "_native.so")
 
 
-def _native_command(out: str) -> list[str]:
-    """Host compiler line of the extension module (torch's headers and ABI, no device code)."""
+def _native_command(out: str) -> list[str] | None:
+    """Host compiler line of the extension module (torch's headers and ABI, no device code); None without torch or a
+    host compiler, which the library itself does not need."""
     import sysconfig
 
-    import torch
-    from torch.utils.cpp_extension import include_paths, library_paths
-
-    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths, library_paths
+    except ImportError:
+        return None
+    if cxx is None:
+        return None
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-DTORCH_API_INCLUDE_EXTENSION_H",
@@ -88,32 +95,49 @@ def _native_command(out: str) -> list[str]:
 
 
 def build(verbose: bool = False, csrc: str = CSRC, lib: str = LIB, defines=(), sanitize: bool = False) -> str:
-    """Always recompiles (one process per source, in parallel); writes the
-    library (default libmuon.so next to this file) atomically and returns its
-    path.  ``csrc``, ``lib`` and ``defines`` (-D flags) build a variant;
+    """Always recompiles (one process per source, in parallel); once all of it
+    has compiled, puts the library (default libmuon.so next to this file, and
+    with it the extension module) in place atomically and returns its path.  ``csrc``, ``lib`` and ``defines`` (-D flags) build a variant;
     ``sanitize`` instruments the host code (see SANITIZE_COMPILE)."""
     objdir = tempfile.mkdtemp(prefix="muon_build_")
-    native = None
-    if lib == LIB:  # a variant of the library uses the same extension module
-        native = _run(_native_command(NATIVE + ".tmp"), verbose)
+    san = SANITIZE_COMPILE if sanitize else []
+    started, made = [], {}  # processes; finished outputs and where they go
+
+    def start(cmd):
+        started.append(_run(cmd, verbose))
+        return started[-1]
+
     try:
-        objs, procs = [], []
-        for src in SOURCES:
-            obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
-            objs.append(obj)
-            san = SANITIZE_COMPILE if sanitize else []
-            procs.append((src, _run([hipcc(), *HIPCC_FLAGS, *san, *[f"-D{d}" for d in defines], "-c", "-o", obj,
-                                     os.path.join(csrc, src)], verbose)))
+        native = None
+        if lib == LIB:  # a variant of the library uses the same extension module
+            made[NATIVE] = NATIVE + ".tmp"
+            command = _native_command(made[NATIVE])
+            native = start(command) if command is not None else None
+        objs = [os.path.join(objdir, os.path.splitext(src)[0] + ".o") for src in SOURCES]
+        procs = [(src, start([hipcc(), *HIPCC_FLAGS, *san, *[f"-D{d}" for d in defines], "-c", "-o", obj,
+                              os.path.join(csrc, src)])) for src, obj in zip(SOURCES, objs)]
         for src, proc in procs:
             _finish(proc, src, verbose)
-        tmp = lib + ".tmp"
-        _finish(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *(SANITIZE_LINK if sanitize else []),
-                      "-o", tmp, *objs], verbose), "link", verbose)
-        os.replace(tmp, lib)
+        made[lib] = lib + ".tmp"
+        _finish(start([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *(SANITIZE_LINK if sanitize else []),
+                       "-o", made[lib], *objs]), "link", verbose)
         if native is not None:
             _finish(native, os.path.basename(NATIVE_SOURCE), verbose)
-            os.replace(NATIVE + ".tmp", NATIVE)
+        elif NATIVE in made:  # one of an earlier build must not stay beside this library
+            del made[NATIVE]
+            if os.path.exists(NATIVE):
+                os.remove(NATIVE)
+            print("the extension module is left out: it needs PyTorch and a C++ compiler", file=sys.stderr)
+        for target, tmp in made.items():  # all of it has compiled
+            os.replace(tmp, target)
     finally:
+        for proc in started:  # after a failure the others may still run
+            if proc.poll() is None:
+                os.killpg(proc.pid, signal.SIGKILL)
+                proc.communicate()
+        for tmp in made.values():
+            if os.path.exists(tmp):
+                os.remove(tmp)
         shutil.rmtree(objdir, ignore_errors=True)
     return lib
 

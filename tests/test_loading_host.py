@@ -66,3 +66,82 @@ def test_muon_calls_need_no_newer_entry_points(tmp_path):
     subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(source)], check=True)
     refusals = run_probe(ROOT, MUON_LIBRARY=str(lib))
     assert len(refusals) == 4 and all("older build of the library" in r for r in refusals)
+
+
+# --- build ---------------------------------------------------------------------------------------------------------
+@pytest.fixture
+def fake_build(tmp_path, monkeypatch):
+    """_build with a stand-in compiler: it fails on a source whose name is in a list, and otherwise writes its output."""
+    from matrix_orthogonalizing_optimizer_step_amd import _build
+
+    compiler = tmp_path / "fakecc"
+    compiler.write_text("""#!/bin/sh
+for a in "$@"; do
+  case "$a" in *bad*) echo "bad source"; exit 3;; esac
+  if [ "$last" = "-o" ]; then out="$a"; fi
+  last="$a"
+done
+echo new > "$out"
+""")
+    compiler.chmod(0o755)
+    lib, native = tmp_path / "libmuon.so", tmp_path / "_native.so"
+    lib.write_text("old")
+    native.write_text("old")
+    monkeypatch.setattr(_build, "LIB", str(lib))
+    monkeypatch.setattr(_build, "NATIVE", str(native))
+    monkeypatch.setattr(_build, "SOURCES", ["one.hip", "two.hip"])
+    monkeypatch.setattr(_build, "hipcc", lambda: str(compiler))
+    monkeypatch.setattr(_build, "_native_command", lambda out: [str(compiler), "module.cpp", "-o", out])
+    return _build, lib, native, compiler
+
+
+def test_build_replaces_library_and_extension_together(fake_build):
+    build, lib, native, compiler = fake_build
+    assert build.build(lib=str(lib)) == str(lib)
+    assert (lib.read_text(), native.read_text()) == ("new\n", "new\n")
+    native.write_text("old")
+    other = lib.with_name("libvariant.so")
+    build.build(lib=str(other))  # a variant leaves the extension module as it is
+    assert (other.read_text(), native.read_text()) == ("new\n", "old")
+
+
+def test_failed_extension_leaves_the_old_pair(fake_build, monkeypatch):
+    build, lib, native, compiler = fake_build
+    monkeypatch.setattr(build, "_native_command", lambda out: ["/bin/sh", str(compiler), "bad.cpp", "-o", out])
+    with pytest.raises(RuntimeError, match="sh failed on muon_native.cpp"):
+        build.build(lib=str(lib))
+    assert (lib.read_text(), native.read_text()) == ("old", "old")
+    assert not list(lib.parent.glob("*.tmp"))
+
+
+def test_failed_source_leaves_no_process_behind(fake_build, monkeypatch):
+    build, lib, native, compiler = fake_build
+    pid = lib.with_name("pid")
+    monkeypatch.setattr(build, "SOURCES", ["one.hip", "bad.hip"])
+    monkeypatch.setattr(build, "_native_command", lambda out: ["/bin/sh", "-c", f"echo $$ > {pid}; exec sleep 60"])
+    with pytest.raises(RuntimeError, match="fakecc failed on bad.hip"):
+        build.build(lib=str(lib))
+    assert (lib.read_text(), native.read_text()) == ("old", "old")
+    if pid.exists() and pid.read_text():  # it may have been ended before it wrote its number
+        assert not os.path.exists(f"/proc/{pid.read_text().strip()}")
+    assert not list(lib.parent.glob("*.tmp"))
+
+
+def test_library_builds_without_torch_or_a_host_compiler(fake_build, monkeypatch, capsys):
+    build, lib, native, compiler = fake_build
+    monkeypatch.setattr(build, "_native_command", lambda out: None)
+    build.build(lib=str(lib))
+    assert lib.read_text() == "new\n" and not native.exists()
+    assert "extension module is left out" in capsys.readouterr().err
+
+
+def test_extension_command_needs_torch_and_a_compiler(monkeypatch):
+    from matrix_orthogonalizing_optimizer_step_amd import _build
+
+    assert _build._native_command("x.so") is not None
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "torch", None)
+        assert _build._native_command("x.so") is None
+    monkeypatch.delenv("CXX", raising=False)
+    monkeypatch.setattr(_build.shutil, "which", lambda name: None)
+    assert _build._native_command("x.so") is None
