@@ -71,11 +71,12 @@ std::vector<const at::Tensor*> tensors_of(const py::object& seq, const char* nam
 struct Range {
   uintptr_t begin, end;
   bool written;
+  const at::Tensor* tensor;
 };
 
 void add_range(std::vector<Range>& all, const at::Tensor& t, bool written) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(t.data_ptr());
-  if (t.nbytes() > 0) all.push_back({p, p + t.nbytes(), written});
+  if (t.nbytes() > 0) all.push_back({p, p + t.nbytes(), written, &t});
 }
 
 // No written buffer may overlap another one.
@@ -88,6 +89,16 @@ void check_overlap(std::vector<Range>& all) {
     end = std::max(end, r.end);
     if (r.written) written_end = std::max(written_end, r.end);
   }
+}
+
+// The status of a call that wrote the written buffers, unless it was refused: their
+// tensors' versions go up, as with any operation in place, so that autograd sees the
+// change (inference tensors have no version).
+int called(muon_status status, const std::vector<Range>& all) {
+  if (status == MUON_OK || status == MUON_ERR_HIP)
+    for (const Range& r : all)
+      if (r.written && !r.tensor->is_inference()) r.tensor->unsafeGetTensorImpl()->bump_version();
+  return status;
 }
 
 muon_dtype dtype_of(const at::Tensor& t, const char* name) {
@@ -173,8 +184,9 @@ int adamw_step(const py::object& W, const py::object& M, const py::object& V, co
   const std::vector<void*> m = a.state(M, "M", a.sizes, at::kFloat), v = a.state(V, "V", a.sizes, at::kFloat);
   check_overlap(a.ranges);
   const c10::DeviceGuard guard(a.device);
-  return fn.adamw(static_cast<int>(a.sizes.size()), a.sizes.data(), a.w.data(), a.w_dtype, m.data(), v.data(),
-                  const_cast<const void* const*>(a.g.data()), a.g_dtype, &a.cfg, current_stream(a.device));
+  return called(fn.adamw(static_cast<int>(a.sizes.size()), a.sizes.data(), a.w.data(), a.w_dtype, m.data(), v.data(),
+                         const_cast<const void* const*>(a.g.data()), a.g_dtype, &a.cfg, current_stream(a.device)),
+                a.ranges);
 }
 
 int adamw8_step(const py::object& W, const py::object& m_codes, const py::object& m_scales, const py::object& r_codes,
@@ -190,8 +202,9 @@ int adamw8_step(const py::object& W, const py::object& m_codes, const py::object
   check_overlap(a.ranges);
   const muon_adamw8_state state{mc.data(), ms.data(), rc.data(), rs.data()};
   const c10::DeviceGuard guard(a.device);
-  return fn.adamw8(static_cast<int>(a.sizes.size()), a.sizes.data(), a.w.data(), a.w_dtype, &state,
-                   const_cast<const void* const*>(a.g.data()), a.g_dtype, &a.cfg, current_stream(a.device));
+  return called(fn.adamw8(static_cast<int>(a.sizes.size()), a.sizes.data(), a.w.data(), a.w_dtype, &state,
+                          const_cast<const void* const*>(a.g.data()), a.g_dtype, &a.cfg, current_stream(a.device)),
+                a.ranges);
 }
 
 // ---------------------------------------------------------------------------
@@ -311,11 +324,11 @@ py::tuple mx4_quantize(const py::object& X, bool along, bool across, const py::o
     }
   }
   check_overlap(ranges);
-  const int st = fn.quantize(x.batch(), as_int(x.rows), as_int(x.cols), x.in(), x.dtype,
-                             along ? q[0].codes.data() : nullptr, along ? q[0].scales.data() : nullptr,
-                             across ? q[1].codes.data() : nullptr, across ? q[1].scales.data() : nullptr,
-                             current_stream(x.device));
-  return py::make_tuple(st, made);
+  const muon_status st = fn.quantize(x.batch(), as_int(x.rows), as_int(x.cols), x.in(), x.dtype,
+                                     along ? q[0].codes.data() : nullptr, along ? q[0].scales.data() : nullptr,
+                                     across ? q[1].codes.data() : nullptr, across ? q[1].scales.data() : nullptr,
+                                     current_stream(x.device));
+  return py::make_tuple(called(st, ranges), made);
 }
 
 // New matrices, as a list.
@@ -344,9 +357,9 @@ py::tuple mx4_dequantize(const py::object& codes, const py::object& scales, int6
   if (y.batch() != q.batch() || y.rows != q.rows || y.cols != cols || y.device != q.device)
     refuse("out must have the shape, batch and device of the result");
   check_overlap(ranges);
-  const int st = fn.dequantize(q.batch(), as_int(q.rows), as_int(cols), q.c(), q.s(), y.ptr.data(), y.dtype,
-                               current_stream(q.device));
-  return py::make_tuple(st, Y);
+  const muon_status st = fn.dequantize(q.batch(), as_int(q.rows), as_int(cols), q.c(), q.s(), y.ptr.data(), y.dtype,
+                                       current_stream(q.device));
+  return py::make_tuple(called(st, ranges), Y);
 }
 
 // Returns (status, C).
@@ -378,10 +391,10 @@ py::tuple mx4_matmul(const py::object& a_codes, const py::object& a_scales, cons
     add_range(ranges, ws, true);
   }
   check_overlap(ranges);
-  const int st = fn.matmul(a.batch(), as_int(a.rows), as_int(b.rows), as_int(k), a.c(), a.s(), b.c(), b.s(),
-                           c.ptr.data(), c.dtype, accumulate ? 1 : 0, ws.data_ptr(), ws.nbytes(),
-                           current_stream(a.device));
-  return py::make_tuple(st, C);
+  const muon_status st = fn.matmul(a.batch(), as_int(a.rows), as_int(b.rows), as_int(k), a.c(), a.s(), b.c(), b.s(),
+                                   c.ptr.data(), c.dtype, accumulate ? 1 : 0, ws.data_ptr(), ws.nbytes(),
+                                   current_stream(a.device));
+  return py::make_tuple(called(st, ranges), C);
 }
 
 }  // namespace

@@ -541,3 +541,34 @@ def test_adamw_launches_are_traced():
     recs = mu.trace_collect()
     mu.trace_enable(False)
     assert [r["role"] for r in recs] == ["adamw", "adamw8"]
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_adamw_raises_the_version_of_what_it_writes(eight):
+    """A step between forward and backward is seen: autograd refuses the old graph's saved weights."""
+    W, M, V, G = make((300, 5), "f32", "f32", 43)
+    lists = (W, M, V)
+    if eight:
+        state = state_of(M, V)
+        lists = (W, state.m_codes, state.m_scales, state.r_codes, state.r_scales)
+    step = lambda: mu.adamw8_step(W, state, G, 1, 1e-3) if eight else mu.adamw_step(W, M, V, G, 1, 1e-3)  # noqa: E731
+    before = [[x._version for x in L] for L in lists]
+    held = [x._version for x in G]
+    step()
+    assert all(x._version > b for L, B in zip(lists, before) for x, b in zip(L, B))
+    assert [x._version for x in G] == held
+    p = torch.nn.Parameter(W[0].clone())
+    W[0] = p
+    loss = (p * p).sum()
+    step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with pytest.raises(ValueError):
+        mu.adamw_step([p], [V[0]], [V[0]], [G[0]], 1, 1e-3)
+    now = p._version
+    with pytest.raises(mu.MuonError):
+        mu.adamw_step([p], [M[0]], [V[0]], [G[0]], 0, 1e-3)
+    assert p._version == now  # a refused call has written nothing
+    with torch.inference_mode():  # tensors without a version
+        Z = [torch.zeros(9, device=DEV) for _ in range(4)]
+        mu.adamw_step(*[[z] for z in Z], 1, 1e-3)

@@ -425,3 +425,25 @@ def test_values_of_every_scale_byte():
     want[big] = np.sign(want[big]) * np.inf
     for dt in (torch.float32, torch.bfloat16):
         assert np.array_equal(want, f64(mu.mx4_dequantize(q, dt)[0]), equal_nan=True)
+
+
+def test_given_outputs_raise_their_version():
+    """Writing into out= is seen by autograd, as any in-place operation is."""
+    X = matrices(1, 40, 200, "f32", 61)
+    q, t = mu.mx4_quantize(X, transpose="both")
+    Y, C = [torch.zeros(40, 200, device=DEV)], [torch.zeros(40, 40, device=DEV)]
+    ws = torch.zeros(mu.mx4_workspace_size(1, 40, 40, 200), dtype=torch.uint8, device=DEV)
+    written = q.codes + q.scales + t.codes + t.scales + Y + C + [ws]
+    before = [x._version for x in written]
+    held = X[0]._version
+    mu.mx4_quantize(X, transpose="both", out=(q, t))
+    codes = [x._version for x in q.codes + q.scales]
+    mu.mx4_dequantize(q, out=Y)
+    mu.mx4_matmul(q, q, out=C, workspace=ws)
+    assert all(x._version > b for x, b in zip(written, before))
+    assert X[0]._version == held and [x._version for x in q.codes + q.scales] == codes
+    p = torch.nn.Parameter(Y[0])
+    loss = (p * p).sum()
+    mu.mx4_dequantize(q, out=[p])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
