@@ -129,12 +129,24 @@ std::vector<void*> list_pointers(const std::vector<const at::Tensor*>& list, con
   return out;
 }
 
-const void* scalar_pointer(const py::object& o, const char* name, at::ScalarType dtype, const at::Device& device) {
+const void* scalar_pointer(const py::object& o, const char* name, at::ScalarType dtype, const at::Device& device,
+                           std::vector<Range>& ranges) {
   if (!THPVariable_Check(o.ptr())) refuse(std::string(name) + ": a device tensor is needed");
   const at::Tensor& t = THPVariable_Unpack(o.ptr());
   if (t.numel() != 1 || t.scalar_type() != dtype || t.device() != device)
     refuse(std::string(name) + ": a tensor must be one " + c10::toString(dtype) + " on the device of W");
+  add_range(ranges, t, false);  // every block reads it while others write
   return t.data_ptr();
+}
+
+// A step number on the host.
+int64_t host_step(const py::object& o) {
+  int overflow = 0;
+  const py::object number = py::reinterpret_steal<py::object>(PyNumber_Index(o.ptr()));
+  if (!number) PyErr_Clear();
+  const int64_t step = number ? PyLong_AsLongLongAndOverflow(number.ptr(), &overflow) : 0;
+  if (!number || overflow != 0) refuse("step: an integer of at most 63 bits or a one-element int64 device tensor is needed");
+  return step;
 }
 
 struct Adamw {
@@ -154,7 +166,7 @@ struct Adamw {
     if (!device.is_cuda()) refuse("W: tensors must be device tensors");
     sizes.reserve(W.size());
     for (const at::Tensor* t : W) sizes.push_back(t->numel());
-    ranges.reserve(6 * W.size());
+    ranges.reserve(6 * W.size() + 2);
     w_dtype = dtype_of(*W[0], "W");
     if (w_dtype == MUON_F16) refuse("W: dtype must be float32 or bfloat16");
     w = list_pointers(W, "W", sizes, device, W[0]->scalar_type(), ranges, true);
@@ -164,12 +176,13 @@ struct Adamw {
     g = list_pointers(G, "G", sizes, device, G[0]->scalar_type(), ranges, false);
     cfg = {lr, beta1, beta2, eps, weight_decay, 0, nullptr, nullptr, seed};
     if (THPVariable_Check(step.ptr())) {
-      cfg.step_dev = static_cast<const int64_t*>(scalar_pointer(step, "step", at::kLong, device));
+      cfg.step_dev = static_cast<const int64_t*>(scalar_pointer(step, "step", at::kLong, device, ranges));
     } else {
-      cfg.step = step.cast<int64_t>();
+      cfg.step = host_step(step);
     }
     if (!grad_scale.is_none())
-      cfg.grad_scale = static_cast<const float*>(scalar_pointer(grad_scale, "grad_scale", at::kFloat, device));
+      cfg.grad_scale =
+          static_cast<const float*>(scalar_pointer(grad_scale, "grad_scale", at::kFloat, device, ranges));
   }
 
   std::vector<void*> state(const py::object& list, const char* name, const std::vector<int64_t>& n, at::ScalarType dtype) {

@@ -177,6 +177,50 @@ def test_adamw_checks_every_list():
         mu.adamw8_step([z(), z(300)], s, [z(), z(300)], 1, 1e-3)
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_adamw_refuses_a_scale_or_step_inside_what_it_writes(eight):
+    """The step number and the gradient scale are read by every block while others write."""
+    z = lambda n=8, dt=torch.float32: torch.zeros(n, dtype=dt, device=DEV)  # noqa: E731
+    W, M, V, G, state = [z()], [z()], [z()], [z()], mu.AdamW8State.zeros([z()])
+
+    def call(step=1, **kw):
+        if eight:
+            mu.adamw8_step(W, state, G, step, 1e-3, **kw)
+        else:
+            mu.adamw_step(W, M, V, G, step, 1e-3, **kw)
+
+    other = state.m_scales[0] if eight else M[0]
+    for t in (W[0], other):
+        with pytest.raises(ValueError, match="overlaps"):
+            call(grad_scale=t[:1])
+        if t.numel() > 1:
+            with pytest.raises(ValueError, match="overlaps"):
+                call(step=t[2:4].view(torch.int64))
+    call(grad_scale=G[0][:1])  # gradients are read only
+    both = torch.ones(2, dtype=torch.int64, device=DEV)
+    call(step=both[:1], grad_scale=both[1:].view(torch.float32)[:1])
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_adamw_step_numbers_of_other_types(eight):
+    z = lambda: torch.zeros(8, device=DEV)  # noqa: E731
+    W, M, V, G, state = [z()], [z()], [z()], [z()], mu.AdamW8State.zeros([z()])
+    call = lambda step: (mu.adamw8_step(W, state, G, step, 1e-3) if eight  # noqa: E731
+                         else mu.adamw_step(W, M, V, G, step, 1e-3))
+    for bad in (1.0, 2.5, None, "3", 1 << 63, -(1 << 63) - 1, [1]):
+        with pytest.raises(ValueError, match="step"):
+            call(bad)
+    for bad in (torch.tensor([1]), torch.tensor([1.0], device=DEV), torch.ones(2, dtype=torch.int64, device=DEV)):
+        with pytest.raises(ValueError, match="step"):
+            call(bad)
+    for good in (1, np.int64(2), np.int32(3), (1 << 63) - 1):
+        call(good)
+    for bad in (0, -1):
+        with pytest.raises(mu.MuonError):
+            call(bad)
+    assert not W[0].any()
+
+
 # --- 8-bit moments -------------------------------------------------------------------------------------------------
 # m and v before they are coded are fp32 values with the relative errors of adamw_tolerance, on top of the decoded
 # moments (one product each, h; v's square 2 h more): at most 10 h of the magnitudes of their terms, so x = sqrt(v) / s
