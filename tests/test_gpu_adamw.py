@@ -177,6 +177,28 @@ def test_adamw_checks_every_list():
         mu.adamw8_step([z(), z(300)], s, [z(), z(300)], 1, 1e-3)
 
 
+@pytest.mark.parametrize("order", ["ascending", "descending", "shuffled", "interleaved"])
+def test_adamw_finds_an_overlap_in_any_order(order):
+    """One element shared by two of 90 neighbouring views, in lists whose addresses run in any order."""
+    n, size = 90, 33
+    at = list(range(n))
+    if order == "descending":
+        at = at[::-1]
+    elif order == "shuffled":
+        np.random.default_rng(48).shuffle(at)
+    elif order == "interleaved":
+        at = at[::2] + at[1::2]
+    flat = [torch.zeros(n * size, device=DEV) for _ in range(4)]
+    lists = [[f[i * size:(i + 1) * size] for i in at] for f in flat]
+    mu.adamw_step(*lists, 1, 1e-3)  # neighbours do not overlap
+    for which in range(3):
+        for j in (0, 41, n - 1):
+            i = at[j]
+            bad = list(lists[which])
+            bad[j] = flat[which][i * size + 1:(i + 1) * size + 1] if i < n - 1 else flat[which][i * size - 1:(i + 1) * size - 1]
+            with pytest.raises(ValueError, match="overlaps"):
+                mu.adamw_step(*(bad if k == which else L for k, L in enumerate(lists)), 1, 1e-3)
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_adamw_refuses_a_scale_or_step_inside_what_it_writes(eight):
     """The step number and the gradient scale are read by every block while others write."""
