@@ -544,6 +544,110 @@ def test_adamw8_follows_a_second_moment_that_changes_slowly():
     assert abs(v.double().mean().item() - want) < 0.05 * want
 
 
+@pytest.mark.parametrize("count", [7, 8, 9, 86, 87, 88, 174, 175])
+def test_adamw_lists_around_the_length_of_a_launch(count):
+    """Short lists of at most 8 tensors, 87 tensors a launch, and one more or less; empty ones among them."""
+    sizes = [(37 * i + 5) % 311 if i % 7 != 3 else 0 for i in range(count)]
+    W, M, V, G = make(sizes, "f32", "bf16", 44)
+    W0, M0, V0 = ([x.clone() for x in L] for L in (W, M, V))
+    mu.trace_enable(True)
+    mu.adamw_step(W, M, V, G, 2, **HYPER)
+    launches = len(mu.trace_collect())
+    mu.trace_enable(False)
+    assert launches == sum(any(sizes[a:a + 87]) for a in range(0, count, 87))  # none for empty tensors alone
+    compare32(W, M, V, G, W0, M0, V0, 2, "f32", **HYPER)
+
+
+@pytest.mark.parametrize("count", [7, 8, 9, 63, 64, 65, 128, 129])
+def test_adamw8_lists_around_the_length_of_a_launch(count):
+    """As above with 64 tensors a launch; the roundings go by the place in the whole list."""
+    sizes = [(53 * i + 5) % 397 if i % 7 != 3 else 0 for i in range(count)]
+    W, M, V, G = make(sizes, "f32", "bf16", 45)
+    state = state_of(M, V)
+    mu.trace_enable(True)
+    step8(W, state, G, 6, 12, "f32", HYPER)
+    launches = len(mu.trace_collect())
+    mu.trace_enable(False)
+    assert launches == sum(any(sizes[a:a + 64]) for a in range(0, count, 64))
+
+
+def code_bytes32(x, u32, v):
+    """Codes of m (nearest) or, with chances, of the root of v, from fp32 values x = value / scale: every operation in
+    fp32 with one rounding, as the definitions in include/muon.h are computed."""
+    f = np.float32
+    if u32 is None:
+        return torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    binade = np.maximum(x.view(np.uint32) & np.uint32(0x7F800000), np.uint32(121 << 23))
+    y = x * (np.uint32(257 << 23) - binade).view(f)
+    lo = np.floor(y)
+    bar = u32 * ((2 * lo + 1) * f(2.0 ** -32))
+    up = ((y - lo) * (y + lo) > bar) | ((lo == 0) & (v > 0))
+    step = (binade - np.uint32(3 << 23)).view(f)
+    value = np.where(up, lo + f(1), lo) * step
+    return torch.from_numpy(value.astype(f)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+@pytest.mark.parametrize("low,high", [(-40, 40), (-62, -20), (0, 1)])
+def test_adamw8_codes_and_scales_bit_for_bit(low, high):
+    """One step from zero over 2^14 groups with scales of any binade and any mantissa: the moments' fp32 sums, the root
+    rounded to nearest, the scales, their reciprocals rounded to nearest and the codes are exactly those of single fp32
+    operations, so they cannot depend on which approximations or fused operations a kernel uses."""
+    f = np.float32
+    groups = 1 << 14
+    rng = np.random.default_rng(46)
+    top = np.exp2(rng.uniform(low, high, (groups, 1)))
+    g = top * rng.standard_normal((groups, 128)) * np.exp2(-rng.exponential(3.0, (groups, 128)))
+    g[:, 7] = top[:, 0] * rng.uniform(4, 8, groups)
+    g = g.astype(f).reshape(-1)
+    W, G = [torch.zeros(g.size, device=DEV)], [torch.from_numpy(g).to(DEV)]
+    state = mu.AdamW8State.zeros(W)
+    mu.adamw8_step(W, state, G, 1, 0.01, seed=9)
+    m, v = f(1 - 0.9) * g, (f(1 - 0.999) * g) * g
+    u32 = (ao.chances(g.size, 9, 1, 0) * 2.0 ** 32).astype(f)
+    for x, codes, scales, chance in ((m, state.m_codes, state.m_scales, None), (np.sqrt(v), state.r_codes, state.r_scales, u32)):
+        assert x.dtype == f
+        s = np.abs(x).reshape(groups, 128).max(1) * (f(1) / f(448))
+        assert (s >= 2.0 ** -126).all()
+        assert np.array_equal(scales[0].cpu().numpy(), s)
+        y = x * np.repeat(f(1) / s, 128)
+        want = code_bytes32(np.clip(y, f(-448), f(448)), chance, v)
+        got = bytes_of(codes[0])
+        assert np.array_equal(got, want), f"{np.sum(got != want)} of {got.size} codes differ"
+
+
+def chances_from(first, count, seed, t, tensor):
+    """ao.chances of the elements from ``first`` on."""
+    key = ao.mix(np.uint64(seed) + ao.mix(np.uint64(t) + ao.mix(np.uint64(tensor))))
+    i = np.arange(first, first + count, dtype=np.uint64)
+    h = ao.mix((i >> np.uint64(1)) + key)
+    return (np.where(i & np.uint64(1), h >> np.uint64(16), h & np.uint64(0xFFFF)).astype(np.float64) + 0.5) / 65536.0
+
+
+def test_adamw8_codes_past_2_31_elements():
+    """Both ends of one tensor of 2^31 + 1003 elements: codes, scales and chances of the last groups too."""
+    n = 2 ** 31 + 1003
+    W, G = [torch.ones(n, dtype=torch.bfloat16, device=DEV)], [torch.zeros(n, dtype=torch.bfloat16, device=DEV)]
+    count = n - 2 ** 31 + 4096  # whole groups, and the short one at the end
+    gen = torch.Generator(DEV).manual_seed(2)
+    for part in (slice(0, 4096), slice(n - count, n)):
+        G[0][part] = torch.randn(part.stop - part.start, device=DEV, generator=gen).to(torch.bfloat16)
+    state = mu.AdamW8State.zeros(W)
+    mu.adamw8_step(W, state, G, 1, 0.03, seed=6)
+    u = np.concatenate((ao.chances(4096, 6, 1, 0), chances_from(n - count, count, 6, 1, 0)))
+    at = 0
+    for part in (slice(0, 4096), slice(n - count, n)):
+        g = f64(G[0][part])
+        groups = slice(part.start // 128, (part.stop + 127) // 128)
+        m, v = (1 - 0.9) * g, (1 - 0.999) * g * g
+        bad = ao.check_moment_codes(bytes_of(state.m_codes[0][part]), f64(state.m_scales[0][groups]), m, SLACK)
+        assert bad == 0, f"{bad} codes of m"
+        bad = ao.check_root_codes(bytes_of(state.r_codes[0][part]), f64(state.r_scales[0][groups]), v, u[at:at + g.size], SLACK)
+        assert bad == 0, f"{bad} codes of the root of v"
+        at += g.size
+    middle = slice(4096 // 128, (n - count) // 128)
+    assert not state.m_scales[0][middle].any() and not state.r_scales[0][middle].any()
+
+
 # --- graphs, streams -----------------------------------------------------------------------------------------------
 def test_adamw_captured_with_a_step_on_the_device():
     """Replays of one captured step of both kinds equal eager steps, with eager work in between."""

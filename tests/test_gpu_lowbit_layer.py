@@ -96,3 +96,47 @@ def test_layer_gradients_against_differences():
             e = np.zeros_like(P)
             e[i] = 1e-5
             assert abs((f(P + e) - f(P - e)) / 2e-5 - dP[i]) < 1e-7 * (1 + abs(dP[i]))
+
+
+def loss64(X, W, T):
+    return 0.5 * np.sum((X @ W.T - T) ** 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,n_in,n_out", [(3, 5, 4), (20, 33, 18), (1, 130, 7)])
+def test_products_give_the_gradients_that_differences_give(tokens, n_in, n_out):
+    """The layer's products through the library, on operands the code holds exactly, against central differences of
+    1/2 |X W^T - T|^2 in fp64: dX = dY W and dW = dY^T X, the latter also added to a gradient that is there.
+
+    X, W and dY hold small multiples of 1/2 with a 6 in every block, so coding changes nothing and all sums are exact in
+    fp32.  The loss is quadratic, so the differences' only error is rounding: at most a few 2^-53 of the loss over 2 e."""
+    rng = np.random.default_rng(47)
+    values = np.array([-3.0, -2.0, -1.0, -0.5, 0.0, 0.5, 1.0, 2.0, 3.0])
+
+    def exact(rows, cols):
+        a = rng.choice(values, (rows, cols))
+        a[::32, :] = 6.0  # every block along rows or columns has its largest magnitude at 6: scale 1
+        a[:, ::32] = 6.0
+        return a
+
+    X, W, D = exact(tokens, n_in), exact(n_out, n_in), exact(tokens, n_out)
+    T = X @ W.T - D
+    dev = lambda a: [torch.from_numpy(a.astype(np.float32)).to(DEV)]  # noqa: E731
+    x, x_t = mu.mx4_quantize(dev(X), transpose="both")
+    w, w_t = mu.mx4_quantize(dev(W), transpose="both")
+    Y = mu.mx4_matmul(x, w, torch.float32)
+    dY = [(Y[0] - dev(T)[0]).contiguous()]
+    assert np.array_equal(f64(dY[0]), D)
+    d, d_t = mu.mx4_quantize(dY, transpose="both")
+    dX = f64(mu.mx4_matmul(d, w_t, torch.float32)[0])
+    G = dev(np.full((n_out, n_in), 0.25))
+    mu.mx4_matmul(d_t, x_t, out=G, accumulate=True)
+    dW = f64(G[0]) - 0.25
+    e = 0.5  # a power of two; the difference quotient of a quadratic is its derivative for every e
+    bound = 64 * 2.0 ** -53 * (loss64(X, W, T) + np.abs(D).sum() * 100 + 1e4) / (2 * e)
+    for P, dP, f in ((X, dX, lambda P: loss64(P, W, T)), (W, dW, lambda P: loss64(X, P, T))):
+        for i in np.ndindex(P.shape):
+            up, down = P.copy(), P.copy()
+            up[i] += e
+            down[i] -= e
+            assert abs((f(up) - f(down)) / (2 * e) - dP[i]) <= bound, i
