@@ -427,7 +427,7 @@ muon_status muon_adamw8_step(int tensors, const int64_t *sizes, void *const *W, 
  * of `rows` rows
  *   codes   uint8 [units][rows][64], element 2 i in the low, 2 i + 1 in the
  *           high half of byte i of its unit; 16-byte aligned
- *   scales  uint8 [units][rows][4]; 4-byte aligned.
+ *   scales  uint8 [units][rows][4]; 4-byte aligned (both checked).
  * Every matrix argument is a HOST array of `batch` device pointers, read during
  * the call only (a layer's products come one or a few at a time; the pointers
  * travel as kernel arguments, one launch per 16 matrices).

@@ -437,13 +437,14 @@ bool mx4_shape_ok(int batch, int rows, int cols) {
   return batch >= 1 && rows >= 1 && cols >= 1 && rows <= MUON_MAX_DIM && cols <= MUON_MAX_DIM;
 }
 
-// A host array of `batch` non-null device pointers.
-bool pointers_ok(int batch, const void* const* p) {
+// A host array of `batch` non-null device pointers, multiples of `align`.
+bool pointers_ok(int batch, const void* const* p, uintptr_t align = 1) {
   if (p == nullptr) return false;
   for (int i = 0; i < batch; ++i)
-    if (p[i] == nullptr) return false;
+    if (p[i] == nullptr || (reinterpret_cast<uintptr_t>(p[i]) & (align - 1)) != 0) return false;
   return true;
 }
+constexpr uintptr_t kCodeAlign = 16, kScaleAlign = 4;
 
 template <class T>
 void take(T* to, T const* from, int at, int count) {
@@ -469,10 +470,11 @@ muon_status muon_mx4_quantize(int batch, int rows, int cols, const void* const* 
     return MUON_ERR_INVALID_ARG;
   if (codes == nullptr && codes_t == nullptr) return MUON_ERR_INVALID_ARG;
   const void* const* arrays[5] = {X, codes, scales, codes_t, scales_t};
+  const uintptr_t align[5] = {1, kCodeAlign, kScaleAlign, kCodeAlign, kScaleAlign};
   for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < i; ++j)
       if (arrays[i] != nullptr && arrays[i] == arrays[j]) return MUON_ERR_INVALID_ARG;
-    if ((i == 0 || arrays[i] != nullptr) && !pointers_ok(batch, arrays[i])) return MUON_ERR_INVALID_ARG;
+    if ((i == 0 || arrays[i] != nullptr) && !pointers_ok(batch, arrays[i], align[i])) return MUON_ERR_INVALID_ARG;
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const double r = rows, c = cols;
@@ -498,8 +500,8 @@ muon_status muon_mx4_quantize(int batch, int rows, int cols, const void* const* 
 
 muon_status muon_mx4_dequantize(int batch, int rows, int cols, const void* const* codes, const void* const* scales,
                                 void* const* Y, muon_dtype y_dtype, void* stream) {
-  if (!mx4_shape_ok(batch, rows, cols) || !pointers_ok(batch, codes) || !pointers_ok(batch, scales) ||
-      !pointers_ok(batch, Y))
+  if (!mx4_shape_ok(batch, rows, cols) || !pointers_ok(batch, codes, kCodeAlign) ||
+      !pointers_ok(batch, scales, kScaleAlign) || !pointers_ok(batch, Y))
     return MUON_ERR_INVALID_ARG;
   if (!mx4_type_ok(y_dtype) || codes == scales || static_cast<const void*>(codes) == Y ||
       static_cast<const void*>(scales) == Y)
@@ -542,8 +544,9 @@ muon_status muon_mx4_matmul(int batch, int m, int n, int k, const void* const* A
   if (need == 0) return MUON_ERR_INVALID_ARG;
   const void* const* in[4] = {A_codes, A_scales, B_codes, B_scales};
   if (!pointers_ok(batch, C)) return MUON_ERR_INVALID_ARG;
-  for (const void* const* p : in)  // A and B may be one matrix (A A^T); C is written
-    if (!pointers_ok(batch, p) || static_cast<const void*>(p) == C) return MUON_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)  // A and B may be one matrix (A A^T); C is written
+    if (!pointers_ok(batch, in[i], i % 2 == 0 ? kCodeAlign : kScaleAlign) || static_cast<const void*>(in[i]) == C)
+      return MUON_ERR_INVALID_ARG;
   if (!mx4_type_ok(c_dtype) || (accumulate != 0 && accumulate != 1)) return MUON_ERR_INVALID_ARG;
   if (c_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
   if (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

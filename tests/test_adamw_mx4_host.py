@@ -193,6 +193,23 @@ def test_mx4_refusals_before_any_device_work():
         assert g(**kw) == code, kw
 
 
+def test_mx4_codes_off_their_alignment_are_refused():
+    """Codes need 16 bytes (they are read and written 16 at a time), scales 4; in any matrix of the batch."""
+    lib = mu.load_library()
+    ok = ptrs(1 << 20, 1 << 21)
+    for off in (1, 4, 8, 12):
+        for at in (0, 1):
+            codes = ptrs(*[(1 << 22) + (off if i == at else 0) for i in range(2)])
+            scales = ptrs(*[(1 << 23) + (off % 4 or 2 if i == at else 0) for i in range(2)])
+            for bad in (0, 1):
+                c, s = (codes, ptrs(1 << 24, 1 << 25)) if bad == 0 else (ptrs(1 << 24, 1 << 25), scales)
+                assert lib.muon_mx4_quantize(2, 4, 4, ok, 0, c, s, None, None, None) == 1
+                assert lib.muon_mx4_quantize(2, 4, 4, ok, 0, None, None, c, s, None) == 1
+                assert lib.muon_mx4_dequantize(2, 4, 4, c, s, ok, 0, None) == 1
+                fine = (ptrs(1 << 26, 1 << 27), ptrs(1 << 28, 1 << 29))
+                assert lib.muon_mx4_matmul(2, 4, 4, 4, c, s, *fine, ok, 0, 0, 256, 1 << 40, None) == 1
+                assert lib.muon_mx4_matmul(2, 4, 4, 4, *fine, c, s, ok, 0, 0, 256, 1 << 40, None) == 1
+
 def test_mx4_binding_refusals():
     u8 = torch.uint8
     good = mu.MX4([torch.zeros(2, 5, 64, dtype=u8)], [torch.zeros(2, 5, 4, dtype=u8)], 200)
