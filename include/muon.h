@@ -569,7 +569,8 @@ muon_status muon_mfma_ceiling(int blocks, int rounds, muon_dtype dtype, float *s
 /* Static description of a status code (never NULL). */
 const char *muon_status_string(muon_status status);
 
-/* MUON_ABI_VERSION of the loaded library. */
+/* MUON_ABI_VERSION of the loaded library.  The AdamW and microscaled 4-bit entry points were
+ * added without a new version: a library of version 6 has them if it has their symbols. */
 int muon_abi_version(void);
 
 #ifdef __cplusplus

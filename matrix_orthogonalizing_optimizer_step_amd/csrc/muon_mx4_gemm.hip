@@ -1,12 +1,12 @@
 // C = A B^T (+ C) of two matrices in the microscaled 4-bit code, on the
-// block-scaled MFMA (v_mfma_scale_f32_32x32x64_f8f6f4 with fp4 operands): a
-// lane holds one block of 32 elements of one row, 16 bytes, and that block's
-// scale byte; the products and their sum over k are fp32.
+// block-scaled MFMA with fp4 operands: a lane holds one block of 32 elements of
+// one row, 16 bytes, and that block's scale byte; the products and their sum over
+// k are fp32.
 //
-// The order of k is free as long as A and B agree, so lanes 0..31 take unit
-// 2 j and lanes 32..63 unit 2 j + 1 of the row, and the four MFMAs of a pair of
-// units take blocks 0..3 of each: a lane reads 64 consecutive code bytes and
-// one 32-bit word of scales for them.
+// The order of k is free as long as A and B agree.  The tiles take 32x32x64 MFMAs,
+// two for a unit of 128 (lanes 0..31 blocks 0 and 1 of their row, lanes 32..63
+// blocks 2 and 3), through LDS; for at most 16 rows of A a 16x16x128 MFMA takes a
+// whole unit (16 lanes a block), straight from memory.
 #include "muon_convert.h"
 #include "muon_internal.h"
 #include "muon_mx4.h"
@@ -555,9 +555,17 @@ void split_k(int64_t tiles, int units, double elements, Mx4Plan* p) {
 // Which kernel, by the tiles there are for 256 compute units (times on bf16 C):
 //   at most 16 rows of A   B's codes are read once, straight into registers.
 //                          16x18944x3584: 9.3 us, 64 x 128 tiles 10.2
-//   256 x 256 tiles        where their last round leaves at most a third of the
+//   256 x 256 tiles        where their rounds together leave at most a third of the
 //                          compute units idle: 4096x4096x2048 (256 tiles) 25.9 us,
-//                          128 x 128 28.3; 2048x4096x8192 (128 tiles) 46.9 and 42.1
+//                          128 x 128 28.3; 2048x4096x8192 (128 tiles) 46.9 and 42.1.
+//                          From 513 tiles on that is always so, however few the last
+//                          round has.  At k = 8192 it is right at every count
+//                          measured (256 x 256 / 128 x 128): 171 tiles 48.8 / 56.8,
+//                          342 100 / 106, 520 156 / 163, 780 214 / 235, and 300, which
+//                          it leaves, 98.3 / 94.1.  At k = 2048 a tile's start and end
+//                          weigh more and the smaller tiles would win behind a full
+//                          round: 171 21.4 / 20.8, 342 39.9 / 35.1, 520 62.1 / 52.6,
+//                          780 82.9 / 77.6, but 512 (two full ones) 46.3 / 49.6.
 //   64 x 128 tiles         for at most 384 of them, split along k if they are
 //                          few: 512x3584x3584 (224) 9.6 us, 128 x 128 11.4;
 //                          256x18944x3584 (592) 22.0 and 19.0
