@@ -75,10 +75,14 @@ class Buffers {
     written_.reserve(n);
   }
 
-  void add(const at::Tensor& t, bool written) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(t.data_ptr());
-    if (t.nbytes() > 0) ranges_.push_back({p, p + t.nbytes(), written});
+  // The tensor's memory, which is noted.
+  void* add(const at::Tensor& t, bool written) {
+    void* const memory = t.data_ptr();
+    const uintptr_t p = reinterpret_cast<uintptr_t>(memory);
+    const size_t bytes = t.nbytes();
+    if (bytes > 0) ranges_.push_back({p, p + bytes, written});
     if (written) written_.push_back(&t);
+    return memory;
   }
 
   // No written buffer may overlap another one.
@@ -161,8 +165,7 @@ std::vector<void*> list_pointers(const std::vector<const at::Tensor*>& list, con
     if (t.device() != device) refuse(std::string(name) + ": all tensors must be on the device of W");
     if (t.numel() != sizes[i]) refuse(std::string(name) + ": wrong number of elements");
     if (!t.is_contiguous()) refuse(std::string(name) + ": tensors must be contiguous");
-    out[i] = t.data_ptr();
-    buffers.add(t, written);
+    out[i] = buffers.add(t, written);
   }
   return out;
 }
@@ -173,8 +176,7 @@ const void* scalar_pointer(const py::object& o, const char* name, at::ScalarType
   const at::Tensor& t = THPVariable_Unpack(o.ptr());
   if (t.numel() != 1 || t.scalar_type() != dtype || t.device() != device)
     refuse(std::string(name) + ": a tensor must be one " + c10::toString(dtype) + " on the device of W");
-  buffers.add(t, false);  // every block reads it while others write
-  return t.data_ptr();
+  return buffers.add(t, false);  // every block reads it while others write
 }
 
 // A step number on the host.
