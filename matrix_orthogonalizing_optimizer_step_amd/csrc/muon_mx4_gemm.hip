@@ -10,13 +10,10 @@
 #include "muon_convert.h"
 #include "muon_internal.h"
 #include "muon_mx4.h"
+#include "muon_tile.h"
 
 namespace muon {
 namespace {
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;  // the operand format field of the MFMA
 
@@ -27,10 +24,6 @@ __device__ __forceinline__ f32x16_t mfma_mx4(const uint4& a, const uint4& b, con
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, kFp4, kFp4, S, static_cast<int>(sa), S,
                                                          static_cast<int>(sb));
 }
-
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kCUs = 256;  // compute units of the MI355X: the plans below depend on shapes only
 
 // ---------------------------------------------------------------------------
 // TM x TN tiles by 4 waves (WM x 4 / WM, each FM x FN MFMA tiles of 32 x 32).  k
@@ -47,10 +40,7 @@ constexpr int kCUs = 256;  // compute units of the MI355X: the plans below depen
 // done by then, so its stage can be filled anew, and the step's other half
 // covers the first reads of the next slab.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
 constexpr int kStages = 4;
-constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;  // sched_group_barrier masks
 
 template <int TM_, int TN_, int WM_>
 struct Tile {
@@ -63,19 +53,6 @@ struct Tile {
     uint32_t scale[TM + TN];
   };
 };
-
-constexpr int waitcnt_imm(int vm, int lgkm) {  // vmcnt, no wait for exports, lgkmcnt
-  return (vm & 15) | (((vm >> 4) & 3) << 14) | (7 << 4) | ((lgkm & 15) << 8);
-}
-
-// A buffer resource of `bytes` bytes at `base` + `offset` (all block-uniform).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t offset, uint32_t bytes) {
-  const uint64_t u = reinterpret_cast<uint64_t>(base) + offset;
-  const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u & 0xffffffffu)));
-  const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32)));
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | (hi << 32)), static_cast<short>(0),
-                                           __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
-}
 
 // One operand's source, seen from this lane.
 struct Source {
@@ -219,142 +196,6 @@ __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f0
   shift_scales<FN>(wn.b, lane);
   shift_scales<FM>(wn.a, lane);
   w = wn;
-}
-
-// Block id -> tile: consecutive ids go to the 8 XCDs in turn, so each XCD gets a
-// contiguous range of tiles, and tiles run down columns of 4 tile rows, so that
-// the tiles an XCD works on at one time share their rows of A and B in its L2.
-__device__ __forceinline__ void tile_of(int id, int total, int tm, int tn, int* outer, int* ti, int* tj) {
-  const int q = total >> 3, rest = total & 7, x = id & 7, at = id >> 3;
-  int t = x * q + (x < rest ? x : rest) + at;
-  const int per = tm * tn;
-  *outer = t / per;
-  t -= *outer * per;
-  constexpr int kGroup = 4;
-  const int g = t / (kGroup * tn), first = g * kGroup, h = tm - first < kGroup ? tm - first : kGroup;
-  t -= g * kGroup * tn;
-  *ti = first + t % h;
-  *tj = t / h;
-}
-
-// Four consecutive elements of a row of C (those with left > 0), with what is
-// there if asked for.  vec: the place is aligned to four elements.
-template <int DC>
-__device__ __forceinline__ void store_quad(void* C, int64_t at, const float (&v)[4], int left, bool vec, int accumulate) {
-  float x[4] = {v[0], v[1], v[2], v[3]};
-  if (vec && left >= 4) {
-    if constexpr (DC == kF32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(C) + at);
-      if (accumulate) {
-        const float4 c = *p;
-        x[0] += c.x; x[1] += c.y; x[2] += c.z; x[3] += c.w;
-      }
-      *p = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-      uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(C) + at);
-      if (accumulate) {
-        const uint2 c = *p;
-        x[0] += bf16_to_f32(static_cast<uint16_t>(c.x));
-        x[1] += bf16_to_f32(static_cast<uint16_t>(c.x >> 16));
-        x[2] += bf16_to_f32(static_cast<uint16_t>(c.y));
-        x[3] += bf16_to_f32(static_cast<uint16_t>(c.y >> 16));
-      }
-      *p = make_uint2(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) store_from_f32(C, at + e, DC, accumulate ? load_as_f32(C, at + e, DC) + x[e] : x[e]);
-  }
-}
-
-typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
-
-// A wave's accumulators to C, 32 rows at a time through its own LDS (`stage`).
-// With D = (B rows) x (A rows) lane l holds row l % 32 of C and, in registers 4 g
-// .. 4 g + 3, columns 8 g + 4 (l / 32) .. + 3 of an MFMA tile; read back, a lane
-// has 16 bytes of a row, so that a store fills whole 128 FN-byte (bf16: 64 FN)
-// pieces of rows.  LDS holds C's type, or fp32 where C is added to: C is rounded
-// once.  Measured on 8192x7168x3584 against 8-byte stores of 32 rows at a time
-// straight from the accumulators: 138 -> 122 us.
-template <class T, int DC, bool ADD>
-__device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
-                                           int m, int n, int lane) {
-  constexpr int kSize = DC == kF32 ? 4 : 2, kHeld = ADD || DC == kF32 ? 4 : 2;  // bytes of an element of C, in LDS
-  constexpr int kCols = 32 * T::FN, kPitch = kCols * kHeld / 16 + 1;            // uint4 of a row, one against conflicts
-  constexpr int kLanes = kCols * kSize / 16, kRows = 64 / kLanes;               // lanes of a row, rows of a store
-  static_assert(32 * kPitch * 16 <= sizeof(typename T::Stage) && kLanes <= 64, "staging");
-  const int row = lane & 31, half = lane >> 5, r0 = lane / kLanes, chunk = lane % kLanes;
-  constexpr int kElems = 16 / kSize;
-  const int jc = j + chunk * kElems;
-#pragma unroll
-  for (int y = 0; y < T::FM; ++y) {
-#pragma unroll
-    for (int x = 0; x < T::FN; ++x)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float v[4] = {acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
-        const int col = 32 * x + 8 * g + 4 * half;
-        if constexpr (kHeld == 4) {
-          stage[row * kPitch + col / 4] = __builtin_bit_cast(uint4, make_float4(v[0], v[1], v[2], v[3]));
-        } else {
-          reinterpret_cast<uint2*>(stage)[row * kPitch * 2 + col / 4] =
-              make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
-        }
-      }
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-    asm volatile("" ::: "memory");  // the wave's own writes, in order with its reads
-#pragma unroll
-    for (int q = 0; q < 32 / kRows; ++q) {
-      const int r = q * kRows + r0, ir = i + 32 * y + r;
-      if (ir < m && jc < n) {
-        char* const p = static_cast<char*>(C) + (static_cast<int64_t>(ir) * n + jc) * kSize;
-        float f[kElems];
-        uint4 h;
-        if constexpr (kHeld == 4) {
-#pragma unroll
-          for (int e = 0; e < kElems; e += 4) {
-            const float4 t = __builtin_bit_cast(float4, stage[r * kPitch + (chunk * kElems + e) / 4]);
-            f[e] = t.x; f[e + 1] = t.y; f[e + 2] = t.z; f[e + 3] = t.w;
-          }
-        } else {
-          h = stage[r * kPitch + chunk];
-        }
-        if (jc + kElems <= n) {
-          if constexpr (kHeld == 4) {
-            if constexpr (ADD) {
-              const u32x4_t c = *reinterpret_cast<const u32x4_a2*>(p);
-#pragma unroll
-              for (int e = 0; e < kElems; ++e)
-                f[e] += DC == kF32 ? __uint_as_float(c[e & 3])
-                                   : bf16_to_f32(static_cast<uint16_t>((e & 1) ? c[e >> 1] >> 16 : c[e >> 1]));
-            }
-            if constexpr (DC == kF32) {
-              *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){__float_as_uint(f[0]), __float_as_uint(f[1]),
-                                                          __float_as_uint(f[2]), __float_as_uint(f[3])};
-            } else {
-              *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
-                                                          f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7])};
-            }
-          } else {
-            *reinterpret_cast<u32x4_a2*>(p) = (u32x4_t){h.x, h.y, h.z, h.w};
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < kElems; ++e)
-            if (jc + e < n) {
-              if constexpr (kHeld == 4) {
-                store_from_f32(p, e, DC, ADD ? load_as_f32(p, e, DC) + f[e] : f[e]);
-              } else {
-                const uint32_t w = (&h.x)[e >> 1];
-                reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>((e & 1) ? w >> 16 : w);
-              }
-            }
-        }
-      }
-    }
-    asm volatile("" ::: "memory");  // the next rows' writes stay behind these reads
-  }
 }
 
 template <class T, int DC>
@@ -525,8 +366,6 @@ __global__ __launch_bounds__(64 * NW) void mx4_few_rows_kernel(Mx4GemmArgs a) {
 typedef Tile<256, 256, 2> Big;
 typedef Tile<128, 128, 2> Mid;
 typedef Tile<64, 128, 1> Low;
-
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 template <class T>
 int64_t tiles_of(int batch, int m, int n) {
