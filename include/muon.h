@@ -469,6 +469,146 @@ muon_status muon_mx4_matmul(int batch, int m, int n, int k,
                             void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * 8-bit code with a scale for each block of 128, for the weights a step has
+ * updated and for what they are multiplied with.  Along a row, each block of 128
+ * elements (with tile = 1, each tile of 128 x 128) shares a scale 2^(byte -
+ * 127): the smallest one, from byte 0 on, with which the block's largest
+ * magnitude is at most 448 (MUON_E4M3) or 57344 (MUON_E5M2) scales; 255 (NaN)
+ * if the block holds a NaN or an infinity (its codes are then 0).  An element is
+ * stored as the 8-bit float nearest to x / scale, ties to even (OCP e4m3 and
+ * e5m2; neither infinities nor NaN are stored).  The conversion is exact
+ * arithmetic.
+ *
+ * Layout: a row of k elements is ceil(k / 128) units, filled up with zero codes
+ * (the product relies on them).  For a matrix of `rows` rows
+ *   codes   [2 units][rows][64] bytes: the first and the last 64 elements of a
+ *           unit; 16-byte aligned
+ *   scales  [units][rows rounded up to 16] bytes; 16-byte aligned (both checked);
+ *           bytes behind the last row are neither written nor used.  A tile's
+ *           scale is repeated for each of its rows.
+ * Matrix arguments are HOST arrays of `batch` device pointers, read during the
+ * call only (one launch per 16 matrices).
+ *
+ * muon_fp8_quantize codes rows x cols matrices X (F32, BF16 or F16) along their
+ * rows (codes, scales), along their columns (codes_t, scales_t: the code of the
+ * cols x rows matrix X^T), or both; the arrays of an orientation that is not
+ * wanted are NULL.  With tile = 1 both orientations hold the same values.
+ *   counts  NULL with groups = 0, or (batch 1, tile 0, codes_t wanted) a device
+ *           array of `groups` row counts: rows of group 0 come first, then those
+ *           of group 1, and so on.  In the columns' code each group fills whole
+ *           units, ceil(count / 128) of them behind one another; codes_t and
+ *           scales_t have room for floor((rows + 127 groups) / 128) units, and
+ *           what is behind the last group's is not written.  The rows' code holds
+ *           all rows.  Counts under 0 count as 0, and groups end with the last
+ *           row.  rows (groups + 1) must be under 2^31 and rows / 128 + groups
+ *           under 65535.
+ * muon_fp8_dequantize writes the values of a code (without groups) as F32 or BF16,
+ * both exact down to 2^-133; smaller values are rounded to the type.
+ */
+typedef enum { MUON_E4M3 = 0, MUON_E5M2 = 1, MUON_FP8_FORMAT_RANGE_ = 0x7fffffff } muon_fp8_format;
+
+muon_status muon_fp8_quantize(int batch, int rows, int cols, const void *const *X, muon_dtype x_dtype,
+                              int tile, muon_fp8_format format, const int32_t *counts, int groups,
+                              void *const *codes, void *const *scales,
+                              void *const *codes_t, void *const *scales_t, void *stream);
+muon_status muon_fp8_dequantize(int batch, int rows, int cols, const void *const *codes,
+                                const void *const *scales, muon_fp8_format format, void *const *Y,
+                                muon_dtype y_dtype, void *stream);
+
+/*
+ * C = A B^T, or C += A B^T, of matrices in that code, as muon_mx4_matmul: A is
+ * m x k in a_format, B is n x k in e4m3, C is m x n in c_dtype (F32 or BF16),
+ * row-major.  Sums are fp32; with accumulate the product is added to C in fp32; C
+ * is rounded once.  Results do not depend on timing.  A scale byte 255 makes NaN
+ * of every element of C that its block enters.
+ *   F32 results add exact products (of codes times scales as bf16 numbers: values
+ * under 2^-133 are rounded to bf16's subnormals, those over its range infinite).
+ *   BF16 results of more than 16 rows take the 8-bit matrix instruction, twice as
+ * fast, which adds eight neighbouring products at a time to 13 bits below the
+ * largest of the eight, and those sums in fp32: some 2^-16 of a normal sum off,
+ * where BF16 rounds to 2^-9.
+ *
+ *   workspace  device buffer of at least muon_fp8_workspace_size() bytes, 256-byte
+ *              aligned; contents on entry are ignored.  Calls that share it
+ *              must not overlap.
+ * muon_fp8_workspace_size returns 0 for invalid arguments.  A and B may be the
+ * same matrix; C must be a buffer of its own.
+ */
+size_t muon_fp8_workspace_size(int batch, int m, int n, int k);
+muon_status muon_fp8_matmul(int batch, int m, int n, int k,
+                            const void *const *A_codes, const void *const *A_scales, muon_fp8_format a_format,
+                            const void *const *B_codes, const void *const *B_scales,
+                            void *const *C, muon_dtype c_dtype, int accumulate,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The product over groups of rows, each with its own B (the experts of a mixture,
+ * whose tokens lie behind one another): C[rows of g] = A[rows of g] B_g^T, or +=.
+ * A is rows x k (one matrix, coded along its rows), B_g n x k, C rows x n.
+ *   counts      device array of `groups` row counts, read by the kernels; as for
+ *               muon_fp8_quantize (no bound on rows / 128 + groups).
+ *   clear_rest  0: rows of C behind the last group are left as they were; 1: they
+ *               become 0.
+ * One launch per 128 groups.  No workspace.
+ */
+muon_status muon_fp8_grouped_matmul(int groups, int rows, int n, int k, const int32_t *counts,
+                                    const void *A_codes, const void *A_scales, muon_fp8_format a_format,
+                                    const void *const *B_codes, const void *const *B_scales,
+                                    void *C, muon_dtype c_dtype, int accumulate, int clear_rest, void *stream);
+
+/*
+ * Their weight gradients, the product along groups of k: C_g = A_g B_g^T, or +=,
+ * C_g m x n.  A and B are the columns' codes of a rows x m and a rows x n matrix
+ * (of the output gradient and of the input), made by muon_fp8_quantize with the
+ * same counts.  A group without rows gives zeros (or leaves C_g as it is).
+ */
+muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, const int32_t *counts,
+                                         const void *A_codes, const void *A_scales, muon_fp8_format a_format,
+                                         const void *B_codes, const void *B_scales,
+                                         void *const *C, muon_dtype c_dtype, int accumulate, void *stream);
+
+/*
+ * The balance loss of a mixture's router, the experts' token counts (those that
+ * the products over groups read) and the gradient for the logits, in one call.
+ * For `sequences` x `tokens` rows of `experts` logits z and `top` chosen experts
+ * (indices; K below) a row, with p = softmax(z) (MUON_SOFTMAX) or sigmoid(z) over
+ * its sum (MUON_SIGMOID), T_s the tokens of sequence s that count:
+ *   f_se = experts count_se / (K T_s),
+ *   loss = coefficient / sequences  sum_s sum_e f_se (1 / T_s) sum_t p_ste,
+ *   grad = grad_scale dloss/dz, f held fixed.
+ * A whole batch balanced as one is sequences = 1.
+ *   logits    row r at logits + r row_stride elements (z_dtype F32, BF16 or F16);
+ *             -infinity takes an expert out of a row, and a row without any
+ *             expert has p = 0.  NaN propagates.  Sigmoids that all are under fp32's
+ *             range count as 0.
+ *   index     contiguous, index_bits 32 or 64.  An index outside 0 .. experts - 1 is a
+ *             choice that is not counted; one that is there twice counts twice.
+ *   mask      NULL, or a byte for each row: rows with 0 (padding) do not count, their
+ *             logits and indices are not used, and their gradient is 0.  A sequence
+ *             without tokens adds nothing.
+ *   grad_scale  NULL (= 1), or a device pointer to the loss's own gradient.
+ *   loss      one float.  counts: `experts` int32, over all sequences.
+ *   grad      NULL, or rows x experts of z_dtype, contiguous; with accumulate = 1 the
+ *             gradient is added there (in fp32, rounded once).
+ *   workspace device buffer of at least muon_expert_balance_workspace_size() bytes,
+ *             256-byte aligned; contents on entry are ignored.  Calls that share it
+ *             must not overlap.
+ * Sums are fp32 over a block's rows and fp64 over blocks.  Results do not depend on
+ * timing.  muon_expert_balance_workspace_size returns 0 for invalid arguments: rows and
+ * rows x top must be under 2^31, sequences at most 65535.
+ */
+#define MUON_MAX_EXPERTS 1024
+typedef enum { MUON_SOFTMAX = 0, MUON_SIGMOID = 1, MUON_EXPERT_SCORE_RANGE_ = 0x7fffffff } muon_expert_score;
+
+size_t muon_expert_balance_workspace_size(int sequences, int tokens, int experts, int top);
+muon_status muon_expert_balance(int sequences, int tokens, int experts, int top,
+                                const void *logits, muon_dtype z_dtype, int64_t row_stride,
+                                const void *index, int index_bits, const uint8_t *mask,
+                                muon_expert_score score, double coefficient, const float *grad_scale,
+                                float *loss, int32_t *counts, void *grad, int accumulate,
+                                void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Per-iteration coefficient schedule in the manner of the Polar Express
  * quintics that [GNS §3.2] iterates with (its printed table is garbled, so
  * the schedule is derived from the method's principle rather than copied):
@@ -569,8 +709,8 @@ muon_status muon_mfma_ceiling(int blocks, int rounds, muon_dtype dtype, float *s
 /* Static description of a status code (never NULL). */
 const char *muon_status_string(muon_status status);
 
-/* MUON_ABI_VERSION of the loaded library.  The AdamW and microscaled 4-bit entry points were
- * added without a new version: a library of version 6 has them if it has their symbols. */
+/* MUON_ABI_VERSION of the loaded library.  The AdamW, microscaled 4-bit and 8-bit entry points
+ * were added without a new version: a library of version 6 has them if it has their symbols. */
 int muon_abi_version(void);
 
 #ifdef __cplusplus

@@ -8,7 +8,8 @@ the batch).  There is no fallback: if the library is missing or a call
 fails, an exception is raised.
 
 The entry points that take lists of parameters or one layer's matrices (the
-AdamW steps, the microscaled 4-bit code and product) go through the extension
+AdamW steps, the microscaled 4-bit and the 8-bit code and products) and the
+experts' balance go through the extension
 module ``_native``, which checks the tensors and calls the same C ABI at the
 cost of a launch.  It is loaded at the first of them: the other calls need the
 library alone.
@@ -69,12 +70,18 @@ class _GraspState(ctypes.Structure):
 
 _lib = None
 _native = None
+_fp8_bound = False
 _LIST_CALLS = ("muon_adamw_step", "muon_adamw8_step", "muon_mx4_quantize", "muon_mx4_dequantize",
                "muon_mx4_workspace_size", "muon_mx4_matmul")
 
 
-def _require_list_calls(lib):
-    missing = [name for name in _LIST_CALLS if not hasattr(lib, name)]
+_FP8_CALLS = ("muon_fp8_quantize", "muon_fp8_dequantize", "muon_fp8_workspace_size", "muon_fp8_matmul",
+              "muon_fp8_grouped_matmul", "muon_fp8_grouped_weight_grad", "muon_expert_balance_workspace_size",
+              "muon_expert_balance")
+
+
+def _require_list_calls(lib, names=_LIST_CALLS):
+    missing = [name for name in names if not hasattr(lib, name)]
     if missing:
         raise ImportError(f"{LIB_PATH} has no {missing[0]}: it is an older build of the library")
 
@@ -96,6 +103,22 @@ def _load_native():
                         torch._C._cuda_getCurrentRawStream)
     _native = module
     return module
+
+
+def _declare_fp8_calls(lib):
+    vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    for name, args, result in (
+            ("muon_fp8_quantize", [i32, i32, i32, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp], i32),
+            ("muon_fp8_dequantize", [i32, i32, i32, vp, vp, i32, vp, i32, vp], i32),
+            ("muon_fp8_workspace_size", [i32, i32, i32, i32], sz),
+            ("muon_fp8_matmul", [i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, i32, i32, vp, sz, vp], i32),
+            ("muon_fp8_grouped_matmul", [i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, vp], i32),
+            ("muon_fp8_grouped_weight_grad", [i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, i32, vp], i32),
+            ("muon_expert_balance_workspace_size", [i32, i32, i32, i32], sz),
+            ("muon_expert_balance", [i32, i32, i32, i32, vp, i32, ctypes.c_int64, vp, i32, vp, i32, ctypes.c_double, vp, vp,
+                                     vp, vp, i32, vp, sz, vp], i32)):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = result
 
 
 def _declare_list_calls(lib):
@@ -172,6 +195,8 @@ def load_library():
         getattr(lib, name).restype = i32
     if all(hasattr(lib, name) for name in _LIST_CALLS):  # an older build is fine for the other calls
         _declare_list_calls(lib)
+    if all(hasattr(lib, name) for name in _FP8_CALLS):
+        _declare_fp8_calls(lib)
     _lib = lib
     return lib
 
@@ -780,6 +805,176 @@ def mx4_workspace_size(batch: int, m: int, n: int, k: int) -> int:
     lib = load_library()
     _require_list_calls(lib)
     n = lib.muon_mx4_workspace_size(batch, m, n, k)
+    if n == 0:
+        raise MuonError(1, "invalid arguments for the workspace size")
+    return int(n)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit code with a scale for each block of 128, and its products (muon_fp8_* in include/muon.h)
+# ---------------------------------------------------------------------------
+_FP8_FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+def _fp8_units(cols: int, groups: int = 0) -> int:
+    return (cols + 127 * groups) // 128 if groups else _nb(cols)
+
+
+@dataclass
+class FP8:
+    """A batch of same-shape matrices in the 8-bit code: per matrix float8_e4m3fn or float8_e5m2 codes (2 units, rows, 64)
+    and uint8 scales (units, rows rounded up to 16), units = ceil(cols / 128).  ``cols`` is the length of a row.
+
+    ``groups``: 0, or how many counts a matrix was coded with along its columns (``fp8_quantize(..., counts=)``): each
+    group's part of a row fills whole units, and there is room for (cols + 127 groups) // 128 of them."""
+    codes: list
+    scales: list
+    cols: int
+    groups: int = 0
+
+    @property
+    def rows(self) -> int:
+        return self.codes[0].shape[1]
+
+    @classmethod
+    def empty(cls, batch: int, rows: int, cols: int, device, format: str = "e4m3", groups: int = 0):
+        """Uninitialised buffers for the code of ``batch`` rows x cols matrices."""
+        units, dtype = _fp8_units(cols, groups), _fp8_format(format)
+        return cls([torch.empty(2 * units, rows, 64, dtype=dtype, device=device) for _ in range(batch)],
+                   [torch.empty(units, -(-rows // 16) * 16, dtype=torch.uint8, device=device) for _ in range(batch)],
+                   int(cols), int(groups))
+
+    def _args(self):
+        return self.codes, self.scales, self.cols, self.groups
+
+
+def _fp8_format(name: str):
+    if name not in _FP8_FORMATS:
+        raise ValueError('format must be "e4m3" or "e5m2"')
+    return _FP8_FORMATS[name]
+
+
+def _fp8_call(entry: str, stream, tensors, *args):
+    """_call of an entry that a library may lack which has those of _LIST_CALLS."""
+    global _fp8_bound
+    if not _fp8_bound:
+        module, lib = _load_native(), load_library()
+        _require_list_calls(lib, _FP8_CALLS)
+        module.bind_fp8({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FP8_CALLS})
+        _fp8_bound = True
+    return _call(entry, stream, tensors, *args)
+
+
+def fp8_quantize(X, block: str = "row", transpose=False, format: str = "e4m3", counts=None, out=None, stream=None):
+    """The 8-bit code of the matrices ``X`` (float32, bfloat16 or float16) along their rows, or with ``transpose=True``
+    that of their transposes (along the columns), or with ``transpose="both"`` the pair of both from one read.
+
+    ``block``: "row" (128 elements share a scale) or "tile" (128 x 128 do, so that both orientations hold the same
+    values, as a weight's two codes should).  ``format``: "e4m3" or "e5m2".  ``counts``: an int32 device tensor of the
+    rows of each group (one matrix, its rows sorted by group); the transposed code then has whole units for every group,
+    as fp8_grouped_weight_grad reads it.  ``out``: an FP8 (or a pair) of the right shape to write into."""
+    both = transpose == "both"
+    if not both and transpose is not False and transpose is not True:
+        raise ValueError('transpose must be False, True or "both"')
+    if block not in ("row", "tile"):
+        raise ValueError('block must be "row" or "tile"')
+    e5m2 = _fp8_format(format) is torch.float8_e5m2
+    given = None
+    if out is not None:
+        given = [q._args() for q in (out if both else (out,))]
+        if len(given) != (2 if both else 1):
+            raise ValueError("out must be a pair of codes")
+    status, made = _fp8_call("fp8_quantize", stream, X, X, transpose is not True, transpose is not False, block == "tile",
+                             e5m2, counts, given)
+    if status:
+        _check(status)
+    if out is not None:
+        return out
+    rows, cols = X[0].shape
+    groups = 0 if counts is None else counts.numel()
+    if both:
+        return FP8(*made[0], cols), FP8(*made[1], rows, groups)
+    return FP8(*made[0], rows, groups) if transpose else FP8(*made[0], cols)
+
+
+def fp8_dequantize(q: FP8, dtype=torch.float32, out=None, stream=None):
+    """The values of a code as float32 or bfloat16 matrices (``out``: matrices to write into, of either type)."""
+    status, Y = _fp8_call("fp8_dequantize", stream, q.codes, *q._args(), dtype, out)
+    if status:
+        _check(status)
+    return Y
+
+
+def fp8_matmul(A: FP8, B: FP8, dtype=torch.bfloat16, out=None, accumulate: bool = False, workspace=None, stream=None):
+    """C = A B^T of every pair of coded matrices (A: m x k, e4m3 or e5m2; B: n x k, e4m3), as new float32 or bfloat16 m x n
+    matrices or into ``out``; with ``accumulate`` C += A B^T there.  ``workspace``: a device tensor of
+    fp8_workspace_size() bytes; without one the call takes its scratch from torch's allocator."""
+    status, C = _fp8_call("fp8_matmul", stream, A.codes, A._args(), B._args(), dtype, out, accumulate, workspace)
+    if status:
+        _check(status)
+    return C
+
+
+def fp8_workspace_size(batch: int, m: int, n: int, k: int) -> int:
+    """Bytes of workspace fp8_matmul needs (see muon_fp8_workspace_size in include/muon.h)."""
+    lib = load_library()
+    _require_list_calls(lib, _FP8_CALLS)
+    n = lib.muon_fp8_workspace_size(batch, m, n, k)
+    if n == 0:
+        raise MuonError(1, "invalid arguments for the workspace size")
+    return int(n)
+
+
+def fp8_grouped_matmul(A: FP8, B: FP8, counts, dtype=torch.bfloat16, out=None, accumulate: bool = False, stream=None):
+    """The product over experts: ``A`` is one matrix whose rows are sorted by expert, ``counts`` an int32 device tensor of
+    the rows of each (as expert_balance gives it), ``B`` one n x k matrix for each expert: C[rows of e] = A[rows of e]
+    B_e^T, a list of one matrix.  Rows behind the last expert's are 0 in a new C and left as they are in ``out``."""
+    status, C = _fp8_call("fp8_grouped_matmul", stream, A.codes, A._args(), B._args(), counts, dtype, out, accumulate)
+    if status:
+        _check(status)
+    return C
+
+
+def fp8_grouped_weight_grad(A: FP8, B: FP8, counts, dtype=torch.float32, out=None, accumulate: bool = False, stream=None):
+    """The experts' weight gradients: ``A`` and ``B`` are the transposed codes, made with the same ``counts``, of the output
+    gradient (rows x m) and the input (rows x n); C_e = A_e B_e^T (m x n) for each expert, zeros for one without rows."""
+    status, C = _fp8_call("fp8_grouped_weight_grad", stream, A.codes, A._args(), B._args(), counts, dtype, out, accumulate)
+    if status:
+        _check(status)
+    return C
+
+
+# ---------------------------------------------------------------------------
+# experts' balance (muon_expert_balance in include/muon.h)
+# ---------------------------------------------------------------------------
+def expert_balance(logits, index, coefficient: float, score: str = "softmax", mask=None, grad=None,
+                   accumulate: bool = False, grad_scale=None, workspace=None, stream=None):
+    """The balance loss of a mixture's router, the tokens of each expert, and the gradient for the logits:
+    (loss, counts, gradient).
+
+    ``logits``: (tokens, experts), or (sequences, tokens, experts) to balance each sequence by itself (the loss is their
+    mean), float32, bfloat16 or float16.  ``index``: the chosen experts, int32 or int64, one row a token; an index outside
+    the experts is a choice that is not counted.  With p = softmax(logits) (``score="sigmoid"``: sigmoids over their sum)
+    and f_e = experts count_e / (choices a token x tokens), loss = coefficient sum_e f_e mean_t p_te.  ``mask``: bool or
+    uint8, one element a token, False for padding.
+
+    ``grad``: None, True (a new tensor) or a tensor of the logits' shape and type to write dloss/dlogits into, with
+    ``accumulate`` to add it to; ``grad_scale``: None or a one-element float32 device tensor it is multiplied with.
+    ``loss`` is a float32 scalar, ``counts`` int32, over all sequences."""
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError('score must be "softmax" or "sigmoid"')
+    status, loss, counts, g = _fp8_call("expert_balance", stream, (logits,), logits, index, coefficient, score == "sigmoid",
+                                        mask, None if grad is False else grad, accumulate, grad_scale, workspace)
+    if status:
+        _check(status)
+    return loss, counts, g
+
+
+def expert_balance_workspace_size(sequences: int, tokens: int, experts: int, top: int) -> int:
+    """Bytes of workspace expert_balance needs (see muon_expert_balance_workspace_size in include/muon.h)."""
+    lib = load_library()
+    _require_list_calls(lib, _FP8_CALLS)
+    n = lib.muon_expert_balance_workspace_size(sequences, tokens, experts, top)
     if n == 0:
         raise MuonError(1, "invalid arguments for the workspace size")
     return int(n)

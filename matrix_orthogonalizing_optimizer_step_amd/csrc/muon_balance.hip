@@ -1,0 +1,426 @@
+// The balance loss of a mixture's router, with the experts' token counts and the
+// gradient for the logits.  With p_t the softmax (or the sigmoids over their sum) of
+// token t's logits z_t and f_e = E count_e / (K T) fixed by the choices made,
+//   L = alpha / S sum_s sum_e f_e mean_t p_te = alpha / S sum_s 1 / T_s sum_t <f, p_t>
+//   dL/dz_te = alpha / (S T_s) slope_te (f_e - <f, p_t>),
+// slope = p (softmax) or s (1 - s) / sum s (sigmoids s).  So once the counts are
+// there one pass over the logits gives both: a row's <f, p> is its share of the loss
+// and what its gradient needs; no mean of p is kept.
+//
+// Two launches: the choices are counted in LDS, a partial count for each block; then
+// every block adds the partial counts of its sequence up to f, takes its rows, and
+// the last block to finish adds the blocks' sums in their order, so results do not
+// depend on timing.  Small calls do all of it in one block and one launch.
+#include "../../include/muon.h"
+#include "muon_convert.h"
+#include "muon_internal.h"
+
+namespace muon {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+
+constexpr int kMaxExperts = MUON_MAX_EXPERTS;
+constexpr int kThreads = 256;
+constexpr int kCountThreads = 1024;
+constexpr int kElems = 8;  // of a row, consecutive, in a lane
+
+struct BalanceArgs {
+  int sequences, tokens, experts, top;
+  const void* logits;
+  int64_t stride;          // of rows of the logits, in elements
+  const void* index;       // rows x top
+  int wide;                // 64-bit indices
+  const uint8_t* mask;     // or null
+  int sigmoid;
+  float coefficient;       // alpha / S
+  const float* grad_scale;
+  float* loss;
+  int32_t* counts;
+  void* grad;              // or null
+  int accumulate;
+  int count_blocks, blocks;  // of a sequence; count_blocks 0: one block does everything
+  // workspace: partial counts [sequence][count block][experts + 1], the last one that
+  // of the tokens; sums [sequence][block]; how many blocks are done
+  int32_t* partial;
+  double* sums;
+  int32_t* done;
+};
+
+__device__ __forceinline__ bool counted(const BalanceArgs& a, int64_t row) { return a.mask == nullptr || a.mask[row] != 0; }
+
+// Choices and tokens of rows first .. last - 1 into bins (experts + 1 of them).
+__device__ __forceinline__ void count_rows(const BalanceArgs& a, int64_t first, int64_t last, int32_t* bins) {
+  const uint32_t end = static_cast<uint32_t>(last * a.top);  // under 2^31
+  for (uint32_t p = static_cast<uint32_t>(first * a.top) + threadIdx.x; p < end; p += blockDim.x) {
+    const int64_t e = a.wide ? static_cast<const int64_t*>(a.index)[p] : static_cast<const int32_t*>(a.index)[p];
+    if (e >= 0 && e < a.experts && counted(a, p / static_cast<uint32_t>(a.top))) atomicAdd(bins + e, 1);
+  }
+  if (a.mask == nullptr) {
+    if (threadIdx.x == 0) atomicAdd(bins + a.experts, static_cast<int32_t>(last - first));
+  } else {
+    int n = 0;
+    for (int64_t r = first + threadIdx.x; r < last; r += blockDim.x) n += a.mask[r] != 0;
+    if (n > 0) atomicAdd(bins + a.experts, n);
+  }
+}
+
+__global__ __launch_bounds__(kCountThreads) void balance_count_kernel(BalanceArgs a) {
+  __shared__ int32_t bins[kMaxExperts + 1];
+  for (int e = threadIdx.x; e <= a.experts; e += kCountThreads) bins[e] = 0;
+  __syncthreads();
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * a.tokens;
+  const int64_t first = static_cast<int64_t>(a.tokens) * blockIdx.x / a.count_blocks;
+  const int64_t last = static_cast<int64_t>(a.tokens) * (blockIdx.x + 1) / a.count_blocks;
+  count_rows(a, base + first, base + last, bins);
+  __syncthreads();
+  int32_t* out = a.partial + (static_cast<int64_t>(blockIdx.y) * a.count_blocks + blockIdx.x) * (a.experts + 1);
+  for (int e = threadIdx.x; e <= a.experts; e += kCountThreads) out[e] = bins[e];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.done = 0;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) x += __shfl_xor(x, m);
+  return x;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+  for (int m = 1; m < L; m *= 2) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+// Elements c .. c + 7 of a row of n, `none` behind its end.
+template <int D>
+__device__ __forceinline__ void load8(const void* p, int64_t row, int c, int n, float none, float* x) {
+  if (c + kElems <= n) {
+    if constexpr (D == kF32) {
+      const u32x4_t lo = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(p) + row + c);
+      const u32x4_t hi = *reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(p) + row + c + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __uint_as_float(lo[e]);
+        x[4 + e] = __uint_as_float(hi[e]);
+      }
+    } else {
+      const u32x4_t v = *reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(p) + row + c);
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) {
+        const uint16_t h = static_cast<uint16_t>((e & 1) ? v[e >> 1] >> 16 : v[e >> 1]);
+        x[e] = D == kBF16 ? bf16_to_f32(h) : f16_to_f32(h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) x[e] = c + e < n ? load_as_f32(p, row + c + e, D) : none;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store8(void* p, int64_t row, int c, int n, const float* x) {
+  if (c + kElems <= n) {
+    if constexpr (D == kF32) {
+      float* q = static_cast<float*>(p) + row + c;
+      *reinterpret_cast<u32x4_a4*>(q) = (u32x4_t){__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                                  __float_as_uint(x[3])};
+      *reinterpret_cast<u32x4_a4*>(q + 4) = (u32x4_t){__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]),
+                                                      __float_as_uint(x[7])};
+    } else {
+      u32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = D == kBF16 ? f32x2_to_bf16x2(x[2 * e], x[2 * e + 1]) : f32x2_to_f16x2(x[2 * e], x[2 * e + 1]);
+      *reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(p) + row + c) = v;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kElems; ++e)
+      if (c + e < n) store_from_f32(p, row + c + e, D, x[e]);
+  }
+}
+
+// Rows first, first + step, ... under last: their <f, p> added up (this thread's
+// share of them), their gradients written.  L lanes take a row, lane `o` of them
+// elements 8 (o + L v).
+template <int D, int L, int NV>
+__device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* bins, int64_t first, int64_t last, int step,
+                                           float scale) {
+  const int o = threadIdx.x % L, E = a.experts, tokens = bins[E];
+  const float unit = tokens > 0 ? static_cast<float>(E) / (static_cast<float>(a.top) * static_cast<float>(tokens)) : 0.0f;
+  float f[NV * kElems];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) {
+      const int c = kElems * (o + L * v) + e;
+      f[v * kElems + e] = c < E ? static_cast<float>(bins[c]) * unit : 0.0f;
+    }
+  const float by = tokens > 0 ? scale / static_cast<float>(tokens) : 0.0f;  // of the gradient
+  float total = 0.0f;
+  // all lanes of a row are in the loop together (they share a row)
+  for (int64_t r = first + threadIdx.x / L; r < last; r += step) {
+    const bool valid = counted(a, r);
+    float x[NV * kElems], slope[NV * kElems];
+    float inner = 0.0f;
+    if (valid) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load8<D>(a.logits, r * a.stride, kElems * (o + L * v), E, -INFINITY, x + v * kElems);
+      float sum = 0.0f;
+      if (a.sigmoid) {
+#pragma unroll
+        for (int e = 0; e < NV * kElems; ++e) {
+          const float t = expf(-fabsf(x[e])), q = 1.0f / (1.0f + t);  // the sigmoid of |z|
+          x[e] = x[e] < 0.0f ? t * q : q;
+          slope[e] = t * q * q;
+          sum += x[e];
+        }
+      } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < NV * kElems; ++e) m = fmaxf(m, x[e]);
+        m = lanes_max<L>(m);
+        m = m == -INFINITY ? 0.0f : m;  // nothing to choose from: p = 0
+#pragma unroll
+        for (int e = 0; e < NV * kElems; ++e) {
+          x[e] = expf(x[e] - m);
+          sum += x[e];
+        }
+      }
+      sum = lanes_sum<L>(sum);
+      const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < NV * kElems; ++e) {
+        x[e] *= inverse;
+        slope[e] = a.sigmoid ? slope[e] * inverse : x[e];
+        inner += f[e] * x[e];
+      }
+      inner = lanes_sum<L>(inner);
+      if (o == 0) total += inner;
+    }
+    if (a.grad != nullptr && (valid || !a.accumulate)) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = kElems * (o + L * v);
+        const int64_t row = r * E;
+        float g[kElems] = {};
+        if (a.accumulate && c < E) load8<D>(a.grad, row, c, E, 0.0f, g);
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+          g[e] += valid ? slope[v * kElems + e] * (f[v * kElems + e] - inner) * by : 0.0f;
+        if (c < E) store8<D>(a.grad, row, c, E, g);
+      }
+    }
+  }
+  return total;
+}
+
+__device__ __forceinline__ double block_sum(double x, double* waves) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) x += __shfl_xor(x, m);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = x;
+  __syncthreads();
+  double s = 0.0;
+  for (int w = 0; w < kThreads / 64; ++w) s += waves[w];
+  __syncthreads();
+  return s;
+}
+
+template <int D, int L, int NV>
+__global__ __launch_bounds__(kThreads) void balance_rows_kernel(BalanceArgs a) {
+  __shared__ int32_t bins[kMaxExperts + 1];
+  __shared__ double waves[kThreads / 64];
+  __shared__ int last_block;
+  const int E = a.experts;
+  const float alpha = a.coefficient, scale = alpha * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
+  if (a.count_blocks == 0) {  // one block
+    double total = 0.0;
+    for (int e = threadIdx.x; e < E; e += kThreads) a.counts[e] = 0;
+    for (int s = 0; s < a.sequences; ++s) {
+      __syncthreads();
+      for (int e = threadIdx.x; e <= E; e += kThreads) bins[e] = 0;
+      __syncthreads();
+      const int64_t base = static_cast<int64_t>(s) * a.tokens;
+      count_rows(a, base, base + a.tokens, bins);
+      __syncthreads();
+      for (int e = threadIdx.x; e < E; e += kThreads) a.counts[e] += bins[e];
+      const float sum = take_rows<D, L, NV>(a, bins, base, base + a.tokens, kThreads / L, scale);
+      total += bins[E] > 0 ? static_cast<double>(sum) / bins[E] : 0.0;
+    }
+    total = block_sum(total, waves);
+    if (threadIdx.x == 0) *a.loss = static_cast<float>(total * alpha);
+    return;
+  }
+  const int s = blockIdx.y;
+  const int32_t* partial = a.partial + static_cast<int64_t>(s) * a.count_blocks * (E + 1);
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    int n = 0;
+    for (int b = 0; b < a.count_blocks; ++b) n += partial[b * (E + 1) + e];
+    bins[e] = n;
+  }
+  __syncthreads();
+  const int64_t base = static_cast<int64_t>(s) * a.tokens;
+  const int64_t first = static_cast<int64_t>(a.tokens) * blockIdx.x / a.blocks;
+  const int64_t last = static_cast<int64_t>(a.tokens) * (blockIdx.x + 1) / a.blocks;
+  const float sum = take_rows<D, L, NV>(a, bins, base + first, base + last, kThreads / L, scale);
+  const double mine = block_sum(bins[E] > 0 ? static_cast<double>(sum) / bins[E] : 0.0, waves);
+  const int blocks = a.blocks * a.sequences;
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(a.sums + static_cast<int64_t>(s) * a.blocks + blockIdx.x, mine, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    last_block = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == blocks - 1;
+  }
+  __syncthreads();
+  if (!last_block) return;
+  double total = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += kThreads)
+    total += __hip_atomic_load(a.sums + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  total = block_sum(total, waves);
+  if (threadIdx.x == 0) *a.loss = static_cast<float>(total * alpha);
+  const int parts = a.sequences * a.count_blocks;
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    int n = 0;
+    for (int b = 0; b < parts; ++b) n += a.partial[static_cast<int64_t>(b) * (E + 1) + e];
+    a.counts[e] = n;
+  }
+}
+
+template <int D, int L, int NV>
+void launch_rows(const BalanceArgs& a, hipStream_t s) {
+  const dim3 grid(a.blocks, a.count_blocks == 0 ? 1 : a.sequences);
+  hipLaunchKernelGGL((balance_rows_kernel<D, L, NV>), grid, dim3(kThreads), 0, s, a);
+}
+
+// Lanes of a row: the fewest that hold it, 8 elements each.
+int lanes_of(int experts) {
+  int lanes = 1;
+  while (lanes < 64 && lanes * kElems < experts) lanes *= 2;
+  return lanes;
+}
+
+template <int D>
+hipError_t launch_rows(const BalanceArgs& a, hipStream_t s) {
+  switch (lanes_of(a.experts)) {
+    case 1: launch_rows<D, 1, 1>(a, s); break;
+    case 2: launch_rows<D, 2, 1>(a, s); break;
+    case 4: launch_rows<D, 4, 1>(a, s); break;
+    case 8: launch_rows<D, 8, 1>(a, s); break;
+    case 16: launch_rows<D, 16, 1>(a, s); break;
+    case 32: launch_rows<D, 32, 1>(a, s); break;
+    default:
+      if (a.experts <= 64 * kElems) {
+        launch_rows<D, 64, 1>(a, s);
+      } else {
+        launch_rows<D, 64, 2>(a, s);
+      }
+      break;
+  }
+  return hipGetLastError();
+}
+
+struct Plan {
+  int count_blocks, blocks;  // of a sequence; count_blocks 0: one block in all
+};
+
+Plan plan_of(int sequences, int tokens, int experts, int top) {
+  const int64_t rows = static_cast<int64_t>(sequences) * tokens;
+  const int per = kThreads / lanes_of(experts);  // rows of a block at a time
+  if (rows * top <= 4 * kThreads && rows <= 4 * per && sequences <= 4) return Plan{0, 1};
+  const int64_t entries = static_cast<int64_t>(tokens) * top;
+  int64_t count_blocks = (entries + 16383) / 16384;
+  count_blocks = count_blocks > 32 ? 32 : count_blocks;
+  int64_t blocks = (tokens + per - 1) / per;
+  const int64_t most = sequences < 1024 ? 1024 / sequences : 1;
+  blocks = blocks > most ? most : blocks;
+  return Plan{static_cast<int>(count_blocks), static_cast<int>(blocks)};
+}
+
+int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+int64_t partial_bytes(const Plan& p, int sequences, int experts) {
+  return up256(static_cast<int64_t>(sequences) * p.count_blocks * (experts + 1) * 4);
+}
+int64_t sums_bytes(const Plan& p, int sequences) { return up256(static_cast<int64_t>(sequences) * p.blocks * 8); }
+
+bool sizes_ok(int sequences, int tokens, int experts, int top) {
+  return sequences >= 1 && tokens >= 1 && experts >= 1 && top >= 1 && experts <= kMaxExperts && sequences <= 65535 &&
+         static_cast<int64_t>(sequences) * tokens < (static_cast<int64_t>(1) << 31) &&
+         static_cast<int64_t>(sequences) * tokens * top < (static_cast<int64_t>(1) << 31);
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t muon_expert_balance_workspace_size(int sequences, int tokens, int experts, int top) {
+  if (!sizes_ok(sequences, tokens, experts, top)) return 0;
+  const Plan p = plan_of(sequences, tokens, experts, top);
+  return static_cast<size_t>(partial_bytes(p, sequences, experts) + sums_bytes(p, sequences) + 256);
+}
+
+muon_status muon_expert_balance(int sequences, int tokens, int experts, int top, const void* logits, muon_dtype z_dtype,
+                                int64_t row_stride, const void* index, int index_bits, const uint8_t* mask,
+                                muon_expert_score score, double coefficient, const float* grad_scale, float* loss,
+                                int32_t* counts, void* grad, int accumulate, void* workspace, size_t ws_bytes,
+                                void* stream) {
+  const size_t need = muon_expert_balance_workspace_size(sequences, tokens, experts, top);
+  if (need == 0) return MUON_ERR_INVALID_ARG;
+  if (z_dtype != MUON_F32 && z_dtype != MUON_BF16 && z_dtype != MUON_F16) return MUON_ERR_INVALID_ARG;
+  if (logits == nullptr || index == nullptr || loss == nullptr || counts == nullptr || row_stride < 0 ||
+      (index_bits != 32 && index_bits != 64) || (score != MUON_SOFTMAX && score != MUON_SIGMOID) ||
+      (accumulate != 0 && accumulate != 1) || (accumulate == 1 && grad == nullptr) || grad == logits)
+    return MUON_ERR_INVALID_ARG;
+  const float alpha = static_cast<float>(coefficient / sequences);
+  if (!(coefficient - coefficient == 0.0) || !(alpha - alpha == 0.0f)) return MUON_ERR_INVALID_ARG;  // not finite
+  if (workspace == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MUON_ERR_WORKSPACE;
+  const Plan p = plan_of(sequences, tokens, experts, top);
+  char* ws = static_cast<char*>(workspace);
+  BalanceArgs a;
+  a.sequences = sequences;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.top = top;
+  a.logits = logits;
+  a.stride = row_stride;
+  a.index = index;
+  a.wide = index_bits == 64;
+  a.mask = mask;
+  a.sigmoid = score == MUON_SIGMOID;
+  a.coefficient = alpha;
+  a.grad_scale = grad_scale;
+  a.loss = loss;
+  a.counts = counts;
+  a.grad = grad;
+  a.accumulate = accumulate;
+  a.count_blocks = p.count_blocks;
+  a.blocks = p.blocks;
+  a.partial = reinterpret_cast<int32_t*>(ws);
+  a.sums = reinterpret_cast<double*>(ws + partial_bytes(p, sequences, experts));
+  a.done = reinterpret_cast<int32_t*>(ws + partial_bytes(p, sequences, experts) + sums_bytes(p, sequences));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const double rows = static_cast<double>(sequences) * tokens, size = z_dtype == MUON_F32 ? 4.0 : 2.0;
+  if (p.count_blocks > 0 &&
+      traced_launch(s, "balance_count_kernel", "expert_counts", 0.0, rows * top * index_bits / 8, [&] {
+        hipLaunchKernelGGL(balance_count_kernel, dim3(a.count_blocks, sequences), dim3(kCountThreads), 0, s, a);
+        return hipGetLastError();
+      }) != hipSuccess)
+    return MUON_ERR_HIP;
+  if (traced_launch(s, "balance_rows_kernel", "expert_balance", 8.0 * rows * experts,
+                    rows * experts * size * (grad == nullptr ? 1.0 : accumulate ? 3.0 : 2.0), [&] {
+                      switch (z_dtype) {
+                        case MUON_F32: return launch_rows<kF32>(a, s);
+                        case MUON_BF16: return launch_rows<kBF16>(a, s);
+                        default: return launch_rows<kF16>(a, s);
+                      }
+                    }) != hipSuccess)
+    return MUON_ERR_HIP;
+  return MUON_OK;
+}
+
+}  // extern "C"

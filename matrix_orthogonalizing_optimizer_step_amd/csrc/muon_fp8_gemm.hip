@@ -1,0 +1,227 @@
+// C = A B^T (+ C) of two matrices in the 8-bit code (see muon_fp8_gemm.h for the
+// tiles), with a kernel of its own for at most 16 rows of A.
+#include "muon_fp8_gemm.h"
+
+namespace muon {
+namespace fp8 {
+namespace {
+
+template <class T, int FA, bool EXACT>
+__global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_tile_gemm_kernel(Fp8GemmArgs a, int tm, int tn) {
+  FP8_LDS(T);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  int outer, ti, tj;
+  tile_of(blockIdx.x, gridDim.x, tm, tn, &outer, &ti, &tj);
+  const int b = outer / a.pieces, piece = outer - b * a.pieces;
+  const int i0 = ti * T::TM, j0 = tj * T::TN;
+  const int ub = piece * a.piece_units, ue = ub + a.piece_units < a.units ? ub + a.piece_units : a.units;
+  const Source A{a.A[b], 0, static_cast<uint32_t>(a.m)};
+  const Source B{a.B[b], 0, static_cast<uint32_t>(a.n)};
+  f32x16_t acc[T::FN][T::FM] = {};
+  tile_product<T, FA, EXACT>(acc, lds, A, B, a.As[b], a.Bs[b], i0, j0, ub, ue, a.units, wave, lane);
+  const int i = i0 + T::FM * 32 * (wave / T::WN), j = j0 + T::FN * 32 * (wave % T::WN);  // this wave's first row, column
+  typename T::Stage& stage = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
+  if (a.pieces > 1) {
+    float* part = a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n;
+    store_tile<T, kF32, false>(part, acc, stage.code, i, j, a.m, a.n, lane);
+  } else {
+    store_product<T, EXACT>(a.C[b], acc, stage, i, j, a.m, a.n, lane, a.accumulate);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The pieces of a product that was split along k, added in their order.
+// ---------------------------------------------------------------------------
+template <int DC>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs a) {
+  const int b = blockIdx.z;
+  const int64_t mn = static_cast<int64_t>(a.m) * a.n, step = static_cast<int64_t>(a.batch) * mn;
+  const float* part = a.partial + b * mn;
+  void* C = a.C[b];
+  const bool vec = (mn & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (DC == kF32 ? 15u : 7u)) == 0;
+  for (int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; at < mn;
+       at += static_cast<int64_t>(gridDim.x) * 1024) {
+    const int left = mn - at < 4 ? static_cast<int>(mn - at) : 4;
+    float v[4] = {};
+    for (int p = 0; p < a.pieces; ++p) {
+      if (vec) {
+        const float4 x = *reinterpret_cast<const float4*>(part + p * step + at);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) v[e] += part[p * step + at + e];
+      }
+    }
+    store_quad<DC>(C, at, v, left, vec, a.accumulate);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// At most 16 rows of A (a few tokens against a weight): the codes of B are what
+// has to be read.  A wave takes 16 rows of B (a lane 32 bytes of one row; a unit of
+// 16 rows is two runs of 1 KB) and every NW-th unit of k, straight from memory into
+// registers, and multiplies as kExact does (16x16x32 MFMAs; memory takes longer than
+// the conversions).  The block's NW sums are added in LDS, in their order.  Rows of A
+// behind the last one repeat it and are not stored.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 16;
+constexpr int kUnitsAhead = 2;
+
+template <int FA, int S>
+__device__ __forceinline__ f32x4_t few_step(f32x4_t acc, const Frag& a, const Frag& b, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16<kE4M3, S>(b, sb), to_bf16<FA, S>(a, sa), acc, 0, 0, 0);
+}
+
+template <int NW, int FA>
+__global__ __launch_bounds__(64 * NW) void fp8_few_rows_kernel(Fp8GemmArgs a) {
+  __shared__ f32x4_t sums[NW][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, b = blockIdx.z;
+  const int j0 = blockIdx.x * 16, r = lane & 15, part = lane >> 4;
+  const int ra = r < a.m ? r : a.m - 1, rb = j0 + r < a.n ? j0 + r : a.n - 1;
+  const int64_t pa = fp8_pitch(a.m), pb = fp8_pitch(a.n);
+  const uint4* A = static_cast<const uint4*>(a.A[b]) + (static_cast<int64_t>(part >> 1) * a.m + ra) * 4 + (part & 1) * 2;
+  const uint4* B = static_cast<const uint4*>(a.B[b]) + (static_cast<int64_t>(part >> 1) * a.n + rb) * 4 + (part & 1) * 2;
+  const uint8_t* As = static_cast<const uint8_t*>(a.As[b]) + ra;
+  const uint8_t* Bs = static_cast<const uint8_t*>(a.Bs[b]) + rb;
+  f32x4_t acc = {};
+  for (int u0 = wave; u0 < a.units; u0 += NW * kUnitsAhead) {
+    Frag av[kUnitsAhead], bv[kUnitsAhead];
+    uint32_t sa[kUnitsAhead], sb[kUnitsAhead];
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k) {
+      const int64_t u = u0 + k * NW < a.units ? u0 + k * NW : u0;  // one behind the last unit is not used
+      av[k].lo = A[u * 8 * a.m];
+      av[k].hi = A[u * 8 * a.m + 1];
+      bv[k].lo = B[u * 8 * a.n];
+      bv[k].hi = B[u * 8 * a.n + 1];
+      sa[k] = As[u * pa];
+      sb[k] = Bs[u * pb];
+    }
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k)
+      if (u0 + k * NW < a.units) {
+        acc = few_step<FA, 0>(acc, av[k], bv[k], sa[k], sb[k]);
+        acc = few_step<FA, 1>(acc, av[k], bv[k], sa[k], sb[k]);
+        acc = few_step<FA, 2>(acc, av[k], bv[k], sa[k], sb[k]);
+        acc = few_step<FA, 3>(acc, av[k], bv[k], sa[k], sb[k]);
+      }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  // lane l: row l % 16 of C, columns 4 (l / 16) .. + 3
+  const int j = j0 + 4 * part;
+  if (r >= a.m || j >= a.n) return;
+  f32x4_t s = sums[0][lane];
+#pragma unroll
+  for (int q = 1; q < NW; ++q) s += sums[q][lane];
+  const float v[4] = {s[0], s[1], s[2], s[3]};
+  void* C = a.C[b];
+  const bool vec = (a.n & 3) == 0 && (reinterpret_cast<uintptr_t>(C) & (a.c_dtype == kF32 ? 15u : 7u)) == 0;
+  const int64_t at = static_cast<int64_t>(r) * a.n + j;
+  if (a.c_dtype == kF32) {
+    store_quad<kF32>(C, at, v, a.n - j, vec, a.accumulate);
+  } else {
+    store_quad<kBF16>(C, at, v, a.n - j, vec, a.accumulate);
+  }
+}
+
+template <class T>
+int64_t tiles_of(int batch, int m, int n) {
+  return static_cast<int64_t>(ceil_div(m, T::TM)) * ceil_div(n, T::TN) * batch;
+}
+
+// Pieces along k of a product in 64 x 128 tiles that leave compute units idle:
+// the fewest microseconds of a unit (two slabs, one block on a compute unit) plus,
+// for more than one piece, the joining launch and the partial sums' way through
+// memory (8 bytes an element and piece at 6 TB/s).
+void split_k(int64_t tiles, int units, double elements, Fp8Plan* p) {
+  constexpr int kMinUnits = 4;  // of a piece
+  double best = 0.0;
+  for (int q = 1; q * tiles <= kCUs && (q == 1 || units / q >= kMinUnits); ++q) {
+    const double us = ceil_div(units, q) * 0.52 + (q > 1 ? 4.5 + q * elements * 8.0 / 6e6 : 0.0);
+    if (q == 1 || us < best) {
+      best = us;
+      p->piece_units = ceil_div(units, q);
+      p->pieces = ceil_div(units, p->piece_units);
+    }
+  }
+}
+
+template <class T>
+void launch_tiles(const Fp8GemmArgs& a, hipStream_t s) {
+  const int tm = ceil_div(a.m, T::TM), tn = ceil_div(a.n, T::TN);
+  const dim3 grid(static_cast<uint32_t>(tm) * tn * a.batch * a.pieces), block(256);
+  const bool e4m3 = a.a_format == kE4M3;
+  if (a.c_dtype == kF32) {
+    auto* kernel = e4m3 ? fp8_tile_gemm_kernel<T, kE4M3, kExact> : fp8_tile_gemm_kernel<T, kE5M2, kExact>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+  } else {
+    auto* kernel = e4m3 ? fp8_tile_gemm_kernel<T, kE4M3, kFast> : fp8_tile_gemm_kernel<T, kE5M2, kFast>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+  }
+}
+
+template <int NW>
+void launch_few(const Fp8GemmArgs& a, hipStream_t s) {
+  const dim3 grid(ceil_div(a.n, 16), 1, a.batch), block(64 * NW);
+  if (a.a_format == kE4M3) {
+    hipLaunchKernelGGL((fp8_few_rows_kernel<NW, kE4M3>), grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((fp8_few_rows_kernel<NW, kE5M2>), grid, block, 0, s, a);
+  }
+}
+
+}  // namespace
+}  // namespace fp8
+
+using namespace fp8;
+
+Fp8Plan fp8_plan(int batch, int m, int n, int k) {
+  const int units = static_cast<int>(fp8_units(k));
+  Fp8Plan p{kF8FewRows, 1, units, 0};
+  if (m <= kFewRows) return p;
+  const int64_t big = tiles_of<Big>(batch, m, n), low = tiles_of<Low>(batch, m, n);
+  const int64_t rounds = (big + kCUs - 1) / kCUs;
+  if (big * 3 >= rounds * kCUs * 2) {
+    p.kind = kF8Big;
+  } else if (low * 2 <= kCUs * 3) {
+    p.kind = kF8Low;
+    const double elements = static_cast<double>(batch) * m * n;
+    split_k(low, units, elements, &p);
+    if (p.pieces > 1) p.bytes = static_cast<size_t>(p.pieces) * batch * m * n * sizeof(float);
+  } else {
+    p.kind = kF8Mid;
+  }
+  return p;
+}
+
+hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, Fp8Kind kind, hipStream_t s) {
+  switch (kind) {
+    case kF8Big: launch_tiles<Big>(a, s); break;
+    case kF8Mid: launch_tiles<Mid>(a, s); break;
+    case kF8Low: launch_tiles<Low>(a, s); break;
+    default:
+      if (a.units >= 64 && ceil_div(a.n, 16) * a.batch <= kCUs) {
+        launch_few<16>(a, s);
+      } else {
+        launch_few<8>(a, s);
+      }
+      break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_join(const Fp8GemmArgs& a, hipStream_t s) {
+  const int64_t blocks = (static_cast<int64_t>(a.m) * a.n + 1023) / 1024;
+  const dim3 grid(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), 1, a.batch), block(256);
+  if (a.c_dtype == kF32) {
+    hipLaunchKernelGGL(fp8_join_kernel<kF32>, grid, block, 0, s, a);
+  } else {
+    hipLaunchKernelGGL(fp8_join_kernel<kBF16>, grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -17,7 +17,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kCUs = 256;  // compute units of the MI355X: plans depend on shapes only
-constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;  // sched_group_barrier masks
+constexpr int kSchedValu = 0x002, kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;  // sched_group_barrier masks
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 

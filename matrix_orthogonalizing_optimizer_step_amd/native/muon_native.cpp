@@ -1,5 +1,6 @@
 // Argument marshalling of the entry points that take HOST arrays of pointers
-// (the AdamW steps and the microscaled 4-bit code and product): checks lists of
+// (the AdamW steps, the microscaled 4-bit and the 8-bit code and products) and of
+// the experts' balance: checks lists of
 // torch tensors, makes the outputs and calls the C ABI of libmuon.so, whose
 // functions binding.py hands over once (so the library that MUON_LIBRARY names
 // is the one that runs).  A call costs the host about as much as its launch; in
@@ -26,6 +27,14 @@ struct Functions {
   decltype(&muon_mx4_dequantize) dequantize = nullptr;
   decltype(&muon_mx4_workspace_size) workspace_size = nullptr;
   decltype(&muon_mx4_matmul) matmul = nullptr;
+  decltype(&muon_fp8_quantize) fp8_quantize = nullptr;
+  decltype(&muon_fp8_dequantize) fp8_dequantize = nullptr;
+  decltype(&muon_fp8_workspace_size) fp8_workspace_size = nullptr;
+  decltype(&muon_fp8_matmul) fp8_matmul = nullptr;
+  decltype(&muon_fp8_grouped_matmul) fp8_grouped_matmul = nullptr;
+  decltype(&muon_fp8_grouped_weight_grad) fp8_grouped_weight_grad = nullptr;
+  decltype(&muon_expert_balance_workspace_size) balance_workspace_size = nullptr;
+  decltype(&muon_expert_balance) balance = nullptr;
 } fn;
 
 PyObject* raw_stream_fn = nullptr;  // torch._C._cuda_getCurrentRawStream
@@ -44,6 +53,18 @@ void bind_library(const py::dict& addresses, const py::object& raw_stream) {
   take(fn.matmul, addresses, "muon_mx4_matmul");
   Py_XDECREF(raw_stream_fn);
   raw_stream_fn = py::object(raw_stream).release().ptr();
+}
+
+// The 8-bit calls and the experts' balance, which an older library may lack.
+void bind_fp8(const py::dict& addresses) {
+  take(fn.fp8_quantize, addresses, "muon_fp8_quantize");
+  take(fn.fp8_dequantize, addresses, "muon_fp8_dequantize");
+  take(fn.fp8_workspace_size, addresses, "muon_fp8_workspace_size");
+  take(fn.fp8_matmul, addresses, "muon_fp8_matmul");
+  take(fn.fp8_grouped_matmul, addresses, "muon_fp8_grouped_matmul");
+  take(fn.fp8_grouped_weight_grad, addresses, "muon_fp8_grouped_weight_grad");
+  take(fn.balance_workspace_size, addresses, "muon_expert_balance_workspace_size");
+  take(fn.balance, addresses, "muon_expert_balance");
 }
 
 void* current_stream(const at::Device& device) {
@@ -452,6 +473,306 @@ py::tuple mx4_matmul(const py::object& a_codes, const py::object& a_scales, cons
   return py::make_tuple(buffers.called(st), C);
 }
 
+// A call's scratch, from the allocator at every call: its memory is reused in the
+// stream's order, and under capture it belongs to the graph, so two graphs never
+// share it.  Or the caller's.
+at::Tensor scratch(const py::object& workspace, size_t need, const at::Device& device, Buffers& buffers) {
+  if (workspace.is_none())
+    return at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(device));
+  if (!THPVariable_Check(workspace.ptr())) refuse("workspace must be a device tensor");
+  const at::Tensor& ws = THPVariable_Unpack(workspace.ptr());  // the Python object's, which outlives the call
+  if (ws.device() != device || !ws.is_contiguous()) refuse("workspace must be a contiguous tensor on the device of the operands");
+  buffers.add(ws, true);
+  return ws;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit code with a scale for each block of 128
+// ---------------------------------------------------------------------------
+// A batch of codes: (codes, scales) lists, the length of a row and, if its rows were
+// coded in groups, their number.
+struct Fp8Codes {
+  std::vector<void*> codes, scales;
+  int64_t rows = 0, cols = 0, groups = 0;
+  muon_fp8_format format = MUON_E4M3;
+  at::Device device{at::kCPU};
+
+  static int64_t units(int64_t k, int64_t groups) { return groups > 0 ? (k + 127 * groups) / 128 : units_of(k); }
+  static int64_t pitch(int64_t rows) { return (rows + 15) / 16 * 16; }
+
+  Fp8Codes() = default;
+  Fp8Codes(const py::object& code_list, const py::object& scale_list, int64_t k, int64_t g, const char* name,
+           Buffers* buffers, bool written)
+      : cols(k), groups(g) {
+    const auto c = tensors_of(code_list, name), s = tensors_of(scale_list, name);
+    if (c.empty() || c.size() != s.size())
+      refuse(std::string(name) + ": codes and scales must hold one tensor per matrix");
+    const at::ScalarType type = c[0]->scalar_type();
+    if (type != at::kFloat8_e4m3fn && type != at::kFloat8_e5m2)
+      refuse(std::string(name) + ": codes must be float8_e4m3fn or float8_e5m2");
+    format = type == at::kFloat8_e4m3fn ? MUON_E4M3 : MUON_E5M2;
+    if (k < 1 || k > INT32_MAX || g < 0 || g > INT32_MAX || c[0]->dim() != 3 || c[0]->size(0) != 2 * units(k, g) ||
+        c[0]->size(1) < 1 || c[0]->size(2) != 64)
+      refuse(std::string(name) + ": codes must be (2 * units, rows, 64), units = ceil(cols / 128), or with groups "
+                                 "(cols + 127 * groups) // 128");
+    rows = c[0]->size(1);
+    device = c[0]->device();
+    if (!device.is_cuda()) refuse(std::string(name) + ": codes must be device tensors");
+    codes.reserve(c.size());
+    scales.reserve(c.size());
+    for (size_t i = 0; i < c.size(); ++i) {
+      if (c[i]->scalar_type() != type || c[i]->device() != device || c[i]->sizes() != c[0]->sizes())
+        refuse(std::string(name) + ": all codes must share type, shape and device");
+      if (s[i]->scalar_type() != at::kByte || s[i]->device() != device || s[i]->dim() != 2 ||
+          s[i]->size(0) != units(k, g) || s[i]->size(1) != pitch(rows))
+        refuse(std::string(name) + ": scales must be uint8 (units, rows rounded up to 16) on the codes' device");
+      for (const at::Tensor* t : {c[i], s[i]}) {
+        void* const p = t->data_ptr();
+        if (!t->is_contiguous() || reinterpret_cast<uintptr_t>(p) % 16 != 0)
+          refuse(std::string(name) + ": codes and scales must be contiguous and 16-byte aligned");
+        (t == c[i] ? codes : scales).push_back(p);
+        if (buffers != nullptr) buffers->add(*t, written);
+      }
+    }
+  }
+  // New buffers for `batch` matrices, appended to the given lists.
+  Fp8Codes(int batch, int64_t r, int64_t k, int64_t g, muon_fp8_format f, const at::Device& d, py::list code_list,
+           py::list scale_list)
+      : rows(r), cols(k), groups(g), format(f), device(d) {
+    const int64_t u = units(k, g), code_bytes = u * r * 128, scale_bytes = u * pitch(r);  // multiples of 16
+    const at::Tensor flat = at::empty({batch * (code_bytes + scale_bytes)}, at::TensorOptions().dtype(at::kByte).device(d));
+    const at::ScalarType type = f == MUON_E4M3 ? at::kFloat8_e4m3fn : at::kFloat8_e5m2;
+    const at::Tensor all = flat.view(type);
+    for (int b = 0; b < batch; ++b) {
+      const at::Tensor c = all.as_strided({2 * u, r, 64}, {r * 64, 64, 1}, b * code_bytes);
+      const at::Tensor s = flat.as_strided({u, pitch(r)}, {pitch(r), 1}, batch * code_bytes + b * scale_bytes);
+      codes.push_back(c.data_ptr());
+      scales.push_back(s.data_ptr());
+      code_list.append(c);
+      scale_list.append(s);
+    }
+  }
+  int batch() const { return static_cast<int>(codes.size()); }
+  const void* const* c() const { return const_cast<const void* const*>(codes.data()); }
+  const void* const* s() const { return const_cast<const void* const*>(scales.data()); }
+};
+
+// Row counts of groups: a contiguous int32 device tensor.
+const int32_t* counts_pointer(const py::object& o, const at::Device& device, int64_t* groups, Buffers& buffers) {
+  if (!THPVariable_Check(o.ptr())) refuse("counts: a device tensor is needed");
+  const at::Tensor& t = THPVariable_Unpack(o.ptr());
+  if (t.scalar_type() != at::kInt || t.dim() != 1 || t.numel() < 1 || !t.is_contiguous() || t.device() != device)
+    refuse("counts must be a contiguous 1-D int32 tensor on the device of the operands");
+  *groups = t.numel();
+  return static_cast<const int32_t*>(buffers.add(t, false));
+}
+
+// out: None, or per orientation (codes, scales, cols, groups).  Returns (status, codes
+// and scales lists of each orientation).
+py::tuple fp8_quantize(const py::object& X, bool along, bool across, bool tile, bool e5m2, const py::object& counts,
+                       const py::object& out) {
+  Buffers buffers;
+  const Matrices x(X, "X", &buffers, false);
+  const c10::DeviceGuard guard(x.device);
+  const muon_fp8_format format = e5m2 ? MUON_E5M2 : MUON_E4M3;
+  int64_t groups = 0;
+  const int32_t* const n = counts.is_none() ? nullptr : counts_pointer(counts, x.device, &groups, buffers);
+  if (n != nullptr && (!across || tile || x.batch() != 1))
+    refuse("counts: one matrix, coded in blocks of a row, with its transposed code");
+  Fp8Codes q[2];
+  py::list made;
+  int given = 0;
+  for (int o = 0; o < 2; ++o) {
+    if (!(o == 0 ? along : across)) continue;
+    const int64_t r = o == 0 ? x.rows : x.cols, k = o == 0 ? x.cols : x.rows, g = o == 0 ? 0 : groups;
+    if (out.is_none()) {
+      if (r < 1 || k < 1) refuse("X: matrices must not be empty");
+      py::list c, s;
+      q[o] = Fp8Codes(x.batch(), r, k, g, format, x.device, c, s);
+      made.append(py::make_tuple(c, s));
+    } else {
+      const py::tuple t = out.cast<py::sequence>()[given++].cast<py::tuple>();
+      q[o] = Fp8Codes(t[0], t[1], t[2].cast<int64_t>(), t[3].cast<int64_t>(), "out", &buffers, true);
+      if (q[o].batch() != x.batch() || q[o].rows != r || q[o].cols != k || q[o].groups != g || q[o].device != x.device ||
+          q[o].format != format)
+        refuse("out must have the shape, batch, groups, format and device of the result");
+    }
+  }
+  buffers.check();
+  const muon_status st = fn.fp8_quantize(x.batch(), as_int(x.rows), as_int(x.cols), x.in(), x.dtype, tile ? 1 : 0, format, n,
+                                         as_int(groups), along ? q[0].codes.data() : nullptr,
+                                         along ? q[0].scales.data() : nullptr, across ? q[1].codes.data() : nullptr,
+                                         across ? q[1].scales.data() : nullptr, current_stream(x.device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), made);
+}
+
+py::tuple fp8_dequantize(const py::object& codes, const py::object& scales, int64_t cols, int64_t groups,
+                         const py::object& dtype, const py::object& out) {
+  Buffers buffers;
+  const Fp8Codes q(codes, scales, cols, groups, "q", &buffers, false);
+  if (groups != 0) refuse("q: a code in groups has no values of its own");
+  const at::ScalarType t = value_type(dtype);
+  const c10::DeviceGuard guard(q.device);
+  const py::object Y = out.is_none() ? py::object(new_matrices(q.batch(), q.rows, cols, t, q.device)) : out;
+  const Matrices y(Y, "out", &buffers, true);
+  if (y.batch() != q.batch() || y.rows != q.rows || y.cols != cols || y.device != q.device)
+    refuse("out must have the shape, batch and device of the result");
+  buffers.check();
+  const muon_status st = fn.fp8_dequantize(q.batch(), as_int(q.rows), as_int(cols), q.c(), q.s(), q.format, y.ptr.data(),
+                                           y.dtype, current_stream(q.device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), Y);
+}
+
+void check_operands(const Fp8Codes& a, const Fp8Codes& b) {
+  if (a.cols != b.cols || a.device != b.device) refuse("A and B must share the row length and the device");
+  if (b.format != MUON_E4M3) refuse("B must be coded in e4m3 (A may be e5m2)");
+}
+
+// Returns (status, C), as the two calls below.
+py::tuple fp8_matmul(const py::tuple& A, const py::tuple& B, const py::object& dtype, const py::object& out, bool accumulate,
+                     const py::object& workspace) {
+  Buffers buffers;
+  const Fp8Codes a(A[0], A[1], A[2].cast<int64_t>(), A[3].cast<int64_t>(), "A", &buffers, false);
+  const Fp8Codes b(B[0], B[1], B[2].cast<int64_t>(), B[3].cast<int64_t>(), "B", &buffers, false);
+  check_operands(a, b);
+  if (a.groups != 0 || b.groups != 0) refuse("a code in groups takes part in fp8_grouped_weight_grad only");
+  if (a.batch() != b.batch()) refuse("A and B must share the batch");
+  if (accumulate && out.is_none()) refuse("accumulate needs out");
+  const c10::DeviceGuard guard(a.device);
+  const size_t need = fn.fp8_workspace_size(a.batch(), as_int(a.rows), as_int(b.rows), as_int(a.cols));
+  if (need == 0) return py::make_tuple(static_cast<int>(MUON_ERR_INVALID_ARG), py::none());
+  const py::object C =
+      out.is_none() ? py::object(new_matrices(a.batch(), a.rows, b.rows, value_type(dtype), a.device)) : out;
+  const Matrices c(C, "out", &buffers, true);
+  if (c.batch() != a.batch() || c.rows != a.rows || c.cols != b.rows || c.device != a.device)
+    refuse("out must have one m x n matrix per pair, on the same device");
+  const at::Tensor ws = scratch(workspace, need, a.device, buffers);
+  buffers.check();
+  const muon_status st = fn.fp8_matmul(a.batch(), as_int(a.rows), as_int(b.rows), as_int(a.cols), a.c(), a.s(), a.format,
+                                       b.c(), b.s(), c.ptr.data(), c.dtype, accumulate ? 1 : 0, ws.data_ptr(), ws.nbytes(),
+                                       current_stream(a.device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), C);
+}
+
+py::tuple fp8_grouped_matmul(const py::tuple& A, const py::tuple& B, const py::object& counts, const py::object& dtype,
+                             const py::object& out, bool accumulate) {
+  Buffers buffers;
+  const Fp8Codes a(A[0], A[1], A[2].cast<int64_t>(), A[3].cast<int64_t>(), "A", &buffers, false);
+  const Fp8Codes b(B[0], B[1], B[2].cast<int64_t>(), B[3].cast<int64_t>(), "B", &buffers, false);
+  check_operands(a, b);
+  if (a.groups != 0 || b.groups != 0) refuse("a code in groups takes part in fp8_grouped_weight_grad only");
+  int64_t groups = 0;
+  const int32_t* const n = counts_pointer(counts, a.device, &groups, buffers);
+  if (a.batch() != 1 || b.batch() != groups) refuse("A must be one matrix, and B one for each of the counts");
+  if (accumulate && out.is_none()) refuse("accumulate needs out");
+  const c10::DeviceGuard guard(a.device);
+  const py::object C = out.is_none() ? py::object(new_matrices(1, a.rows, b.rows, value_type(dtype), a.device)) : out;
+  const Matrices c(C, "out", &buffers, true);
+  if (c.batch() != 1 || c.rows != a.rows || c.cols != b.rows || c.device != a.device)
+    refuse("out must be one m x n matrix on the same device");
+  buffers.check();
+  const muon_status st = fn.fp8_grouped_matmul(as_int(groups), as_int(a.rows), as_int(b.rows), as_int(a.cols), n, a.codes[0],
+                                               a.scales[0], a.format, b.c(), b.s(), c.ptr[0], c.dtype, accumulate ? 1 : 0,
+                                               out.is_none() ? 1 : 0, current_stream(a.device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), C);
+}
+
+py::tuple fp8_grouped_weight_grad(const py::tuple& A, const py::tuple& B, const py::object& counts, const py::object& dtype,
+                                  const py::object& out, bool accumulate) {
+  Buffers buffers;
+  const Fp8Codes a(A[0], A[1], A[2].cast<int64_t>(), A[3].cast<int64_t>(), "A", &buffers, false);
+  const Fp8Codes b(B[0], B[1], B[2].cast<int64_t>(), B[3].cast<int64_t>(), "B", &buffers, false);
+  check_operands(a, b);
+  int64_t groups = 0;
+  const int32_t* const n = counts_pointer(counts, a.device, &groups, buffers);
+  if (a.batch() != 1 || b.batch() != 1 || a.groups != groups || b.groups != groups)
+    refuse("A and B must be one matrix each, coded along columns with as many counts");
+  if (accumulate && out.is_none()) refuse("accumulate needs out");
+  const c10::DeviceGuard guard(a.device);
+  const py::object C =
+      out.is_none() ? py::object(new_matrices(as_int(groups), a.rows, b.rows, value_type(dtype), a.device)) : out;
+  const Matrices c(C, "out", &buffers, true);
+  if (c.batch() != groups || c.rows != a.rows || c.cols != b.rows || c.device != a.device)
+    refuse("out must have one m x n matrix per group, on the same device");
+  buffers.check();
+  const muon_status st = fn.fp8_grouped_weight_grad(as_int(groups), as_int(a.cols), as_int(a.rows), as_int(b.rows), n,
+                                                    a.codes[0], a.scales[0], a.format, b.codes[0], b.scales[0], c.ptr.data(),
+                                                    c.dtype, accumulate ? 1 : 0, current_stream(a.device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), C);
+}
+
+// ---------------------------------------------------------------------------
+// experts' balance
+// ---------------------------------------------------------------------------
+const at::Tensor& one_tensor(const py::object& o, const char* name) {
+  if (!THPVariable_Check(o.ptr())) refuse(std::string(name) + ": a device tensor is needed");
+  return THPVariable_Unpack(o.ptr());
+}
+
+// grad: None (no gradient), True (a new one) or a tensor.  Returns (status, loss, counts, gradient).
+py::tuple expert_balance(const py::object& logits, const py::object& index, double coefficient, bool sigmoid,
+                         const py::object& mask, const py::object& grad, bool accumulate, const py::object& grad_scale,
+                         const py::object& workspace) {
+  Buffers buffers;
+  const at::Tensor &z = one_tensor(logits, "logits"), &choice = one_tensor(index, "index");
+  const at::Device device = z.device();
+  if (!device.is_cuda()) refuse("logits must be a device tensor");
+  const muon_dtype type = dtype_of(z, "logits");
+  const int64_t dim = z.dim();
+  if (dim != 2 && dim != 3) refuse("logits must be (tokens, experts) or (sequences, tokens, experts)");
+  const int64_t S = dim == 3 ? z.size(0) : 1, T = z.size(dim - 2), E = z.size(dim - 1);
+  if (z.numel() == 0) refuse("logits must not be empty");
+  const int64_t stride = z.stride(dim - 2);
+  if ((E > 1 && z.stride(dim - 1) != 1) || stride < 0 || (S > 1 && T > 1 && z.stride(0) != T * stride))
+    refuse("logits: the experts of a token must lie behind one another, and all tokens one stride apart");
+  const int64_t step = T > 1 ? stride : (dim == 3 ? z.stride(0) : stride);
+  if (choice.dim() != dim || choice.size(dim - 1) < 1 || choice.device() != device ||
+      (choice.scalar_type() != at::kInt && choice.scalar_type() != at::kLong) || !choice.is_contiguous())
+    refuse("index must be a contiguous int32 or int64 tensor on the device of the logits, with one row a token");
+  for (int64_t d = 0; d + 1 < dim; ++d)
+    if (choice.size(d) != z.size(d)) refuse("index must have one row for each row of the logits");
+  const int64_t K = choice.size(dim - 1);
+  buffers.add(z, false);
+  buffers.add(choice, false);
+  const uint8_t* m = nullptr;
+  if (!mask.is_none()) {
+    const at::Tensor& t = one_tensor(mask, "mask");
+    if ((t.scalar_type() != at::kBool && t.scalar_type() != at::kByte) || !t.is_contiguous() || t.device() != device ||
+        t.dim() != dim - 1 || t.size(0) != z.size(0) || (dim == 3 && t.size(1) != T))
+      refuse("mask must be a contiguous bool or uint8 tensor on the device of the logits, one element a token");
+    m = static_cast<const uint8_t*>(buffers.add(t, false));
+  }
+  const float* scale = nullptr;
+  if (!grad_scale.is_none())
+    scale = static_cast<const float*>(scalar_pointer(grad_scale, "grad_scale", at::kFloat, device, buffers));
+  const c10::DeviceGuard guard(device);
+  const size_t need = fn.balance_workspace_size(as_int(S), as_int(T), as_int(E), as_int(K));
+  if (need == 0)
+    return py::make_tuple(static_cast<int>(MUON_ERR_INVALID_ARG), py::none(), py::none(), py::none());
+  const auto options = at::TensorOptions().device(device);
+  at::Tensor g;
+  if (grad.ptr() == Py_True) {
+    if (accumulate) refuse("accumulate needs a gradient to add to");
+    g = at::empty(z.sizes(), options.dtype(z.scalar_type()));
+  } else if (!grad.is_none()) {
+    g = one_tensor(grad, "grad");
+    if (g.scalar_type() != z.scalar_type() || g.sizes() != z.sizes() || g.device() != device || !g.is_contiguous())
+      refuse("grad must be contiguous, of the shape, dtype and device of the logits");
+    buffers.add(g, true);
+  } else if (accumulate) {
+    refuse("accumulate needs a gradient to add to");
+  }
+  const at::Tensor loss = at::empty({}, options.dtype(at::kFloat)), counts = at::empty({E}, options.dtype(at::kInt));
+  const at::Tensor ws = scratch(workspace, need, device, buffers);
+  buffers.check();
+  const muon_status st =
+      fn.balance(as_int(S), as_int(T), as_int(E), as_int(K), z.data_ptr(), type, step, choice.data_ptr(),
+                 choice.scalar_type() == at::kLong ? 64 : 32, m, sigmoid ? MUON_SIGMOID : MUON_SOFTMAX, coefficient, scale,
+                 static_cast<float*>(loss.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
+                 g.defined() ? g.data_ptr() : nullptr, accumulate ? 1 : 0, ws.data_ptr(), ws.nbytes(), current_stream(device));
+  return py::make_tuple(static_cast<int>(buffers.called(st)), loss, counts, g.defined() ? py::cast(g) : py::none());
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_native, m) {
@@ -461,4 +782,11 @@ PYBIND11_MODULE(_native, m) {
   m.def("mx4_quantize", &mx4_quantize);
   m.def("mx4_dequantize", &mx4_dequantize);
   m.def("mx4_matmul", &mx4_matmul);
+  m.def("bind_fp8", &bind_fp8);
+  m.def("fp8_quantize", &fp8_quantize);
+  m.def("fp8_dequantize", &fp8_dequantize);
+  m.def("fp8_matmul", &fp8_matmul);
+  m.def("fp8_grouped_matmul", &fp8_grouped_matmul);
+  m.def("fp8_grouped_weight_grad", &fp8_grouped_weight_grad);
+  m.def("expert_balance", &expert_balance);
 }
