@@ -11,6 +11,11 @@
 // every block adds the partial counts of its sequence up to f, takes its rows, and
 // the last block to finish adds the blocks' sums in their order, so results do not
 // depend on timing.  Small calls do all of it in one block and one launch.
+//
+// The blocks' sums are all that passes from block to block within a launch.  They go
+// by agent-scope atomic stores, which write through to memory, and are waited for
+// before the block is counted as done; a release of everything the block wrote would
+// write back the XCD's whole L2 for each of a thousand blocks.
 #include "../../include/muon.h"
 #include "muon_convert.h"
 #include "muon_internal.h"
@@ -23,7 +28,8 @@ typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
 
 constexpr int kMaxExperts = MUON_MAX_EXPERTS;
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;      // of a block, 512 for rows of more than 512 experts (registers)
+constexpr int kSmallThreads = 256;  // where one block does everything
 constexpr int kCountThreads = 1024;
 constexpr int kElems = 8;  // of a row, consecutive, in a lane
 
@@ -54,9 +60,18 @@ __device__ __forceinline__ bool counted(const BalanceArgs& a, int64_t row) { ret
 // Choices and tokens of rows first .. last - 1 into bins (experts + 1 of them).
 __device__ __forceinline__ void count_rows(const BalanceArgs& a, int64_t first, int64_t last, int32_t* bins) {
   const uint32_t end = static_cast<uint32_t>(last * a.top);  // under 2^31
-  for (uint32_t p = static_cast<uint32_t>(first * a.top) + threadIdx.x; p < end; p += blockDim.x) {
-    const int64_t e = a.wide ? static_cast<const int64_t*>(a.index)[p] : static_cast<const int32_t*>(a.index)[p];
-    if (e >= 0 && e < a.experts && counted(a, p / static_cast<uint32_t>(a.top))) atomicAdd(bins + e, 1);
+  constexpr int kAhead = 8;  // loads under way
+  for (uint32_t p0 = static_cast<uint32_t>(first * a.top) + threadIdx.x; p0 < end; p0 += kAhead * blockDim.x) {
+    int64_t e[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t p = p0 + k * blockDim.x;
+      e[k] = p >= end ? -1 : a.wide ? static_cast<const int64_t*>(a.index)[p] : static_cast<const int32_t*>(a.index)[p];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (e[k] >= 0 && e[k] < a.experts && counted(a, (p0 + k * blockDim.x) / static_cast<uint32_t>(a.top)))
+        atomicAdd(bins + e[k], 1);
   }
   if (a.mask == nullptr) {
     if (threadIdx.x == 0) atomicAdd(bins + a.experts, static_cast<int32_t>(last - first));
@@ -78,20 +93,36 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(BalanceArg
   __syncthreads();
   int32_t* out = a.partial + (static_cast<int64_t>(blockIdx.y) * a.count_blocks + blockIdx.x) * (a.experts + 1);
   for (int e = threadIdx.x; e <= a.experts; e += kCountThreads) out[e] = bins[e];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.done = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int e = threadIdx.x; e < a.experts; e += kCountThreads) a.counts[e] = 0;
+    if (threadIdx.x == 0) *a.done = 0;
+  }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // quads, reversal within 8 and 16 lanes
+
+// Over L neighbouring lanes, the same result in each of them.
+template <int L, class F>
+__device__ __forceinline__ float lanes(float x, F op) {
+  if constexpr (L >= 2) x = op(x, dpp<kXor1>(x));
+  if constexpr (L >= 4) x = op(x, dpp<kXor2>(x));
+  if constexpr (L >= 8) x = op(x, dpp<kHalfMirror>(x));
+  if constexpr (L >= 16) x = op(x, dpp<kMirror>(x));
+  if constexpr (L >= 32) x = op(x, __shfl_xor(x, 16));
+  if constexpr (L >= 64) x = op(x, __shfl_xor(x, 32));
+  return x;
+}
 template <int L>
 __device__ __forceinline__ float lanes_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < L; m *= 2) x += __shfl_xor(x, m);
-  return x;
+  return lanes<L>(x, [](float a, float b) { return a + b; });
 }
 template <int L>
 __device__ __forceinline__ float lanes_max(float x) {
-#pragma unroll
-  for (int m = 1; m < L; m *= 2) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
+  return lanes<L>(x, [](float a, float b) { return fmaxf(a, b); });
 }
 
 // Elements c .. c + 7 of a row of n, `none` behind its end.
@@ -143,15 +174,77 @@ __device__ __forceinline__ void store8(void* p, int64_t row, int c, int n, const
   }
 }
 
+// e^x for x <= 0 (NaN for NaN), 0 under the normal range: 2^h (1 + l ln 2) with h + l = x
+// log2(e), l what the rounding of h left, so that the result is good to two steps for
+// every x; half the instructions of the general function.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  x = __builtin_elementwise_maximum(x, -128.0f);  // -infinity has no l
+  const float h = x * kLog2e, l = fmaf(x, kRest, fmaf(x, kLog2e, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return fmaf(e, l * kLn2, e);
+}
+
+// p of a row's logits x, and the gradient's factor slope, in place; returns <f, p>.
+template <int L, int N>
+__device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], const float (&f)[N], bool sigmoid) {
+  float sum = 0.0f, inner = 0.0f;
+  if (sigmoid) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float t = exp_of(-fabsf(x[e])), q = 1.0f / (1.0f + t);  // the sigmoid of |z|
+      x[e] = x[e] < 0.0f ? t * q : q;
+      slope[e] = t * q * q;
+      sum += x[e];
+    }
+    sum = lanes_sum<L>(sum);
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      slope[e] *= inverse;
+      inner += f[e] * (x[e] * inverse);
+    }
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m = fmaxf(m, x[e]);
+    m = lanes_max<L>(m);
+    m = m == -INFINITY ? 0.0f : m;  // nothing to choose from: p = 0
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      x[e] = exp_of(x[e] - m);
+      sum += x[e];
+    }
+    sum = lanes_sum<L>(sum);
+    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      slope[e] = x[e] * inverse;
+      inner += f[e] * slope[e];
+    }
+  }
+  return lanes_sum<L>(inner);
+}
+
 // Rows first, first + step, ... under last: their <f, p> added up (this thread's
 // share of them), their gradients written.  L lanes take a row, lane `o` of them
-// elements 8 (o + L v).
+// elements 8 (o + L v).  The next row's logits are on their way meanwhile.
+template <int D, int L, int NV>
+__device__ __forceinline__ void load_row(const BalanceArgs& a, int64_t r, float (&x)[NV * kElems]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    load8<D>(a.logits, r * a.stride, kElems * (static_cast<int>(threadIdx.x) % L + L * v), a.experts, -INFINITY,
+             x + v * kElems);
+}
+
+// (x: the thread's first row, valid: whether it counts)
 template <int D, int L, int NV>
 __device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* bins, int64_t first, int64_t last, int step,
-                                           float scale) {
+                                           float scale, float (&x)[NV * kElems], bool valid) {
+  constexpr int N = NV * kElems;
   const int o = threadIdx.x % L, E = a.experts, tokens = bins[E];
   const float unit = tokens > 0 ? static_cast<float>(E) / (static_cast<float>(a.top) * static_cast<float>(tokens)) : 0.0f;
-  float f[NV * kElems];
+  float f[N];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -161,59 +254,41 @@ __device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* 
     }
   const float by = tokens > 0 ? scale / static_cast<float>(tokens) : 0.0f;  // of the gradient
   float total = 0.0f;
+  int64_t r = first + threadIdx.x / L;
   // all lanes of a row are in the loop together (they share a row)
-  for (int64_t r = first + threadIdx.x / L; r < last; r += step) {
-    const bool valid = counted(a, r);
-    float x[NV * kElems], slope[NV * kElems];
-    float inner = 0.0f;
+  while (r < last) {
+    const int64_t after = r + step;
+    const bool valid_after = after < last && counted(a, after);
+    float next[N], g[N];
+    if (valid_after) load_row<D, L, NV>(a, after, next);
     if (valid) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) load8<D>(a.logits, r * a.stride, kElems * (o + L * v), E, -INFINITY, x + v * kElems);
-      float sum = 0.0f;
-      if (a.sigmoid) {
-#pragma unroll
-        for (int e = 0; e < NV * kElems; ++e) {
-          const float t = expf(-fabsf(x[e])), q = 1.0f / (1.0f + t);  // the sigmoid of |z|
-          x[e] = x[e] < 0.0f ? t * q : q;
-          slope[e] = t * q * q;
-          sum += x[e];
-        }
-      } else {
-        float m = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < NV * kElems; ++e) m = fmaxf(m, x[e]);
-        m = lanes_max<L>(m);
-        m = m == -INFINITY ? 0.0f : m;  // nothing to choose from: p = 0
-#pragma unroll
-        for (int e = 0; e < NV * kElems; ++e) {
-          x[e] = expf(x[e] - m);
-          sum += x[e];
-        }
-      }
-      sum = lanes_sum<L>(sum);
-      const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int e = 0; e < NV * kElems; ++e) {
-        x[e] *= inverse;
-        slope[e] = a.sigmoid ? slope[e] * inverse : x[e];
-        inner += f[e] * x[e];
-      }
-      inner = lanes_sum<L>(inner);
+      const float inner = row_scores<L>(x, g, f, a.sigmoid != 0);
       if (o == 0) total += inner;
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] *= (f[e] - inner) * by;
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) g[e] = 0.0f;
     }
     if (a.grad != nullptr && (valid || !a.accumulate)) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = kElems * (o + L * v);
-        const int64_t row = r * E;
-        float g[kElems] = {};
-        if (a.accumulate && c < E) load8<D>(a.grad, row, c, E, 0.0f, g);
+        if (c < E) {
+          if (a.accumulate) {
+            float was[kElems];
+            load8<D>(a.grad, r * E, c, E, 0.0f, was);
 #pragma unroll
-        for (int e = 0; e < kElems; ++e)
-          g[e] += valid ? slope[v * kElems + e] * (f[v * kElems + e] - inner) * by : 0.0f;
-        if (c < E) store8<D>(a.grad, row, c, E, g);
+            for (int e = 0; e < kElems; ++e) g[v * kElems + e] += was[e];
+          }
+          store8<D>(a.grad, r * E, c, E, g + v * kElems);
+        }
       }
     }
+    r = after;
+    valid = valid_after;
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = next[e];
   }
   return total;
 }
@@ -224,13 +299,13 @@ __device__ __forceinline__ double block_sum(double x, double* waves) {
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = x;
   __syncthreads();
   double s = 0.0;
-  for (int w = 0; w < kThreads / 64; ++w) s += waves[w];
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 64; ++w) s += waves[w];
   __syncthreads();
   return s;
 }
 
 template <int D, int L, int NV>
-__global__ __launch_bounds__(kThreads) void balance_rows_kernel(BalanceArgs a) {
+__global__ __launch_bounds__(kThreads / NV) void balance_rows_kernel(BalanceArgs a) {
   __shared__ int32_t bins[kMaxExperts + 1];
   __shared__ double waves[kThreads / 64];
   __shared__ int last_block;
@@ -238,16 +313,20 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(BalanceArgs a) {
   const float alpha = a.coefficient, scale = alpha * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
   if (a.count_blocks == 0) {  // one block
     double total = 0.0;
-    for (int e = threadIdx.x; e < E; e += kThreads) a.counts[e] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) a.counts[e] = 0;
     for (int s = 0; s < a.sequences; ++s) {
       __syncthreads();
-      for (int e = threadIdx.x; e <= E; e += kThreads) bins[e] = 0;
+      for (int e = threadIdx.x; e <= E; e += blockDim.x) bins[e] = 0;
       __syncthreads();
       const int64_t base = static_cast<int64_t>(s) * a.tokens;
       count_rows(a, base, base + a.tokens, bins);
       __syncthreads();
-      for (int e = threadIdx.x; e < E; e += kThreads) a.counts[e] += bins[e];
-      const float sum = take_rows<D, L, NV>(a, bins, base, base + a.tokens, kThreads / L, scale);
+      for (int e = threadIdx.x; e < E; e += blockDim.x) a.counts[e] += bins[e];
+      const int64_t r = base + threadIdx.x / L;
+      const bool valid = r < base + a.tokens && counted(a, r);
+      float x[NV * kElems];
+      if (valid) load_row<D, L, NV>(a, r, x);
+      const float sum = take_rows<D, L, NV>(a, bins, base, base + a.tokens, blockDim.x / L, scale, x, valid);
       total += bins[E] > 0 ? static_cast<double>(sum) / bins[E] : 0.0;
     }
     total = block_sum(total, waves);
@@ -255,43 +334,58 @@ __global__ __launch_bounds__(kThreads) void balance_rows_kernel(BalanceArgs a) {
     return;
   }
   const int s = blockIdx.y;
+  const int64_t base = static_cast<int64_t>(s) * a.tokens;
+  const int64_t first = base + static_cast<int64_t>(a.tokens) * blockIdx.x / a.blocks;
+  const int64_t last = base + static_cast<int64_t>(a.tokens) * (blockIdx.x + 1) / a.blocks;
+  const int64_t r = first + threadIdx.x / L;
+  const bool valid = r < last && counted(a, r);
+  float x[NV * kElems];
+  if (valid) load_row<D, L, NV>(a, r, x);  // on its way while the counts are added up
   const int32_t* partial = a.partial + static_cast<int64_t>(s) * a.count_blocks * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) bins[e] = 0;
+  __syncthreads();
+  // as many threads for a bin as there are, eight loads at a time under way
+  const int per = static_cast<int>(blockDim.x) / (E + 1) > 0 ? static_cast<int>(blockDim.x) / (E + 1) : 1;
+  for (int p = threadIdx.x; p < per * (E + 1); p += blockDim.x) {
+    const int e = p % (E + 1);
     int n = 0;
-    for (int b = 0; b < a.count_blocks; ++b) n += partial[b * (E + 1) + e];
-    bins[e] = n;
+    for (int b0 = p / (E + 1); b0 < a.count_blocks; b0 += 8 * per) {
+      int part[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) part[b] = partial[(b0 + b * per < a.count_blocks ? b0 + b * per : b0) * (E + 1) + e];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) n += b0 + b * per < a.count_blocks ? part[b] : 0;
+    }
+    if (n != 0) atomicAdd(bins + e, n);
   }
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(s) * a.tokens;
-  const int64_t first = static_cast<int64_t>(a.tokens) * blockIdx.x / a.blocks;
-  const int64_t last = static_cast<int64_t>(a.tokens) * (blockIdx.x + 1) / a.blocks;
-  const float sum = take_rows<D, L, NV>(a, bins, base + first, base + last, kThreads / L, scale);
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+      if (bins[e] != 0) atomicAdd(a.counts + e, bins[e]);  // whole numbers: in any order
+  const float sum = take_rows<D, L, NV>(a, bins, first, last, blockDim.x / L, scale, x, valid);
   const double mine = block_sum(bins[E] > 0 ? static_cast<double>(sum) / bins[E] : 0.0, waves);
   const int blocks = a.blocks * a.sequences;
   if (threadIdx.x == 0) {
     __hip_atomic_store(a.sums + static_cast<int64_t>(s) * a.blocks + blockIdx.x, mine, __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
-    last_block = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == blocks - 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the sum is in memory
+    last_block = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == blocks - 1;
+    asm volatile("" ::: "memory");
   }
   __syncthreads();
   if (!last_block) return;
   double total = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += kThreads)
+  for (int b = threadIdx.x; b < blocks; b += blockDim.x)
     total += __hip_atomic_load(a.sums + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   total = block_sum(total, waves);
   if (threadIdx.x == 0) *a.loss = static_cast<float>(total * alpha);
-  const int parts = a.sequences * a.count_blocks;
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    int n = 0;
-    for (int b = 0; b < parts; ++b) n += a.partial[static_cast<int64_t>(b) * (E + 1) + e];
-    a.counts[e] = n;
-  }
 }
 
 template <int D, int L, int NV>
 void launch_rows(const BalanceArgs& a, hipStream_t s) {
-  const dim3 grid(a.blocks, a.count_blocks == 0 ? 1 : a.sequences);
-  hipLaunchKernelGGL((balance_rows_kernel<D, L, NV>), grid, dim3(kThreads), 0, s, a);
+  const bool small = a.count_blocks == 0;
+  const dim3 grid(a.blocks, small ? 1 : a.sequences), block(small ? kSmallThreads : kThreads / NV);
+  hipLaunchKernelGGL((balance_rows_kernel<D, L, NV>), grid, block, 0, s, a);
 }
 
 // Lanes of a row: the fewest that hold it, 8 elements each.
@@ -327,13 +421,17 @@ struct Plan {
 
 Plan plan_of(int sequences, int tokens, int experts, int top) {
   const int64_t rows = static_cast<int64_t>(sequences) * tokens;
-  const int per = kThreads / lanes_of(experts);  // rows of a block at a time
-  if (rows * top <= 4 * kThreads && rows <= 4 * per && sequences <= 4) return Plan{0, 1};
+  const int lanes = lanes_of(experts);
+  if (rows * top <= 4 * kSmallThreads && rows <= 4 * kSmallThreads / lanes && sequences <= 4) return Plan{0, 1};
+  const int per = (experts > 64 * kElems ? kThreads / 2 : kThreads) / lanes;  // rows of a block at a time
   const int64_t entries = static_cast<int64_t>(tokens) * top;
-  int64_t count_blocks = (entries + 16383) / 16384;
-  count_blocks = count_blocks > 32 ? 32 : count_blocks;
+  int64_t count_blocks = (entries + 2047) / 2048;  // two rounds of loads of a thread
+  const int64_t limit = sequences < 8 ? 48 : 8;
+  count_blocks = count_blocks > limit ? limit : count_blocks;
   int64_t blocks = (tokens + per - 1) / per;
-  const int64_t most = sequences < 1024 ? 1024 / sequences : 1;
+  // one block a compute unit: all of them count themselves as done at one address,
+  // 1024 blocks of a quarter of the threads took 25 us where these take 10
+  const int64_t most = sequences < 256 ? 256 / sequences : 1;
   blocks = blocks > most ? most : blocks;
   return Plan{static_cast<int>(count_blocks), static_cast<int>(blocks)};
 }

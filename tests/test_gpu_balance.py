@@ -119,6 +119,10 @@ def test_extreme_logits():
     for scale in (50.0, 1e4):
         z, index = case(1, 200, 32, 4, "f32", 5, scale)
         check(mu.expert_balance(z.to(DEV), index.to(DEV), 1.0, grad=True), z, index, 1.0, "softmax", "f32")
+    z, index = case(1, 100, 32, 4, "f32", 5)
+    z[..., :16] = -3.4e38  # the lowest numbers in place of -infinity
+    z[0, 7] = 3.4e38
+    check(mu.expert_balance(z.to(DEV), index.to(DEV), 1.0, grad=True), z, index, 1.0, "softmax", "f32")
     for shift in (-60.0, 60.0):
         z, index = case(1, 200, 32, 4, "f32", 6)
         z = z + shift
