@@ -160,29 +160,28 @@ struct RowTile {
   int before;      // tiles of the groups before it
 };
 
-// Tiles of TM rows of groups first .. last - 1 in order (group `groups` being the
-// rest).  all: how many there are; of(t): tile t of width 1, or, with `width` tiles
-// side by side, the one that the t-th of them all belongs to.
-template <int TM>
+// Tiles of TM rows of groups 0 .. groups - 1 in order, count(g) rows each from row
+// `row0` on.  all: how many there are; of(t): tile t of width 1, or, with `width`
+// tiles side by side, the one that the t-th of them all belongs to.
+template <int TM, class Count>
 struct RowTiles {
-  const int32_t* counts;
-  int groups, rows, first, last;
+  const Count& count;
+  int rows, groups, row0;
 
   __device__ __forceinline__ int all(int lane) const {
-    int row = 0, n = 0;
-    for (int g0 = 0; g0 < last; g0 += 64) {
-      int upto, tiles;
-      chunk(g0, lane, row, &upto, &tiles, nullptr, nullptr);
-      const int sum = wave_scan(tiles);
-      n += __builtin_amdgcn_readlane(sum, 63);
+    int row = row0, n = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+      int upto, tiles, begin, end;
+      chunk(g0, lane, row, &upto, &tiles, &begin, &end);
+      n += __builtin_amdgcn_readlane(wave_scan(tiles), 63);
       row = __builtin_amdgcn_readlane(upto, 63);
     }
     return n;
   }
 
   __device__ __forceinline__ RowTile of(int t, int width, int lane) const {
-    int row = 0, n = 0;
-    for (int g0 = 0; g0 < last; g0 += 64) {
+    int row = row0, n = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
       int upto, tiles, begin, end;
       chunk(g0, lane, row, &upto, &tiles, &begin, &end);
       const int sum = n + wave_scan(tiles);  // tiles up to this lane's group
@@ -207,38 +206,12 @@ struct RowTiles {
  private:
   // Of groups g0 .. g0 + 63, one a lane: rows up to the group's end, its tiles and place.
   __device__ __forceinline__ void chunk(int g0, int lane, int row, int* upto, int* tiles, int* begin, int* end) const {
-    const int g = g0 + lane;
-    const int c = g < last ? group_count(counts, g, groups, rows) : 0;
+    const int g = g0 + lane, c = g < groups ? count(g) : 0;
     *upto = row + wave_scan(c);
-    const int b = *upto - c < rows ? *upto - c : rows, e = *upto < rows ? *upto : rows;
-    *tiles = g >= first && g < last ? (e - b + TM - 1) / TM : 0;
-    if (begin != nullptr) {
-      *begin = b;
-      *end = e;
-    }
+    *begin = *upto - c < rows ? *upto - c : rows;
+    *end = *upto < rows ? *upto : rows;
+    *tiles = (*end - *begin + TM - 1) / TM;
   }
 };
-
-// The units of group g in a code with whole units for each group.
-__device__ __forceinline__ void group_units(const int32_t* counts, int groups, int rows, int g, int units, int lane,
-                                            int* begin, int* end) {
-  int row = 0, n = 0;
-  for (int g0 = 0;; g0 += 64) {
-    const int me = g0 + lane;
-    const int c = me < groups ? group_count(counts, me, groups, rows) : 0;
-    const int upto = row + wave_scan(c);
-    const int b = upto - c < rows ? upto - c : rows, e = upto < rows ? upto : rows;
-    const int mine = (e - b + kF8Unit - 1) / kF8Unit;
-    const int sum = n + wave_scan(mine);
-    if (g < g0 + 64) {
-      *end = __builtin_amdgcn_readlane(sum, g - g0);
-      *begin = *end - __builtin_amdgcn_readlane(mine, g - g0);
-      *end = *end < units ? *end : units;
-      return;
-    }
-    n = __builtin_amdgcn_readlane(sum, 63);
-    row = __builtin_amdgcn_readlane(upto, 63);
-  }
-}
 
 }  // namespace muon

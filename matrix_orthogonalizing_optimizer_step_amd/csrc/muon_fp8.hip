@@ -225,7 +225,8 @@ __global__ __launch_bounds__(kThreads) void fp8_tile_kernel(Fp8QuantArgs a) {
   bool cols = a.codes_t[b] != nullptr;
   int i0 = blockIdx.y * 128, end = a.rows, unit = blockIdx.y;  // first row, end of its group, unit of the columns' code
   if (a.counts != nullptr) {
-    const RowTiles<128> tiles{a.counts, a.groups, a.rows, 0, a.groups + (rows ? 1 : 0)};
+    const auto count = [&](int g) { return group_count(a.counts, g, a.groups, a.rows); };
+    const RowTiles<128, decltype(count)> tiles{count, a.rows, a.groups + (rows ? 1 : 0), 0};
     const RowTile t = tiles.of(blockIdx.y, 1, tid & 63);
     if (t.group < 0) return;
     i0 = t.begin + t.tile * 128;

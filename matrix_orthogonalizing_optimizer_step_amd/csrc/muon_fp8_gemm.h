@@ -23,7 +23,17 @@
 //
 // A slab's fragments are read into registers while the MFMAs of the slab before
 // run, so that behind the one barrier of a slab its stage can be filled anew.
+//
+// Blocks that fill a compute unit can stay for tile after tile: what they load runs 4
+// slabs ahead of what they multiply, over the end of a tile into the next one, whose
+// first slabs are there when a tile's results have gone.  A tile takes whole rounds of
+// the ring: behind an odd number of units two slabs are loaded for nothing.  That pays
+// where k is short against the results: the weight gradients of 16 experts of 2048 x
+// 7168 with 8190 rows in all take 350 us so and 387 with a block a tile.  Long products
+// are limited by power and gain nothing (8192x8192x8192 bf16 389 and 391 us).
 #pragma once
+
+#include <type_traits>
 
 #include "muon_fp8.h"
 #include "muon_tile.h"
@@ -34,11 +44,13 @@ namespace fp8 {
 constexpr int kStages = 4;
 constexpr bool kFast = false, kExact = true;
 
-template <int TM_, int TN_, int WM_>
+template <int TM_, int TN_, int WM_, bool STAYS = false>
 struct Tile {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = 4 / WM_;
   static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
   static constexpr int kCodeLoads = TM / 64 + TN / 64;  // per wave and slab
+  static constexpr bool kStays = STAYS;                 // its block takes tile after tile
+  static constexpr int kStores(bool fp32) { return FM * FN * 32 * 32 * (fp32 ? 4 : 2) / 1024; }  // of a wave and tile
   struct Stage {
     uint4 code[(TM + TN) * 4];  // A rows, then B rows, 4 slots each
   };
@@ -50,58 +62,103 @@ struct ScaleStage {
   uint8_t a[1024], b[1024];
 };
 
-// One operand's source (block-uniform but for vcode).
-struct Source {
+__device__ __forceinline__ uint32_t clip(uint64_t bytes) {
+  return (bytes >> 31) != 0 ? 0x7fffffffu : static_cast<uint32_t>(bytes);
+}
+
+// One operand of a tile (block-uniform): codes and scales of its matrix, its first
+// row, and the matrix's rows and units.
+struct Operand {
   const void* code;
-  int vcode;       // byte offset of this lane's first load from a piece's first row
-  uint32_t rows;
-};
-// What this wave loads of the scales, A's or B's.
-struct ScaleSource {
   const void* scale;
-  int voff;        // byte offset of this lane's load from a unit's first row, or behind everything
-  uint32_t pitch;
+  int row;
+  uint32_t rows;
+  int units;
 };
 
-__device__ __forceinline__ uint32_t clip(uint64_t bytes) { return bytes < 0x7fffffffu ? static_cast<uint32_t>(bytes) : 0x7fffffffu; }
+// What is loaded next (block-uniform): addresses of the tile's first row in the next
+// slab, for the scales of the operand that this wave brings them of, and the bytes
+// from there to the end of the matrix, which every load is checked against: rows
+// behind the last row read the next piece's, or zeros behind the last piece.
+// Neither enters a stored element.
+struct Stream {
+  uint64_t a, b, s;
+  uint64_t a_left, b_left, s_left;
+  uint32_t a_step, b_step, s_step;
+  int slabs;  // of the tile, still to load
 
-// The loads that bring this wave's share of slab s into a stage: the codes of A and
-// of B, 16 rows each.  Behind the last slab the last one is read again.  The
-// resource starts at the piece and ends with the matrix, so every load is checked
-// against the matrix's end: rows behind the last row read the next piece's, or
-// zeros behind the last piece.  Neither enters a stored element.
+  // Units ub .. ue - 1 (at least one) of a tile.
+  __device__ __forceinline__ void start(const Operand& A, const Operand& B, int ub, int ue, int wave) {
+    a_step = A.rows * kF8Piece;
+    b_step = B.rows * kF8Piece;
+    const uint64_t at_a = 2 * static_cast<uint64_t>(ub) * a_step + static_cast<uint64_t>(A.row) * kF8Piece;
+    const uint64_t at_b = 2 * static_cast<uint64_t>(ub) * b_step + static_cast<uint64_t>(B.row) * kF8Piece;
+    a = reinterpret_cast<uint64_t>(A.code) + at_a;
+    b = reinterpret_cast<uint64_t>(B.code) + at_b;
+    a_left = 2 * static_cast<uint64_t>(A.units) * a_step - at_a;
+    b_left = 2 * static_cast<uint64_t>(B.units) * b_step - at_b;
+    const bool of_b = (wave & 1) != 0;
+    s_step = ((of_b ? B.rows : A.rows) + kF8Line - 1) & ~(kF8Line - 1u);
+    const uint64_t at_s = static_cast<uint64_t>(ub) * s_step + ((of_b ? B.row : A.row) & ~(kF8Line - 1));
+    s = (of_b ? reinterpret_cast<uint64_t>(B.scale) : reinterpret_cast<uint64_t>(A.scale)) + at_s;
+    s_left = static_cast<uint64_t>(A.units) * s_step - at_s;
+    slabs = 2 * (ue - ub);
+  }
+  // To the next slab; behind the tile's last one it stays there.
+  template <bool ODD>
+  __device__ __forceinline__ void advance() {
+    --slabs;
+    const bool on = slabs > 0;
+    const uint32_t da = on ? a_step : 0u, db = on ? b_step : 0u;
+    a += da;
+    a_left -= da;
+    b += db;
+    b_left -= db;
+    if constexpr (ODD) {
+      const uint32_t ds = on ? s_step : 0u;
+      s += ds;
+      s_left -= ds;
+    }
+  }
+};
+
+// This lane's byte offsets in a wave's loads.
+struct Offsets {
+  int a, b, s;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(uint64_t at, uint64_t left) {
+  return make_rsrc(reinterpret_cast<const void*>(at), 0, clip(left));
+}
+
+// The loads that bring this wave's share of a slab into a stage: the codes of A and
+// of B, 16 rows each.
 template <class T>
-__device__ __forceinline__ void load_slab(typename T::Stage& st, const Source& A, const Source& B, int s, int slabs,
-                                          int wave) {
+__device__ __forceinline__ void load_slab(typename T::Stage& st, const Stream& S, const Offsets& off, int wave) {
   constexpr int RA = T::TM / 4, RB = T::TN / 4;  // rows of this wave
-  const uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(s < slabs ? s : slabs - 1));
-  const uint64_t la = static_cast<uint64_t>(p) * A.rows, lb = static_cast<uint64_t>(p) * B.rows;
-  const __amdgpu_buffer_rsrc_t ca = make_rsrc(A.code, la * 64, clip((static_cast<uint64_t>(slabs) * A.rows - la) * 64));
-  const __amdgpu_buffer_rsrc_t cb = make_rsrc(B.code, lb * 64, clip((static_cast<uint64_t>(slabs) * B.rows - lb) * 64));
+  const __amdgpu_buffer_rsrc_t ca = resource(S.a, S.a_left), cb = resource(S.b, S.b_left);
   lds_ptr_t da = (lds_ptr_t)(st.code + wave * RA * 4), db = (lds_ptr_t)(st.code + (T::TM + wave * RB) * 4);
 #define FP8_LOAD(R, RSRC, DST, VOFF, PIECE)     \
   if constexpr ((PIECE) * 1024 < (R) * 64)      \
     __builtin_amdgcn_raw_ptr_buffer_load_lds(RSRC, DST, 16, VOFF, 0, (PIECE) * 1024, 0)
-  FP8_LOAD(RA, ca, da, A.vcode, 0);
-  FP8_LOAD(RA, ca, da, A.vcode, 1);
-  FP8_LOAD(RA, ca, da, A.vcode, 2);
-  FP8_LOAD(RA, ca, da, A.vcode, 3);
-  FP8_LOAD(RB, cb, db, B.vcode, 0);
-  FP8_LOAD(RB, cb, db, B.vcode, 1);
-  FP8_LOAD(RB, cb, db, B.vcode, 2);
-  FP8_LOAD(RB, cb, db, B.vcode, 3);
+  FP8_LOAD(RA, ca, da, off.a, 0);
+  FP8_LOAD(RA, ca, da, off.a, 1);
+  FP8_LOAD(RA, ca, da, off.a, 2);
+  FP8_LOAD(RA, ca, da, off.a, 3);
+  FP8_LOAD(RB, cb, db, off.b, 0);
+  FP8_LOAD(RB, cb, db, off.b, 1);
+  FP8_LOAD(RB, cb, db, off.b, 2);
+  FP8_LOAD(RB, cb, db, off.b, 3);
 #undef FP8_LOAD
   static_assert(RA % 16 == 0 && RB % 16 == 0 && RA <= 64 && RB <= 64, "loads of a slab");
 }
 
-// One load: even waves bring A's scales of the unit that slab s begins, odd ones B's,
+// One load: even waves bring A's scales of the unit that the slab begins, odd ones B's,
 // two of them the same bytes, so that every wave has the same loads under way.
 // Lanes behind the tile's rows have an offset behind the matrix and write zeros.
-__device__ __forceinline__ void load_scales(ScaleStage& st, const ScaleSource& S, int s, int slabs, int wave) {
-  const uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(s < slabs ? s : slabs - 1));
-  const uint64_t at = static_cast<uint64_t>(p >> 1) * S.pitch;
-  const __amdgpu_buffer_rsrc_t r = make_rsrc(S.scale, at, clip(static_cast<uint64_t>(slabs >> 1) * S.pitch - at));
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)((wave & 1) != 0 ? st.b : st.a), 16, S.voff, 0, 0, 0);
+__device__ __forceinline__ void load_scales(ScaleStage& st, const Stream& S, const Offsets& off, int wave) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(S.s, S.s_left), (lds_ptr_t)((wave & 1) != 0 ? st.b : st.a), 16, off.s, 0,
+                                           0, 0);
 }
 
 struct Frag {
@@ -198,32 +255,34 @@ struct Reads {
 };
 
 // One slab from stage `cur`, whose fragments are in f and scales in w; leaves those
-// of the next slab (stage `nxt`) there.  The loads of the slab 4 ahead go into `cur`
-// and, in even slabs, those of the scales of the unit two ahead into `sc`; odd slabs
-// read the next unit's scales from `sc`.  Loads and reads are spread over the MFMAs
-// (a burst of them would hold up the wave, which issues in order).
-template <class T, int FA, bool EXACT, bool ODD>
+// of the next slab (stage `nxt`) there.  The slab 4 ahead is loaded into `cur` and,
+// in even slabs, its unit's scales into `sc`; odd slabs read the next unit's scales
+// from `sc`.  Loads and reads are spread over the MFMAs (a burst of them would hold
+// up the wave, which issues in order).  kStores: stores that were issued behind the
+// loads that are waited for.
+template <class T, int FA, bool EXACT, bool ODD, int kStores>
 __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f, Scales<T>& w, Wide<T>& v,
-                                     typename T::Stage& cur, const typename T::Stage& nxt, ScaleStage& sc, const Source& A,
-                                     const Source& B, const ScaleSource& S, int s, int slabs, int wave, int lane,
-                                     const Reads& at) {
+                                     typename T::Stage& cur, const typename T::Stage& nxt, ScaleStage& sc, Stream& S,
+                                     const Offsets& off, int wave, int lane, const Reads& at) {
   constexpr int M = T::FM * T::FN, kLoads = T::kCodeLoads + (ODD ? 0 : 1);
   constexpr int kReads = (ODD ? 3 : 2) * (T::FM + T::FN);
+  constexpr int kAhead = 2 * T::kCodeLoads + 1;  // loads of two slabs
   // this wave's part of the next slab has landed (two slabs stay under way), and all
   // its reads of this one are done
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kAhead + kStores < 63 ? kAhead + kStores : 63, 0));
   asm volatile("s_barrier" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
   Frags<T> fn;
   Scales<T> wn;
-  load_slab<T>(cur, A, B, s + kStages, slabs, wave);
-  if constexpr (!ODD) load_scales(sc, S, s + kStages, slabs, wave);
+  load_slab<T>(cur, S, off, wave);
+  if constexpr (!ODD) load_scales(sc, S, off, wave);
   read_frag<T::FN>(fn.b, nxt, at.b, lane);
   read_frag<T::FM>(fn.a, nxt, at.a, lane);
   if constexpr (ODD) {
     read_scales<T::FN>(wn.b, sc.b, at.sb, lane);
     read_scales<T::FM>(wn.a, sc.a, at.sa, lane);
   }
+  S.template advance<ODD>();
   if constexpr (!EXACT) {
     mfmas<T, FA>(acc, f, w);
 #pragma unroll
@@ -263,89 +322,171 @@ __device__ __forceinline__ void slab(f32x16_t (&acc)[T::FN][T::FM], Frags<T>& f,
   if constexpr (ODD) w = wn;
 }
 
+// The LDS of a block.  (The stages are objects of their own so that the compiler can
+// tell a read of one from a load into another.)
 template <class T>
 struct Lds {
   typename T::Stage &s0, &s1, &s2, &s3;
   ScaleStage &c0, &c1;
+  uint4* out;  // where a block stays: 32 rows of 128 bytes for each wave's results
+};
+constexpr int kOutPitch = 9;  // uint4 of such a row, one against bank conflicts
+#define FP8_LDS(T)                                                              \
+  __shared__ typename T::Stage s0, s1, s2, s3;                                  \
+  __shared__ ScaleStage c0, c1;                                                 \
+  __shared__ uint4 out_stage[T::kStays ? 4 * 32 * kOutPitch : 1];               \
+  const Lds<T> lds{s0, s1, s2, s3, c0, c1, out_stage}
+
+// A tile of a launch: rows of A and of B, and units ub .. ue - 1 (one at least).
+struct Work {
+  Operand A, B;
+  int ub, ue;
+  void* C;
+  int rows, cols;    // the ends of its rows and columns in C, whose rows are `cols` long
+  int add;           // C is added to
+  int sums;          // C holds fp32 sums of a piece of k
 };
 
-// Units ub .. ue - 1 of the tile at rows i0 of A and j0 of B into the accumulators.
-// All of the block's LDS is free behind it.  (The stages are objects of their own so
-// that the compiler can tell a read of one from a load into another.)
-template <class T, int FA, bool EXACT>
-__device__ __forceinline__ void tile_product(f32x16_t (&acc)[T::FN][T::FM], const Lds<T>& lds, Source A, Source B,
-                                             const void* a_scale, const void* b_scale, int i0, int j0, int ub, int ue,
-                                             int units, int wave, int lane) {
-  // lane l fills slot l % 4 of row l / 4 of each 16-row run
-  const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
-  A.vcode = (i0 + wave * (T::TM / 4)) * 64 + vcode;
-  B.vcode = (j0 + wave * (T::TN / 4)) * 64 + vcode;
-  const bool odd = (wave & 1) != 0;
-  const int lines = (odd ? T::TN : T::TM) / kF8Line + 1;
-  const uint32_t rows = odd ? B.rows : A.rows;
-  const ScaleSource S{odd ? b_scale : a_scale, lane < lines ? ((odd ? j0 : i0) & ~(kF8Line - 1)) + lane * 16 : 0x7ffffff0,
-                      (rows + kF8Line - 1) & ~(kF8Line - 1u)};
-  const int ra = T::FM * 32 * (wave / T::WN), rb = T::FN * 32 * (wave % T::WN);
-  const Reads at{ra, T::TM + rb, (i0 & (kF8Line - 1)) + ra, (j0 & (kF8Line - 1)) + rb};
-  const int slabs = 2 * units, se = 2 * ue;
-  int s = 2 * ub;
-  load_slab<T>(lds.s0, A, B, s, slabs, wave);
-  load_scales(lds.c0, S, s, slabs, wave);
-  load_slab<T>(lds.s1, A, B, s + 1, slabs, wave);
-  load_slab<T>(lds.s2, A, B, s + 2, slabs, wave);
-  load_scales(lds.c1, S, s + 2, slabs, wave);
-  load_slab<T>(lds.s3, A, B, s + 3, slabs, wave);
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::kCodeLoads + 1, 0));  // the first slab has landed
-  asm volatile("s_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  Frags<T> f;
-  Scales<T> w;
-  read_frag<T::FN>(f.b, lds.s0, at.b, lane);
-  read_frag<T::FM>(f.a, lds.s0, at.a, lane);
-  read_scales<T::FN>(w.b, lds.c0.b, at.sb, lane);
-  read_scales<T::FM>(w.a, lds.c0.a, at.sa, lane);
-  Wide<T> v;
-  if constexpr (EXACT) widen<T, FA, 0>(v, f, w);
-  for (; s + kStages <= se; s += kStages) {
-    slab<T, FA, EXACT, false>(acc, f, w, v, lds.s0, lds.s1, lds.c0, A, B, S, s, slabs, wave, lane, at);
-    slab<T, FA, EXACT, true>(acc, f, w, v, lds.s1, lds.s2, lds.c1, A, B, S, s + 1, slabs, wave, lane, at);
-    slab<T, FA, EXACT, false>(acc, f, w, v, lds.s2, lds.s3, lds.c1, A, B, S, s + 2, slabs, wave, lane, at);
-    slab<T, FA, EXACT, true>(acc, f, w, v, lds.s3, lds.s0, lds.c0, A, B, S, s + 3, slabs, wave, lane, at);
-  }
-  if (s < se) {
-    slab<T, FA, EXACT, false>(acc, f, w, v, lds.s0, lds.s1, lds.c0, A, B, S, s, slabs, wave, lane, at);
-    slab<T, FA, EXACT, true>(acc, f, w, v, lds.s1, lds.s2, lds.c1, A, B, S, s + 1, slabs, wave, lane, at);
-  }
-  // loads behind the last unit are still on their way into LDS: they end here, and
-  // so do all waves' reads
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-  asm volatile("s_barrier" ::: "memory");
+// A wave's accumulators to C; fp32 C for exact sums.
+template <class T, bool EXACT, bool ADD>
+__device__ __forceinline__ void store_product(const Work& t, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
+                                              int lane) {
+  constexpr int DC = EXACT ? kF32 : kBF16;
+  constexpr int XS = !T::kStays ? T::FN : (EXACT || ADD ? 1 : 2);  // rows of 128 bytes, where a block stays
+  store_tile<T, DC, ADD, XS>(t.C, acc, stage, i, j, t.rows, t.cols, lane);
 }
 
-// A wave's accumulators to C (rows under m, columns under n); fp32 C for exact sums.
-template <class T, bool EXACT>
-__device__ __forceinline__ void store_product(void* C, const f32x16_t (&acc)[T::FN][T::FM], typename T::Stage& stage, int i,
-                                              int j, int m, int n, int lane, int accumulate) {
-  constexpr int DC = EXACT ? kF32 : kBF16;
-  if (accumulate) {
-    store_tile<T, DC, true>(C, acc, stage.code, i, j, m, n, lane);
-  } else {
-    store_tile<T, DC, false>(C, acc, stage.code, i, j, m, n, lane);
+// All the block's tiles: find(&id, &work) is the first tile of the launch from the id-th
+// on, in steps of gridDim.x, if there is one.
+template <class T, int FA, bool EXACT, class Find>
+__device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, int wave, int lane) {
+  // lane l fills slot l % 4 of row l / 4 of each 16-row run
+  const int vcode = (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  const int lines = ((wave & 1) != 0 ? T::TN : T::TM) / kF8Line + 1;
+  const Offsets off{wave * (T::TM / 4) * 64 + vcode, wave * (T::TN / 4) * 64 + vcode, lane < lines ? lane * 16 : 0x7ffffff0};
+  const int ra = T::FM * 32 * (wave / T::WN), rb = T::FN * 32 * (wave % T::WN);
+
+  int id = blockIdx.x;
+  Work t;
+  if (!find(&id, &t)) return;
+  Stream S;  // always a round of the ring ahead of the products
+  S.start(t.A, t.B, t.ub, t.ue, wave);
+  load_slab<T>(lds.s0, S, off, wave);
+  load_scales(lds.c0, S, off, wave);
+  S.template advance<false>();
+  load_slab<T>(lds.s1, S, off, wave);
+  S.template advance<true>();
+  load_slab<T>(lds.s2, S, off, wave);
+  load_scales(lds.c1, S, off, wave);
+  S.template advance<false>();
+  load_slab<T>(lds.s3, S, off, wave);
+  S.template advance<true>();
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::kCodeLoads + 1, 0));  // the first slab has landed
+  asm volatile("s_barrier" ::: "memory");
+  bool full = false;  // the last tile had all its stores
+  for (;;) {
+    const int i = t.A.row + ra, j = t.B.row + rb;  // this wave's first row and column
+    f32x16_t acc[T::FN][T::FM] = {};
+    // the first slab is in s0: the last barrier stood behind its loads
+    const Reads at{ra, T::TM + rb, (t.A.row & (kF8Line - 1)) + ra, (t.B.row & (kF8Line - 1)) + rb};
+    Frags<T> f;
+    Scales<T> w;
+    Wide<T> v;
+    __builtin_amdgcn_sched_barrier(0);
+    read_frag<T::FN>(f.b, lds.s0, at.b, lane);
+    read_frag<T::FM>(f.a, lds.s0, at.a, lane);
+    read_scales<T::FN>(w.b, lds.c0.b, at.sb, lane);
+    read_scales<T::FM>(w.a, lds.c0.a, at.sa, lane);
+    if constexpr (EXACT) widen<T, FA, 0>(v, f, w);
+    // what the last round loads: the next tile's first one, or anything
+    Work n = t;
+    bool more = false;
+    if constexpr (T::kStays) {
+      id += gridDim.x;
+      more = find(&id, &n);
+    }
+    Stream N;
+    N.start(n.A, n.B, n.ub, n.ue, wave);
+    int units = t.ue - t.ub;
+    const auto round = [&](auto stores) {
+      constexpr int kStores = decltype(stores)::value;
+      if (units == 2) S = N;
+      slab<T, FA, EXACT, false, kStores>(acc, f, w, v, lds.s0, lds.s1, lds.c0, S, off, wave, lane, at);
+      slab<T, FA, EXACT, true, kStores>(acc, f, w, v, lds.s1, lds.s2, lds.c1, S, off, wave, lane, at);
+      slab<T, FA, EXACT, false, kStores>(acc, f, w, v, lds.s2, lds.s3, lds.c1, S, off, wave, lane, at);
+      slab<T, FA, EXACT, true, 0>(acc, f, w, v, lds.s3, lds.s0, lds.c0, S, off, wave, lane, at);
+      units -= 2;
+    };
+    // the loads that the first round waits for were issued before the stores of the
+    // tile before; if it had all of them, they need not have ended
+    if constexpr (T::kStays)
+      if (full && units >= 2) round(std::integral_constant<int, T::kStores(EXACT)>());
+    while (units >= 2) round(std::integral_constant<int, 0>());
+    if (units > 0) {
+      S = N;
+      slab<T, FA, EXACT, false, 0>(acc, f, w, v, lds.s0, lds.s1, lds.c0, S, off, wave, lane, at);
+      slab<T, FA, EXACT, true, 0>(acc, f, w, v, lds.s1, lds.s2, lds.c1, S, off, wave, lane, at);
+      if constexpr (T::kStays) {
+        // the two slabs that were loaded for nothing give way to others
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
+        asm volatile("s_barrier" ::: "memory");
+        load_slab<T>(lds.s2, S, off, wave);
+        load_scales(lds.c1, S, off, wave);
+        S.template advance<false>();
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
+        asm volatile("s_barrier" ::: "memory");
+        load_slab<T>(lds.s3, S, off, wave);
+        S.template advance<true>();
+      }
+    }
+    uint4* stage = lds.out + wave * 32 * kOutPitch;
+    if constexpr (!T::kStays) {
+      // loads behind the last unit are still on their way into LDS: they end here,
+      // and so do all waves' reads, before LDS takes the results
+      __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+      asm volatile("s_barrier" ::: "memory");
+      stage = (wave == 0 ? lds.s0 : wave == 1 ? lds.s1 : wave == 2 ? lds.s2 : lds.s3).code;
+      if (t.sums) {
+        store_tile<T, kF32, false>(t.C, acc, stage, i, j, t.rows, t.cols, lane);
+        return;
+      }
+    }
+    if (t.add) {
+      store_product<T, EXACT, true>(t, acc, stage, i, j, lane);
+    } else {
+      store_product<T, EXACT, false>(t, acc, stage, i, j, lane);
+    }
+    if (!more) break;
+    full = i + 32 * T::FM <= t.rows && j + 32 * T::FN <= t.cols;
+    t = n;
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));  // loads into this block's LDS end with it
+}
+
+// `bytes` bytes from p on (both even) to zero, shared by the launch's blocks.
+__device__ __forceinline__ void clear_bytes(void* p, int64_t bytes) {
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(p), end = begin + bytes;
+  uintptr_t head = (begin + 15) & ~uintptr_t{15}, tail = end & ~uintptr_t{15};
+  if (head > tail) head = tail = end;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, all = static_cast<int64_t>(gridDim.x) * 256;
+  for (uintptr_t q = head + me * 16; q < tail; q += all * 16) *reinterpret_cast<uint4*>(q) = make_uint4(0, 0, 0, 0);
+  if (me < 16) {  // at most 7 elements of two bytes at either end (15 without a middle)
+    if (begin + me * 2 < head) *reinterpret_cast<uint16_t*>(begin + me * 2) = 0;
+    if (tail + me * 2 < end) *reinterpret_cast<uint16_t*>(tail + me * 2) = 0;
   }
 }
 
 typedef Tile<256, 256, 2> Big;
+typedef Tile<256, 256, 2, true> Staying;
 typedef Tile<128, 128, 2> Mid;
 typedef Tile<64, 128, 1> Low;
 
-// The block's LDS, `lds`.
-#define FP8_LDS(T)                                  \
-  __shared__ typename T::Stage s0, s1, s2, s3;      \
-  __shared__ ScaleStage c0, c1;                     \
-  const Lds<T> lds{s0, s1, s2, s3, c0, c1}
-
 template <class T>
 constexpr int kBlocksPerCU = T::TM == 256 ? 1 : 2;
+template <class T>
+uint32_t blocks_of(int64_t tiles) {
+  return static_cast<uint32_t>(T::kStays && tiles > kCUs ? kCUs : tiles);
+}
 
 }  // namespace fp8
 }  // namespace muon

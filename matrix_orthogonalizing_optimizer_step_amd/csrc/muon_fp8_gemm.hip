@@ -7,26 +7,28 @@ namespace fp8 {
 namespace {
 
 template <class T, int FA, bool EXACT>
-__global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_tile_gemm_kernel(Fp8GemmArgs a, int tm, int tn) {
+__global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_tile_gemm_kernel(Fp8GemmArgs a, int tm, int tn, int tiles) {
   FP8_LDS(T);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  int outer, ti, tj;
-  tile_of(blockIdx.x, gridDim.x, tm, tn, &outer, &ti, &tj);
-  const int b = outer / a.pieces, piece = outer - b * a.pieces;
-  const int i0 = ti * T::TM, j0 = tj * T::TN;
-  const int ub = piece * a.piece_units, ue = ub + a.piece_units < a.units ? ub + a.piece_units : a.units;
-  const Source A{a.A[b], 0, static_cast<uint32_t>(a.m)};
-  const Source B{a.B[b], 0, static_cast<uint32_t>(a.n)};
-  f32x16_t acc[T::FN][T::FM] = {};
-  tile_product<T, FA, EXACT>(acc, lds, A, B, a.As[b], a.Bs[b], i0, j0, ub, ue, a.units, wave, lane);
-  const int i = i0 + T::FM * 32 * (wave / T::WN), j = j0 + T::FN * 32 * (wave % T::WN);  // this wave's first row, column
-  typename T::Stage& stage = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
-  if (a.pieces > 1) {
-    float* part = a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n;
-    store_tile<T, kF32, false>(part, acc, stage.code, i, j, a.m, a.n, lane);
-  } else {
-    store_product<T, EXACT>(a.C[b], acc, stage, i, j, a.m, a.n, lane, a.accumulate);
-  }
+  take_tiles<T, FA, EXACT>(
+      lds,
+      [&](int* id, Work* t) {
+        if (*id >= tiles) return false;
+        int outer, ti, tj;
+        tile_of(*id, tiles, tm, tn, &outer, &ti, &tj);
+        const int b = outer / a.pieces, piece = outer - b * a.pieces;
+        t->A = Operand{a.A[b], a.As[b], ti * T::TM, static_cast<uint32_t>(a.m), a.units};
+        t->B = Operand{a.B[b], a.Bs[b], tj * T::TN, static_cast<uint32_t>(a.n), a.units};
+        t->ub = piece * a.piece_units;
+        t->ue = t->ub + a.piece_units < a.units ? t->ub + a.piece_units : a.units;
+        t->sums = a.pieces > 1;
+        t->C = t->sums ? a.partial + (static_cast<int64_t>(piece) * a.batch + b) * a.m * a.n : a.C[b];
+        t->rows = a.m;
+        t->cols = a.n;
+        t->add = a.accumulate != 0;
+        return true;
+      },
+      wave, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -152,14 +154,15 @@ void split_k(int64_t tiles, int units, double elements, Fp8Plan* p) {
 template <class T>
 void launch_tiles(const Fp8GemmArgs& a, hipStream_t s) {
   const int tm = ceil_div(a.m, T::TM), tn = ceil_div(a.n, T::TN);
-  const dim3 grid(static_cast<uint32_t>(tm) * tn * a.batch * a.pieces), block(256);
+  const int tiles = tm * tn * a.batch * a.pieces;
+  const dim3 grid(blocks_of<T>(tiles)), block(256);
   const bool e4m3 = a.a_format == kE4M3;
   if (a.c_dtype == kF32) {
     auto* kernel = e4m3 ? fp8_tile_gemm_kernel<T, kE4M3, kExact> : fp8_tile_gemm_kernel<T, kE5M2, kExact>;
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, tiles);
   } else {
     auto* kernel = e4m3 ? fp8_tile_gemm_kernel<T, kE4M3, kFast> : fp8_tile_gemm_kernel<T, kE5M2, kFast>;
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, tiles);
   }
 }
 

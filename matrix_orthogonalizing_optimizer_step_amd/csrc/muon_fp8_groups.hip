@@ -7,54 +7,119 @@ namespace muon {
 namespace fp8 {
 namespace {
 
-// The grid holds as many row tiles as any counts can need; a block finds its group
-// by a scan of the counts, and those behind the last tile end at once.
+// Counts of a launch's groups (at most `rows` each, the rest as one more group) and
+// the rows before them, in LDS: a block that stays looks for its next tile while its
+// loads are under way, and must not wait for other ones.
+struct Counts {
+  int32_t rows[kF8Groups + 1];
+  int before;
+};
+
+__device__ __forceinline__ void read_counts(Counts& c, const int32_t* counts, int groups, int rows, int first, int count) {
+  if (threadIdx.x <= kF8Groups) {
+    const int g = static_cast<int>(threadIdx.x);
+    c.rows[g] = g <= count ? group_count(counts, first + g, groups, rows) : 0;
+  }
+  if (threadIdx.x < 64) {
+    int n = 0;
+    for (int g = threadIdx.x; g < first; g += 64) n += group_count(counts, g, groups, rows);
+    n = wave_scan(n);
+    if (threadIdx.x == 63) c.before = n;
+  }
+  __syncthreads();
+}
+
+// As many row tiles as there are at most are launched; a block finds its group by a
+// scan of the counts, and those behind the last tile end at once.
 template <class T, int FA, bool EXACT>
 __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp8RowGroupArgs a, int tn) {
   FP8_LDS(T);
+  __shared__ Counts counts;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  const RowTiles<T::TM> tiles{a.counts, a.groups, a.m, a.first, a.first + a.count + a.clear};
-  // consecutive ids go to the 8 XCDs in turn: each gets a contiguous range of tiles
-  const int total = tiles.all(lane) * tn, q = total >> 3, rest = total & 7, x = blockIdx.x & 7, at = blockIdx.x >> 3;
-  if (at >= q + (x < rest ? 1 : 0)) return;
-  const RowTile g = tiles.of(x * q + (x < rest ? x : rest) + at, tn, lane);
-  if (g.group < 0) return;
-  // down columns of 4 tile rows of the group, as in tile_of
-  constexpr int kGroup = 4;
-  const int band = g.tile / (kGroup * tn), top = band * kGroup, h = g.tiles - top < kGroup ? g.tiles - top : kGroup;
-  const int t = g.tile - band * kGroup * tn;
-  const int i0 = g.begin + (top + t % h) * T::TM, j0 = t / h * T::TN;
-  if (g.group == a.groups) {  // rows behind the last group
-    const int rows = g.end - i0 < T::TM ? g.end - i0 : T::TM, cols = a.n - j0 < T::TN ? a.n - j0 : T::TN;
-    for (int p = threadIdx.x; p < rows * cols; p += 256)
-      store_from_f32(a.C, static_cast<int64_t>(i0 + p / cols) * a.n + j0 + p % cols, a.c_dtype, 0.0f);
-    return;
+  read_counts(counts, a.counts, a.groups, a.m, a.first, a.count);
+  const auto count = [&](int g) { return counts.rows[g]; };
+  const RowTiles<T::TM, decltype(count)> row_tiles{count, a.m, a.count, __builtin_amdgcn_readfirstlane(counts.before)};
+  if (a.clear) {  // rows behind the last group
+    int used = counts.before;
+    for (int g = 0; g < a.count; ++g) used += counts.rows[g];
+    const int64_t row = static_cast<int64_t>(a.n) * (EXACT ? 4 : 2);
+    if (used < a.m) clear_bytes(static_cast<char*>(a.C) + used * row, (a.m - used) * row);
   }
-  const int e = g.group - a.first;
-  const Source A{a.A, 0, static_cast<uint32_t>(a.m)};
-  const Source B{a.B[e], 0, static_cast<uint32_t>(a.n)};
-  f32x16_t acc[T::FN][T::FM] = {};
-  tile_product<T, FA, EXACT>(acc, lds, A, B, a.As, a.Bs[e], i0, j0, 0, a.units, a.units, wave, lane);
-  const int i = i0 + T::FM * 32 * (wave / T::WN), j = j0 + T::FN * 32 * (wave % T::WN);
-  typename T::Stage& stage = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
-  store_product<T, EXACT>(a.C, acc, stage, i, j, g.end, a.n, lane, a.accumulate);
+  // consecutive ids go to the 8 XCDs in turn: each gets a contiguous range of tiles
+  const int total = row_tiles.all(lane) * tn, q = total >> 3, rest = total & 7;
+  take_tiles<T, FA, EXACT>(
+      lds,
+      [&](int* id, Work* t) {
+        const int x = *id & 7, at = *id >> 3;
+        if (at >= q + (x < rest ? 1 : 0)) return false;
+        const RowTile g = row_tiles.of(x * q + (x < rest ? x : rest) + at, tn, lane);
+        int ti, tj;
+        tile_in_bands(g.tile, g.tiles, tn, &ti, &tj);
+        const int e = g.group;
+        t->A = Operand{a.A, a.As, g.begin + ti * T::TM, static_cast<uint32_t>(a.m), a.units};
+        t->B = Operand{a.B[e], a.Bs[e], tj * T::TN, static_cast<uint32_t>(a.n), a.units};
+        t->ub = 0;
+        t->ue = a.units;
+        t->sums = false;
+        t->C = a.C;
+        t->rows = g.end;
+        t->cols = a.n;
+        t->add = a.accumulate != 0;
+        return true;
+      },
+      wave, lane);
 }
 
 template <class T, int FA, bool EXACT>
-__global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8KGroupArgs a, int tm, int tn) {
+__global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8KGroupArgs a, int tm, int tn, int ids) {
   FP8_LDS(T);
+  __shared__ Counts counts;
+  __shared__ int units[kF8Groups + 1];  // before each group
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-  int e, ti, tj, ub, ue;
-  tile_of(blockIdx.x, gridDim.x, tm, tn, &e, &ti, &tj);
-  group_units(a.counts, a.groups, a.rows, a.first + e, a.units, lane, &ub, &ue);
-  const int i0 = ti * T::TM, j0 = tj * T::TN;
-  const Source A{a.A, 0, static_cast<uint32_t>(a.m)};
-  const Source B{a.B, 0, static_cast<uint32_t>(a.n)};
-  f32x16_t acc[T::FN][T::FM] = {};
-  tile_product<T, FA, EXACT>(acc, lds, A, B, a.As, a.Bs, i0, j0, ub, ue, a.units, wave, lane);
-  const int i = i0 + T::FM * 32 * (wave / T::WN), j = j0 + T::FN * 32 * (wave % T::WN);
-  typename T::Stage& stage = wave == 0 ? s0 : wave == 1 ? s1 : wave == 2 ? s2 : s3;
-  store_product<T, EXACT>(a.C[e], acc, stage, i, j, a.m, a.n, lane, a.accumulate);
+  read_counts(counts, a.counts, a.groups, a.rows, a.first, a.count);
+  if (threadIdx.x < 64) {
+    int row = 0, n = 0;  // up to the group
+    for (int g0 = -a.first; g0 <= a.count; g0 += 64) {
+      const int g = g0 + lane;
+      const int c = g >= a.count ? 0 : g >= 0 ? counts.rows[g] : group_count(a.counts, a.first + g, a.groups, a.rows);
+      const int upto = row + wave_scan(c);
+      const int begin = upto - c < a.rows ? upto - c : a.rows, end = upto < a.rows ? upto : a.rows;
+      const int mine = (end - begin + kF8Unit - 1) / kF8Unit, sum = n + wave_scan(mine);
+      if (g >= 0 && g <= a.count) units[g] = sum - mine < a.units ? sum - mine : a.units;
+      row = __builtin_amdgcn_readlane(upto, 63);
+      n = __builtin_amdgcn_readlane(sum, 63);
+    }
+  }
+  __syncthreads();
+  // consecutive ids go to the 8 XCDs in turn: each gets a contiguous eighth of every
+  // group's tiles, since groups take very different times (with whole groups to an
+  // XCD, 16 of 2048 x 7168 with 8190 rows in all took 524 us, so 387)
+  const int per = tm * tn, share = (per + 7) >> 3;
+  if (!a.accumulate)
+    for (int e = 0; e < a.count; ++e)
+      if (units[e] == units[e + 1]) clear_bytes(a.C[e], static_cast<int64_t>(a.m) * a.n * (EXACT ? 4 : 2));
+  take_tiles<T, FA, EXACT>(
+      lds,
+      [&](int* id, Work* t) {
+        for (; *id < ids; *id += gridDim.x) {
+          const int at = *id >> 3, e = at / share, tile = (*id & 7) * share + at - e * share;
+          t->ub = __builtin_amdgcn_readfirstlane(units[e]);
+          t->ue = __builtin_amdgcn_readfirstlane(units[e + 1]);
+          if (tile >= per || t->ub == t->ue) continue;  // behind the last eighth's end, or without rows
+          int ti, tj;
+          tile_in_bands(tile, tm, tn, &ti, &tj);
+          t->A = Operand{a.A, a.As, ti * T::TM, static_cast<uint32_t>(a.m), a.units};
+          t->B = Operand{a.B, a.Bs, tj * T::TN, static_cast<uint32_t>(a.n), a.units};
+          t->sums = false;
+          t->C = a.C[e];
+          t->rows = a.m;
+          t->cols = a.n;
+          t->add = a.accumulate != 0;
+          return true;
+        }
+        return false;
+      },
+      wave, lane);
 }
 
 template <class T>
@@ -62,7 +127,7 @@ void launch_rows(const Fp8RowGroupArgs& a, hipStream_t s) {
   const int tn = ceil_div(a.n, T::TN);
   // whole tiles of all rows, and one that is not full for each group and for the rest
   const int64_t tm = a.m / T::TM + a.count + a.clear;
-  const dim3 grid(static_cast<uint32_t>(tm * tn)), block(256);
+  const dim3 grid(blocks_of<T>(tm * tn)), block(256);
   const bool e4m3 = a.a_format == kE4M3;
   if (a.c_dtype == kF32) {
     auto* kernel = e4m3 ? fp8_row_groups_kernel<T, kE4M3, kExact> : fp8_row_groups_kernel<T, kE5M2, kExact>;
@@ -76,14 +141,15 @@ void launch_rows(const Fp8RowGroupArgs& a, hipStream_t s) {
 template <class T>
 void launch_k(const Fp8KGroupArgs& a, hipStream_t s) {
   const int tm = ceil_div(a.m, T::TM), tn = ceil_div(a.n, T::TN);
-  const dim3 grid(static_cast<uint32_t>(tm) * tn * a.count), block(256);
+  const int ids = 8 * ((tm * tn + 7) / 8) * a.count;
+  const dim3 grid(blocks_of<T>(ids)), block(256);
   const bool e4m3 = a.a_format == kE4M3;
   if (a.c_dtype == kF32) {
     auto* kernel = e4m3 ? fp8_k_groups_kernel<T, kE4M3, kExact> : fp8_k_groups_kernel<T, kE5M2, kExact>;
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, ids);
   } else {
     auto* kernel = e4m3 ? fp8_k_groups_kernel<T, kE4M3, kFast> : fp8_k_groups_kernel<T, kE5M2, kFast>;
-    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn);
+    hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, ids);
   }
 }
 
@@ -113,7 +179,7 @@ Fp8Kind fp8_k_group_kind(int groups, int m, int n) {
 
 hipError_t launch_fp8_k_groups(const Fp8KGroupArgs& a, Fp8Kind kind, hipStream_t s) {
   switch (kind) {
-    case kF8Big: launch_k<Big>(a, s); break;
+    case kF8Big: launch_k<Staying>(a, s); break;
     default: launch_k<Mid>(a, s); break;
   }
   return hipGetLastError();

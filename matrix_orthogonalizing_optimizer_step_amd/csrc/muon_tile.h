@@ -34,20 +34,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
                                            __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
 }
 
+// Tile t of tm x tn, running down columns of 4 tile rows, so that tiles worked on at
+// one time share their rows of A and B in an L2.
+__device__ __forceinline__ void tile_in_bands(int t, int tm, int tn, int* ti, int* tj) {
+  constexpr int kGroup = 4;
+  const int g = t / (kGroup * tn), first = g * kGroup, h = tm - first < kGroup ? tm - first : kGroup;
+  t -= g * kGroup * tn;
+  *ti = first + t % h;
+  *tj = t / h;
+}
+
 // Block id -> tile: consecutive ids go to the 8 XCDs in turn, so each XCD gets a
-// contiguous range of tiles, and tiles run down columns of 4 tile rows, so that
-// the tiles an XCD works on at one time share their rows of A and B in its L2.
+// contiguous range of tiles.
 __device__ __forceinline__ void tile_of(int id, int total, int tm, int tn, int* outer, int* ti, int* tj) {
   const int q = total >> 3, rest = total & 7, x = id & 7, at = id >> 3;
   int t = x * q + (x < rest ? x : rest) + at;
   const int per = tm * tn;
   *outer = t / per;
   t -= *outer * per;
-  constexpr int kGroup = 4;
-  const int g = t / (kGroup * tn), first = g * kGroup, h = tm - first < kGroup ? tm - first : kGroup;
-  t -= g * kGroup * tn;
-  *ti = first + t % h;
-  *tj = t / h;
+  tile_in_bands(t, tm, tn, ti, tj);
 }
 
 // Four consecutive elements of a row of C (those with left > 0), with what is
@@ -89,24 +94,27 @@ typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 // has 16 bytes of a row, so that a store fills whole 128 FN-byte (bf16: 64 FN)
 // pieces of rows.  LDS holds C's type, or fp32 where C is added to: C is rounded
 // once.  Measured on 8192x7168x3584 against 8-byte stores of 32 rows at a time
-// straight from the accumulators: 138 -> 122 us.
-template <class T, int DC, bool ADD>
+// straight from the accumulators: 138 -> 122 us.  XS: columns of MFMA tiles that are
+// staged together (the LDS takes 32 rows of them).
+template <class T, int DC, bool ADD, int XS = T::FN>
 __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
                                            int m, int n, int lane) {
   constexpr int kSize = DC == kF32 ? 4 : 2, kHeld = ADD || DC == kF32 ? 4 : 2;  // bytes of an element of C, in LDS
-  constexpr int kCols = 32 * T::FN, kPitch = kCols * kHeld / 16 + 1;            // uint4 of a row, one against conflicts
+  constexpr int kCols = 32 * XS, kPitch = kCols * kHeld / 16 + 1;            // uint4 of a row, one against conflicts
   constexpr int kLanes = kCols * kSize / 16, kRows = 64 / kLanes;               // lanes of a row, rows of a store
-  static_assert(32 * kPitch * 16 <= sizeof(typename T::Stage) && kLanes <= 64, "staging");
+  static_assert(T::FN % XS == 0 && 32 * kPitch * 16 <= sizeof(typename T::Stage) && kLanes <= 64, "staging");
   const int row = lane & 31, half = lane >> 5, r0 = lane / kLanes, chunk = lane % kLanes;
   constexpr int kElems = 16 / kSize;
-  const int jc = j + chunk * kElems;
 #pragma unroll
-  for (int y = 0; y < T::FM; ++y) {
+  for (int yx = 0; yx < T::FM * (T::FN / XS); ++yx) {
+    const int y = yx / (T::FN / XS), x0 = yx % (T::FN / XS) * XS;
+    const int jc = j + 32 * x0 + chunk * kElems;
 #pragma unroll
-    for (int x = 0; x < T::FN; ++x)
+    for (int x = 0; x < XS; ++x)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float v[4] = {acc[x][y][4 * g], acc[x][y][4 * g + 1], acc[x][y][4 * g + 2], acc[x][y][4 * g + 3]};
+        const f32x16_t& t = acc[x0 + x][y];
+        const float v[4] = {t[4 * g], t[4 * g + 1], t[4 * g + 2], t[4 * g + 3]};
         const int col = 32 * x + 8 * g + 4 * half;
         if constexpr (kHeld == 4) {
           stage[row * kPitch + col / 4] = __builtin_bit_cast(uint4, make_float4(v[0], v[1], v[2], v[3]));
