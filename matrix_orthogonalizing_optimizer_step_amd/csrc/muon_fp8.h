@@ -100,7 +100,7 @@ struct Fp8KGroupArgs {
 };
 
 // How a product of one launch is computed.
-enum Fp8Kind : int { kF8FewRows = 0, kF8Low, kF8Mid, kF8Big };
+enum Fp8Kind : int { kF8FewRows = 0, kF8Low, kF8Mid, kF8Big, kF8Staying };
 struct Fp8Plan {
   Fp8Kind kind;
   int pieces, piece_units;
@@ -111,7 +111,7 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, Fp8Kind kind, hipStream_t s);
 hipError_t launch_fp8_join(const Fp8GemmArgs& a, hipStream_t s);  // the pieces' sums into C
 Fp8Kind fp8_row_group_kind(int groups, int m, int n);
 hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStream_t s);
-Fp8Kind fp8_k_group_kind(int groups, int m, int n);
+Fp8Kind fp8_k_group_kind(int groups, int rows, int m, int n, bool fp32);
 hipError_t launch_fp8_k_groups(const Fp8KGroupArgs& a, Fp8Kind kind, hipStream_t s);
 
 // 2^(byte - 127), NaN for byte 255.

@@ -746,7 +746,7 @@ muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, con
   if (!type_ok(c_dtype) || (accumulate != 0 && accumulate != 1)) return MUON_ERR_INVALID_ARG;
   if (c_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const Fp8Kind kind = fp8_k_group_kind(groups, m, n);
+  const Fp8Kind kind = fp8_k_group_kind(groups, rows, m, n, c_dtype == MUON_F32);
   for (int at = 0; at < groups; at += kF8Groups) {
     Fp8KGroupArgs a;
     a.count = groups - at < kF8Groups ? groups - at : kF8Groups;

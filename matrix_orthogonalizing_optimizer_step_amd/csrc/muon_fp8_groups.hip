@@ -158,9 +158,23 @@ void launch_k(const Fp8KGroupArgs& a, hipStream_t s) {
 
 using namespace fp8;
 
+// Which tiles, for rows that are not known here but as a sum: a group's last tile row
+// is taken to be half full.  Times in us, 64 x 128 / 128 x 128 / 256 x 256 tiles, rows
+// spread unevenly:
+//   256 x 256  where that leaves at least 3/5 of their rounds on 256 compute units to
+//              real work: 64 groups, n 2048, k 7168, 16380 rows 430 / 341 / 300, 32768
+//              rows 749 / 589 / 528; not 8000 rows 275 / 254 / 270, nor 16 groups with
+//              8190 rows 170 / 137 / 160, fp32 270 / 240 / 300
+//   128 x 128  from a mean of 96 rows on: those, and 8 groups, 1024 x 1024, 4096 rows 13 /
+//              12 / 20
+//   64 x 128   for fewer: 64 groups, 4000 rows 188 / 194 / 197, fp32 207 / 259 / 340, 24
+//              rows 62 / 74 / 87; 8 groups, 1024 x 1024, 600 rows 7.2 / 8.0 / 18
 Fp8Kind fp8_row_group_kind(int groups, int m, int n) {
-  const int64_t mean = m / groups;
-  return mean >= 192 && n >= 192 ? kF8Big : mean >= 48 ? kF8Mid : kF8Low;
+  const int64_t big = (static_cast<int64_t>(m) / Big::TM + (groups + 1) / 2) * ceil_div(n, Big::TN);
+  const int64_t rounds = (big + kCUs - 1) / kCUs;
+  const double work = static_cast<double>(m) * n / (Big::TM * Big::TN);
+  if (work * 5 >= static_cast<double>(rounds) * kCUs * 3) return kF8Big;
+  return m / groups >= 96 ? kF8Mid : kF8Low;
 }
 
 hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStream_t s) {
@@ -172,14 +186,26 @@ hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStre
   return hipGetLastError();
 }
 
-Fp8Kind fp8_k_group_kind(int groups, int m, int n) {
+// Which tiles (us, 128 x 128 / 256 x 256 / 256 x 256 by blocks that stay):
+//   that stay  fp32 results from three rounds of tiles on, where the results' way to
+//              memory counts most: 16 groups of 2048 x 7168, 8190 rows 400 / 387 / 350, 64
+//              groups, 16380 rows 1195 / 1069 / 979, 4 groups, 8190 rows 231 / 234 / 219.
+//              A fixed share of the tiles is no good for fewer: 8 groups of 2048 x 2048,
+//              32768 rows (two rounds) 235 / 240 / 288
+//   256 x 256  otherwise from two rounds on, if groups have 192 rows on average: bf16
+//              271 / 242 / 270, 815 / 795 / 937, 131 / 126 / 131, 131 / 121 / 141
+//   128 x 128  for fewer tiles or rows: 16 groups of 1024 x 1024, 2000 rows bf16 15 / 20 /
+//              22; 64 of 512 x 2048, 1000 rows 35 / 49 / 59
+Fp8Kind fp8_k_group_kind(int groups, int rows, int m, int n, bool fp32) {
   const int64_t big = static_cast<int64_t>(ceil_div(m, Big::TM)) * ceil_div(n, Big::TN) * groups;
-  return big >= kCUs ? kF8Big : kF8Mid;
+  if (fp32 && big >= 3 * kCUs) return kF8Staying;
+  return big >= 2 * kCUs && rows / groups >= 192 ? kF8Big : kF8Mid;
 }
 
 hipError_t launch_fp8_k_groups(const Fp8KGroupArgs& a, Fp8Kind kind, hipStream_t s) {
   switch (kind) {
-    case kF8Big: launch_k<Staying>(a, s); break;
+    case kF8Staying: launch_k<Staying>(a, s); break;
+    case kF8Big: launch_k<Big>(a, s); break;
     default: launch_k<Mid>(a, s); break;
   }
   return hipGetLastError();

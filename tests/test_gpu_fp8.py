@@ -368,15 +368,17 @@ def test_grouped_product(counts, rows, fmt):
         assert not C[0][total:].any() and torch.equal(D[0][total:], C0[total:]) and torch.equal(F[0][total:], C0[total:])
 
 
-@pytest.mark.parametrize("rows,groups,n,k", [(5000, 4, 600, 300), (1100, 9, 520, 640), (700, 2, 300, 400)])
+@pytest.mark.parametrize("rows,groups,n,k", [(10000, 4, 1100, 200), (1100, 9, 520, 640), (700, 2, 300, 400)])
 def test_grouped_product_in_larger_tiles(rows, groups, n, k):
-    """Means of 128 x 128 and 256 x 256 tiles, exact."""
-    counts = skewed(rows, groups, 5)
+    """256 x 256 tiles and 128 x 128 ones, exact."""
+    counts = skewed(rows - 3, groups, 5)
     A, B = random_code(1, rows, k, 33, 127, 127, whole=True), random_code(groups, n, k, 34, 127, 127, whole=True)
-    C = mu.fp8_grouped_matmul(A, B, device_counts(counts), torch.float32)[0]
     a, b = values(A)[0], values(B)
-    for e, i, j in groups_of(counts, rows):
-        assert np.array_equal(f64(C[i:j]), a[i:j] @ b[e].T), e
+    for dtype in ("f32", "bf16"):
+        C = mu.fp8_grouped_matmul(A, B, device_counts(counts), DT[dtype])[0]
+        for e, i, j in groups_of(counts, rows):
+            check(C[i:j], a[i:j], b[e], dtype, exact=True)
+        assert not C[-3:].any()
 
 
 def test_grouped_product_with_counts_that_do_not_fit():
@@ -446,14 +448,188 @@ def test_grouped_weight_gradient(counts, rows, fmt):
             at += u
 
 
-def test_grouped_weight_gradient_in_large_tiles():
-    counts = [700, 0, 130, 1]
-    A = random_code(1, 2300, sum(counts), 53, 127, 127, whole=True, groups=4)
-    B = random_code(1, 2100, sum(counts), 54, 127, 127, whole=True, groups=4)
-    C = mu.fp8_grouped_weight_grad(A, B, device_counts(counts))
-    whole = lambda q: values(mu.FP8(q.codes, q.scales, q.codes[0].shape[0] * 64))[0]  # noqa: E731
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,counts", [(4100, 4099, [700, 0, 130, 1]), (2300, 2100, [700, 0, 130, 1]),
+                                        (1030, 515, [129, 3, 0, 256, 300, 128] * 12)])
+def test_grouped_weight_gradient_in_large_tiles(m, n, counts, dtype):
+    """Every size of tiles, blocks that stay for tile after tile (odd and even numbers of units, groups without rows, tiles
+    that are not full), exact; also added to C."""
+    G, rows = len(counts), sum(counts)
+    A = random_code(1, m, rows, 53, 127, 127, whole=True, groups=G)
+    B = random_code(1, n, rows, 54, 127, 127, whole=True, groups=G)
+    C = mu.fp8_grouped_weight_grad(A, B, device_counts(counts), DT[dtype])
+    D = [torch.ones(m, n, dtype=DT[dtype], device=DEV) for _ in counts]
+    mu.fp8_grouped_weight_grad(A, B, device_counts(counts), out=D, accumulate=True)
+    whole = lambda q: torch.from_numpy(values(mu.FP8(q.codes, q.scales, q.codes[0].shape[0] * 64))[0]).to(DEV)  # noqa: E731
     a, b, at = whole(A), whole(B), 0
-    for c, g in zip(counts, C):
+    for c, g, d in zip(counts, C, D):
         part = slice(at * 128, (at + -(-c // 128)) * 128)
-        assert np.array_equal(f64(g), a[:, part] @ b[:, part].T)
+        want = a[:, part] @ b[:, part].t().contiguous()
+        assert torch.equal(g, want.to(g.dtype)) and torch.equal(d, (want + 1).to(g.dtype))
         at += -(-c // 128)
+
+
+# --- refusals, graphs, streams, sizes ---------------------------------------------------------------------------------
+def test_refusals_on_the_device():
+    A, B = random_code(1, 4, 100, 19), random_code(1, 5, 100, 20)
+    X, n2 = torch.zeros(4, 100, device=DEV), device_counts([2, 2])
+    for match, call in [
+            ("row length", lambda: mu.fp8_matmul(A, random_code(1, 5, 101, 20))),
+            ("batch", lambda: mu.fp8_matmul(A, random_code(2, 5, 100, 20))),
+            ("accumulate", lambda: mu.fp8_matmul(A, B, accumulate=True)),
+            ("e4m3", lambda: mu.fp8_matmul(A, random_code(1, 5, 100, 20, fmt="e5m2"))),
+            ("out", lambda: mu.fp8_matmul(A, B, out=[torch.zeros(5, 4, device=DEV)])),
+            ("transpose", lambda: mu.fp8_quantize([X], transpose="rows")),
+            ("block", lambda: mu.fp8_quantize([X], block="cell")),
+            ("format", lambda: mu.fp8_quantize([X], format="e3m4")),
+            ("out", lambda: mu.fp8_quantize([X], out=random_code(1, 4, 101, 1))),
+            ("out", lambda: mu.fp8_quantize([X], out=A, format="e5m2")),
+            ("contiguous", lambda: mu.fp8_quantize([torch.zeros(3, 4, device=DEV).t()])),
+            ("empty", lambda: mu.fp8_quantize([torch.zeros(0, 5, device=DEV)])),
+            ("counts", lambda: mu.fp8_quantize([X], counts=n2)),
+            ("counts", lambda: mu.fp8_quantize([X], "tile", True, counts=n2)),
+            ("counts", lambda: mu.fp8_quantize([X, X + 1], transpose=True, counts=n2)),
+            ("counts", lambda: mu.fp8_quantize([X], transpose=True, counts=n2.long())),
+            ("counts", lambda: mu.fp8_quantize([X], transpose=True, counts=[2, 2])),
+            ("counts", lambda: mu.fp8_grouped_matmul(A, B, n2)),
+            ("counts", lambda: mu.fp8_grouped_matmul(A, B, n2.view(1, 2))),
+            ("out", lambda: mu.fp8_grouped_matmul(A, random_code(2, 5, 100, 3), n2, out=[torch.zeros(5, 5, device=DEV)])),
+            ("groups", lambda: mu.fp8_matmul(mu.fp8_quantize([X], transpose=True, counts=n2), random_code(1, 5, 4, 20))),
+            ("groups", lambda: mu.fp8_dequantize(mu.fp8_quantize([X], transpose=True, counts=n2))),
+            ("counts", lambda: mu.fp8_grouped_weight_grad(A, A, n2)),
+            ("units", lambda: mu.fp8_matmul(mu.FP8(A.codes, A.scales, 300), B)),
+            ("rows rounded", lambda: mu.fp8_matmul(mu.FP8(A.codes, [A.scales[0][:, :4]], 100), B)),
+            ("float8", lambda: mu.fp8_matmul(mu.FP8([A.codes[0].view(torch.uint8)], A.scales, 100), B)),
+            ("overlaps", lambda: mu.fp8_matmul(random_code(2, 4, 100, 19), random_code(2, 5, 100, 20),
+                                               out=[torch.zeros(4, 5, device=DEV)] * 2)),
+            ("stream", lambda: mu.fp8_matmul(A, B, stream=type("S", (), {"cuda_stream": 0, "device": torch.device("cuda:1")})()))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    codes = torch.zeros(2 * 4 * 64 + 8, dtype=torch.uint8, device=DEV)[8:].view(F8["e4m3"]).view(2, 4, 64)
+    with pytest.raises(ValueError, match="aligned"):
+        mu.fp8_matmul(mu.FP8([codes], A.scales, 100), B)
+    for call in (lambda: mu.fp8_matmul(A, B, torch.float16), lambda: mu.fp8_dequantize(A, torch.float16),
+                 lambda: mu.fp8_grouped_matmul(A, random_code(2, 5, 100, 3), n2, torch.float16)):
+        with pytest.raises(mu.MuonError):
+            call()
+
+
+def test_captured_layer_replays_like_eager():
+    """Codes, products (the split over k among them), the experts' three products and accumulation in one graph; new data
+    and new counts between the replays; two graphs replayed side by side."""
+    sets = []
+    for seed in range(2):
+        gen = torch.Generator().manual_seed(seed)
+        X, dY = torch.randn(300, 2000, generator=gen).to(DEV).bfloat16(), torch.randn(300, 200, generator=gen).to(DEV)
+        W = random_code(1, 200, 2000, 21 + seed)
+        E, Et = random_code(3, 200, 2000, 23 + seed), random_code(3, 2000, 200, 25 + seed)
+        counts = device_counts([100, 150, 50])
+        C, S = [torch.zeros(300, 200, device=DEV)], [torch.zeros(300, 200, device=DEV)]
+        Y, dX, dW = [torch.zeros(300, 200, device=DEV)], [torch.zeros(300, 2000, device=DEV)], \
+            [torch.zeros(200, 2000, device=DEV) for _ in range(3)]
+
+        def layer(X=X, dY=dY, W=W, E=E, Et=Et, counts=counts, C=C, S=S, Y=Y, dX=dX, dW=dW):
+            q, qt = mu.fp8_quantize([X], transpose="both", counts=counts)
+            mu.fp8_matmul(q, W, out=C)
+            mu.fp8_matmul(q, W, out=S, accumulate=True)
+            mu.fp8_grouped_matmul(q, E, counts, out=Y)
+            d, dt = mu.fp8_quantize([dY], transpose="both", counts=counts)
+            mu.fp8_grouped_matmul(d, Et, counts, out=dX)
+            mu.fp8_grouped_weight_grad(dt, qt, counts, out=dW)
+
+        layer()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer()
+        sets.append((graph, torch.cuda.Stream(), layer, X, counts, (C, Y, dX, dW), S, S[0].clone()))
+    for i, new in enumerate(([100, 150, 50], [0, 300, 0], [1, 2, 3], [299, 0, 1])):
+        for _, _, _, X, counts, *_ in sets:
+            X.copy_(torch.randn(300, 2000, generator=torch.Generator().manual_seed(i)))
+            counts.copy_(torch.tensor(new, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for graph, s, *_ in sets:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, layer, _, _, outs, S, total in sets:
+            got = [x.clone() for o in outs for x in o]
+            total += got[0]
+            assert torch.equal(S[0], total), i
+            layer()
+            S[0].copy_(total)
+            assert all(torch.equal(a, b) for a, b in zip(got, [x for o in outs for x in o])), i
+
+
+def test_two_products_at_once_on_two_streams():
+    A, B = random_code(1, 260, 6000, 22), random_code(1, 300, 6000, 23)
+    want = mu.fp8_matmul(A, B, torch.float32)[0]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[mu.fp8_matmul(A, B, torch.float32, stream=s)[0] for s in streams] for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for pair in got for x in pair)
+
+
+def test_given_outputs_raise_their_version_and_launches_are_traced():
+    X = matrices(1, 40, 200, "f32", 61)
+    counts = device_counts([40])
+    q, t = mu.fp8_quantize(X, transpose="both", counts=counts)
+    Y, C, G = [torch.zeros(40, 200, device=DEV)], [torch.zeros(40, 40, device=DEV)], [torch.zeros(200, 200, device=DEV)]
+    ws = torch.zeros(mu.fp8_workspace_size(1, 40, 40, 200), dtype=torch.uint8, device=DEV)
+    written = q.codes + q.scales + t.codes + t.scales + Y + C + G + [ws]
+    before, held = [x._version for x in written], (X[0]._version, counts._version)
+    mu.trace_enable(True)
+    mu.fp8_quantize(X, transpose="both", counts=counts, out=(q, t))
+    codes = [x._version for x in q.codes + q.scales]
+    mu.fp8_dequantize(q, out=Y)
+    mu.fp8_matmul(q, q, out=C, workspace=ws)
+    mu.fp8_grouped_matmul(q, q, counts, out=C)
+    mu.fp8_grouped_weight_grad(t, t, counts, out=G)
+    recs = mu.trace_collect()
+    mu.trace_enable(False)
+    assert all(x._version > b for x, b in zip(written, before))
+    assert (X[0]._version, counts._version) == held and [x._version for x in q.codes + q.scales] == codes
+    assert [r["role"] for r in recs] == ["fp8_quantize", "fp8_dequantize", "fp8_matmul", "fp8_grouped_matmul", "fp8_weight_grad"]
+    assert recs[2]["flops"] == 2.0 * 40 * 40 * 200
+
+
+def test_code_and_product_past_2_31_bytes():
+    """66000 x 32768: 2.16e9 elements of X and as many code bytes; the last rows' codes in both orientations, and a product
+    whose A ends behind 2^31 bytes."""
+    rows, cols = 66000, 32768
+    X = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    X[-300:] = torch.randn(300, cols, device=DEV, generator=torch.Generator(DEV).manual_seed(3)).to(torch.bfloat16)
+    q, t = mu.fp8_quantize([X], transpose="both")
+    wc, ws = fo.quantize(f64(X[-80:]))
+    assert np.array_equal(bytes_of(q.codes[0][:, -80:].contiguous()), wc)
+    assert np.array_equal(q.scales[0][:, rows - 80:rows].cpu().numpy(), ws)
+    wc, ws = fo.quantize(f64(X[65920:]).T)  # the last unit starts at row 515 * 128
+    assert np.array_equal(bytes_of(t.codes[0][2 * 515:]), wc) and np.array_equal(t.scales[0][515:].cpu().numpy(), ws)
+    assert not bytes_of(t.codes[0][:2 * 513, :4].contiguous()).any()
+    only = mu.fp8_quantize([X])
+    assert torch.equal(only.codes[0].view(torch.uint8), q.codes[0].view(torch.uint8))
+    del only, t
+    Y = mu.fp8_dequantize(q, torch.bfloat16)[0]
+    want = fo.decode(bytes_of(q.codes[0][:, -80:].contiguous()), q.scales[0][:, rows - 80:rows].cpu().numpy(), cols)
+    assert np.array_equal(f64(Y[-80:]), want)
+    del Y, X
+    B = random_code(1, 40, cols, 3)
+    for dt in (torch.float32, torch.bfloat16):
+        C = mu.fp8_matmul(q, B, dt)[0]
+        check(C[-80:], want, values(B)[0], "f32" if dt == torch.float32 else "bf16")
+        assert not C[:65000].any()
+    # the same rows as the last of two groups
+    C = mu.fp8_grouped_matmul(q, mu.FP8([B.codes[0].clone(), B.codes[0]], [B.scales[0].clone(), B.scales[0]], cols),
+                              device_counts([65900, 100]), torch.float32)[0]
+    check(C[-80:], want, values(B)[0], "f32")
+
+
+def test_product_past_2_31_elements():
+    """50000 x 50000 results (2.5e9): rows at the start, in the middle and at the end."""
+    A = random_code(1, 50000, 100, 26, 127, 127, whole=True)
+    B = random_code(1, 50000, 100, 27, 127, 127, whole=True)
+    b64, a64 = values(B)[0], values(A)[0]
+    C = mu.fp8_matmul(A, B, torch.bfloat16)[0]
+    for i in (0, 1, 255, 256, 42949, 42950, 49997, 49999):
+        assert np.array_equal(f64(C[i]), f64(torch.from_numpy((a64[i] @ b64.T).astype(np.float32)).to(torch.bfloat16))), i
