@@ -50,7 +50,7 @@ struct Tile {
   static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;
   static constexpr int kCodeLoads = TM / 64 + TN / 64;  // per wave and slab
   static constexpr bool kStays = STAYS;                 // its block takes tile after tile
-  static constexpr int kStores(bool fp32) { return FM * FN * 32 * 32 * (fp32 ? 4 : 2) / 1024; }  // of a wave and tile
+  static constexpr int kStores = FM * FN * 4;           // of a wave and tile of fp32 results, 1 KB each
   struct Stage {
     uint4 code[(TM + TN) * 4];  // A rows, then B rows, 4 slots each
   };
@@ -352,7 +352,8 @@ template <class T, bool EXACT, bool ADD>
 __device__ __forceinline__ void store_product(const Work& t, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
                                               int lane) {
   constexpr int DC = EXACT ? kF32 : kBF16;
-  constexpr int XS = !T::kStays ? T::FN : (EXACT || ADD ? 1 : 2);  // rows of 128 bytes, where a block stays
+  static_assert(EXACT || !T::kStays, "blocks that stay are for fp32 results");
+  constexpr int XS = T::kStays ? 1 : T::FN;  // rows of 128 bytes, where a block stays
   store_tile<T, DC, ADD, XS>(t.C, acc, stage, i, j, t.rows, t.cols, lane);
 }
 
@@ -383,9 +384,50 @@ __device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, 
   S.template advance<true>();
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(3 * T::kCodeLoads + 1, 0));  // the first slab has landed
   asm volatile("s_barrier" ::: "memory");
+  // One slab of a wave that has no rows or columns of the tile: only its loads.
+  const auto pass = [&](auto odd, typename T::Stage& stage, ScaleStage& sc) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
+    asm volatile("s_barrier" ::: "memory");
+    load_slab<T>(stage, S, off, wave);
+    if constexpr (!decltype(odd)::value) load_scales(sc, S, off, wave);
+    S.template advance<decltype(odd)::value>();
+  };
+  constexpr std::false_type kEvenSlab;
+  constexpr std::true_type kOddSlab;
   bool full = false;  // the last tile had all its stores
   for (;;) {
     const int i = t.A.row + ra, j = t.B.row + rb;  // this wave's first row and column
+    // what the last round loads: the next tile's first one, or anything
+    Work n = t;
+    bool more = false;
+    if constexpr (T::kStays) {
+      id += gridDim.x;
+      more = find(&id, &n);
+    }
+    Stream N;
+    N.start(n.A, n.B, n.ub, n.ue, wave);
+    int units = t.ue - t.ub;
+    // groups end anywhere in a tile: half of the last tiles' waves have nothing to do,
+    // and leave their power to the others
+    if (i >= t.rows || j >= t.cols) {
+      for (; units > 0; units -= 2) {
+        if (units <= 2) S = N;
+        pass(kEvenSlab, lds.s0, lds.c0);
+        pass(kOddSlab, lds.s1, lds.c1);
+        if (T::kStays || units >= 2) {
+          pass(kEvenSlab, lds.s2, lds.c1);
+          pass(kOddSlab, lds.s3, lds.c0);
+        }
+      }
+      if constexpr (!T::kStays) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        asm volatile("s_barrier" ::: "memory");  // the others' in front of their results
+      }
+      if (!more) break;
+      full = false;
+      t = n;
+      continue;
+    }
     f32x16_t acc[T::FN][T::FM] = {};
     // the first slab is in s0: the last barrier stood behind its loads
     const Reads at{ra, T::TM + rb, (t.A.row & (kF8Line - 1)) + ra, (t.B.row & (kF8Line - 1)) + rb};
@@ -398,16 +440,6 @@ __device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, 
     read_scales<T::FN>(w.b, lds.c0.b, at.sb, lane);
     read_scales<T::FM>(w.a, lds.c0.a, at.sa, lane);
     if constexpr (EXACT) widen<T, FA, 0>(v, f, w);
-    // what the last round loads: the next tile's first one, or anything
-    Work n = t;
-    bool more = false;
-    if constexpr (T::kStays) {
-      id += gridDim.x;
-      more = find(&id, &n);
-    }
-    Stream N;
-    N.start(n.A, n.B, n.ub, n.ue, wave);
-    int units = t.ue - t.ub;
     const auto round = [&](auto stores) {
       constexpr int kStores = decltype(stores)::value;
       if (units == 2) S = N;
@@ -420,7 +452,7 @@ __device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, 
     // the loads that the first round waits for were issued before the stores of the
     // tile before; if it had all of them, they need not have ended
     if constexpr (T::kStays)
-      if (full && units >= 2) round(std::integral_constant<int, T::kStores(EXACT)>());
+      if (full && units >= 2) round(std::integral_constant<int, T::kStores>());
     while (units >= 2) round(std::integral_constant<int, 0>());
     if (units > 0) {
       S = N;
@@ -428,15 +460,8 @@ __device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, 
       slab<T, FA, EXACT, true, 0>(acc, f, w, v, lds.s1, lds.s2, lds.c1, S, off, wave, lane, at);
       if constexpr (T::kStays) {
         // the two slabs that were loaded for nothing give way to others
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
-        asm volatile("s_barrier" ::: "memory");
-        load_slab<T>(lds.s2, S, off, wave);
-        load_scales(lds.c1, S, off, wave);
-        S.template advance<false>();
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * T::kCodeLoads + 1, 0));
-        asm volatile("s_barrier" ::: "memory");
-        load_slab<T>(lds.s3, S, off, wave);
-        S.template advance<true>();
+        pass(kEvenSlab, lds.s2, lds.c1);
+        pass(kOddSlab, lds.s3, lds.c0);
       }
     }
     uint4* stage = lds.out + wave * 32 * kOutPitch;

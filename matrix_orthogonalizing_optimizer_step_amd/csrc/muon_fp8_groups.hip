@@ -144,10 +144,10 @@ void launch_k(const Fp8KGroupArgs& a, hipStream_t s) {
   const int ids = 8 * ((tm * tn + 7) / 8) * a.count;
   const dim3 grid(blocks_of<T>(ids)), block(256);
   const bool e4m3 = a.a_format == kE4M3;
-  if (a.c_dtype == kF32) {
+  if (T::kStays || a.c_dtype == kF32) {
     auto* kernel = e4m3 ? fp8_k_groups_kernel<T, kE4M3, kExact> : fp8_k_groups_kernel<T, kE5M2, kExact>;
     hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, ids);
-  } else {
+  } else if constexpr (!T::kStays) {
     auto* kernel = e4m3 ? fp8_k_groups_kernel<T, kE4M3, kFast> : fp8_k_groups_kernel<T, kE5M2, kFast>;
     hipLaunchKernelGGL(kernel, grid, block, 0, s, a, tm, tn, ids);
   }
