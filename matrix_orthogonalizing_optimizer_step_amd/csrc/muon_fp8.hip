@@ -213,7 +213,7 @@ __device__ __forceinline__ void load_tile(const void* X, int64_t at, int64_t pit
   }
 }
 
-template <int D, int F, bool NT>
+template <int D, int F, bool NT, bool PAST>
 __global__ __launch_bounds__(kThreads) void fp8_tile_kernel(Fp8QuantArgs a) {
   __shared__ __align__(16) uint8_t col_code[128 * kCodePitch];
   __shared__ __align__(16) uint8_t row_code[128 * kCodePitch];
@@ -320,14 +320,22 @@ __global__ __launch_bounds__(kThreads) void fp8_tile_kernel(Fp8QuantArgs a) {
           code4<F>(x[e][0], x[e][1], x[e][2], x[e][3], (row_bytes[e >> 2] >> (8 * (e & 3))) & 255u);
   }
   __syncthreads();
+  const auto put = [&](u32x4_t* to, const uint8_t* from) {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(from);
+    if constexpr (PAST) {
+      __builtin_nontemporal_store(v, to);
+    } else {
+      *to = v;
+    }
+  };
   if (cols) {
     const int left = a.cols - j0;
-    uint4* codes = static_cast<uint4*>(a.codes_t[b]);
+    u32x4_t* codes = static_cast<u32x4_t*>(a.codes_t[b]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int p = q * kThreads + tid, half = p >> 9, col = (p >> 2) & 127, chunk = p & 3;
       if (col < left)
-        codes[(static_cast<int64_t>(2 * unit + half) * a.cols + j0 + col) * 4 + chunk] = *reinterpret_cast<const uint4*>(
+        put(codes + (static_cast<int64_t>(2 * unit + half) * a.cols + j0 + col) * 4 + chunk,
             col_code + (32 * (col & 3) + (col >> 2)) * kCodePitch + half * kF8Piece + chunk * 16);
     }
     if (tid < 128 && tid < left)
@@ -335,13 +343,13 @@ __global__ __launch_bounds__(kThreads) void fp8_tile_kernel(Fp8QuantArgs a) {
   }
   if (rows) {
     const int left = end - i0;
-    uint4* codes = static_cast<uint4*>(a.codes[b]);
+    u32x4_t* codes = static_cast<u32x4_t*>(a.codes[b]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int p = q * kThreads + tid, half = p >> 9, row = (p >> 2) & 127, chunk = p & 3;
       if (row < left)
-        codes[(static_cast<int64_t>(2 * blockIdx.x + half) * a.rows + i0 + row) * 4 + chunk] =
-            *reinterpret_cast<const uint4*>(row_code + row * kCodePitch + half * kF8Piece + chunk * 16);
+        put(codes + (static_cast<int64_t>(2 * blockIdx.x + half) * a.rows + i0 + row) * 4 + chunk,
+            row_code + row * kCodePitch + half * kF8Piece + chunk * 16);
     }
     if (tid < 128 && tid < left)
       static_cast<uint8_t*>(a.scales[b])[blockIdx.x * fp8_pitch(a.rows) + i0 + tid] = row_scale[tid];
@@ -425,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void fp8_values_kernel(Fp8DequantArgs a, 
   }
 }
 
-template <int D, int F, bool NT>
+template <int D, int F, bool NT, bool PAST>
 void quantize(const Fp8QuantArgs& a, int batch, hipStream_t s) {
   const int64_t col_units = fp8_units(a.cols);
   if (a.codes_t[0] == nullptr && a.tile == 0) {
@@ -437,19 +445,25 @@ void quantize(const Fp8QuantArgs& a, int batch, hipStream_t s) {
   const int64_t row_units =
       a.counts == nullptr ? fp8_units(a.rows) : a.rows / kF8Unit + a.groups + (a.codes[0] != nullptr ? 1 : 0);
   const dim3 grid(static_cast<uint32_t>(col_units), static_cast<uint32_t>(row_units), batch);
-  hipLaunchKernelGGL((fp8_tile_kernel<D, F, NT>), grid, dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((fp8_tile_kernel<D, F, NT, PAST>), grid, dim3(kThreads), 0, s, a);
 }
 
-// Inputs larger than the 256 MB cache are read past it.
-constexpr double kStreamBytes = 256.0 * (1 << 20);
+// A call that moves more than the 256 MB cache holds reads past it (us): 16380x7168
+// bf16 along rows 66 -> 56, both ways 90 -> 73; 4096x18944 bf16 both ways 56 -> 54,
+// along rows, which fits, 35 -> 39.  One of several times that also writes a tile's
+// codes past it: 3 x 3584x18944 fp32 both ways 224 -> 206, one of them 65 -> 70.
+constexpr double kCacheBytes = 256.0 * (1 << 20), kPastBytes = 3.0 * kCacheBytes;
 
 template <int D, int F>
 void quantize(const Fp8QuantArgs& a, int batch, hipStream_t s) {
-  const double bytes = static_cast<double>(a.rows) * a.cols * batch * (D == kF32 ? 4 : 2);
-  if (bytes > kStreamBytes) {
-    quantize<D, F, true>(a, batch, s);
+  const double elements = static_cast<double>(a.rows) * a.cols * batch;
+  const double bytes = elements * ((D == kF32 ? 4 : 2) + (a.codes[0] != nullptr ? 1 : 0) + (a.codes_t[0] != nullptr ? 1 : 0));
+  if (bytes > kPastBytes) {
+    quantize<D, F, true, true>(a, batch, s);
+  } else if (bytes > kCacheBytes) {
+    quantize<D, F, true, false>(a, batch, s);
   } else {
-    quantize<D, F, false>(a, batch, s);
+    quantize<D, F, false, false>(a, batch, s);
   }
 }
 template <int D>
