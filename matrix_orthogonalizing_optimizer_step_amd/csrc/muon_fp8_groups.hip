@@ -40,8 +40,8 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp
   const auto count = [&](int g) { return counts.rows[g]; };
   const RowTiles<T::TM, decltype(count)> row_tiles{count, a.m, a.count, __builtin_amdgcn_readfirstlane(counts.before)};
   if (a.clear) {  // rows behind the last group
-    int used = counts.before;
-    for (int g = 0; g < a.count; ++g) used += counts.rows[g];
+    const int mine = (lane < a.count ? counts.rows[lane] : 0) + (lane + 64 < a.count ? counts.rows[lane + 64] : 0);
+    const int used = counts.before + __builtin_amdgcn_readlane(wave_scan(mine), 63);
     const int64_t row = static_cast<int64_t>(a.n) * (EXACT ? 4 : 2);
     if (used < a.m) clear_bytes(static_cast<char*>(a.C) + used * row, (a.m - used) * row);
   }
@@ -96,8 +96,10 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8K
   // XCD, 16 of 2048 x 7168 with 8190 rows in all took 524 us, so 387)
   const int per = tm * tn, share = (per + 7) >> 3;
   if (!a.accumulate)
-    for (int e = 0; e < a.count; ++e)
-      if (units[e] == units[e + 1]) clear_bytes(a.C[e], static_cast<int64_t>(a.m) * a.n * (EXACT ? 4 : 2));
+    for (int e0 = 0; e0 < a.count; e0 += 64)
+      for (uint64_t none = __ballot(e0 + lane < a.count && units[e0 + lane] == units[e0 + lane + 1]); none != 0;
+           none &= none - 1)
+        clear_bytes(a.C[e0 + __builtin_ctzll(none)], static_cast<int64_t>(a.m) * a.n * (EXACT ? 4 : 2));
   take_tiles<T, FA, EXACT>(
       lds,
       [&](int* id, Work* t) {

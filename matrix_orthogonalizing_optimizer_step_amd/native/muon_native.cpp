@@ -106,6 +106,12 @@ class Buffers {
     return memory;
   }
 
+  // `bytes` bytes from p on that are read.
+  void add_read(const void* p, size_t bytes) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p);
+    if (bytes > 0) ranges_.push_back({begin, begin + bytes, false});
+  }
+
   // No written buffer may overlap another one.
   void check() {
     sort();
@@ -732,7 +738,7 @@ py::tuple expert_balance(const py::object& logits, const py::object& index, doub
   for (int64_t d = 0; d + 1 < dim; ++d)
     if (choice.size(d) != z.size(d)) refuse("index must have one row for each row of the logits");
   const int64_t K = choice.size(dim - 1);
-  buffers.add(z, false);
+  buffers.add_read(z.data_ptr(), ((S * T - 1) * step + E) * z.element_size());  // with what lies between the rows
   buffers.add(choice, false);
   const uint8_t* m = nullptr;
   if (!mask.is_none()) {

@@ -217,7 +217,7 @@ def test_captured_calls_replay_like_eager():
 
 def test_refusals_on_the_device():
     z, index = (t.to(DEV) for t in case(1, 10, 8, 2))
-    z, index = z[0], index[0]
+    z, index, wide = z[0], index[0], torch.zeros(10, 20, device=DEV)
     for match, call in [
             ("score", lambda: mu.expert_balance(z, index, 1.0, "argmax")),
             ("logits must be", lambda: mu.expert_balance(z[0], index, 1.0)),
@@ -233,6 +233,7 @@ def test_refusals_on_the_device():
             ("accumulate", lambda: mu.expert_balance(z, index, 1.0, grad=True, accumulate=True)),
             ("grad_scale", lambda: mu.expert_balance(z, index, 1.0, grad_scale=torch.ones(2, device=DEV))),
             ("overlaps", lambda: mu.expert_balance(z, index, 1.0, grad=z)),
+            ("overlaps", lambda: mu.expert_balance(wide[:, :8], index, 1.0, grad=wide.flatten()[90:170].view(10, 8))),
             ("dtype", lambda: mu.expert_balance(z.double(), index, 1.0))]:
         with pytest.raises(ValueError, match=match):
             call()
