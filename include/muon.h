@@ -27,7 +27,7 @@
  *   live in device memory.  A call works on a batch of `batch` matrices of one
  *   shape rows x cols; matrix arguments are DEVICE arrays of `batch` device
  *   pointers (one per matrix), so independent tensors can be batched (the AdamW
- *   step and the microscaled code take HOST arrays, see there).  The
+ *   step, the microscaled and the 8-bit code take HOST arrays, see there).  The
  *   caller owns every buffer, including the workspace; the library allocates
  *   no device memory.  A matrix with rows > cols is iterated transposed
  *   ([GNS §1.2] works with n = min(rows, cols) <= m = max(rows, cols)); the

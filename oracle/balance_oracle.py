@@ -70,9 +70,9 @@ def tolerance(z, index, coefficient, score="softmax", mask=None):
         d = (far + E + 12) * u
         inner = (p @ f)[:, None]
         by = abs(coefficient) / (S * len(rows))
-        # what is under fp32's normal range keeps no relative accuracy: 2^-126 of each p
+        # what is under fp32's normal range keeps no relative accuracy: 2^-126 of each p, so sum f 2^-126 of <f, p>
         bound[s][mask[s]] = by * ((slope + 2.0 ** -126) * ((f + inner) * (3 * u + d + (E + 4) * u) +
-                                                          np.abs(f - inner) * (2 * d + 8 * u)) +
+                                                          np.abs(f - inner) * (2 * d + 8 * u) + f.sum() * 2.0 ** -126) +
                                   2.0 ** -126 * (f + inner)) + 2.0 ** -149
         loss_bound += abs(coefficient) / S * (inner * (d + (len(rows) + E + 8) * u)).mean()
     return loss_bound + 2.0 ** -149, bound
