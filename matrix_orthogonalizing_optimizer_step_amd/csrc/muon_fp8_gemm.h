@@ -403,6 +403,7 @@ __device__ __forceinline__ void take_tiles(const Lds<T>& lds, const Find& find, 
     if constexpr (T::kStays) {
       id += gridDim.x;
       more = find(&id, &n);
+      if (!more) n = t;  // whatever the search left there may lie behind the matrices
     }
     Stream N;
     N.start(n.A, n.B, n.ub, n.ue, wave);

@@ -450,7 +450,8 @@ def test_grouped_weight_gradient(counts, rows, fmt):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("m,n,counts", [(4100, 4099, [700, 0, 130, 1]), (2300, 2100, [700, 0, 130, 1]),
-                                        (1030, 515, [129, 3, 0, 256, 300, 128] * 12)])
+                                        (1030, 515, [129, 3, 0, 256, 300, 128] * 12),
+                                        (2100, 2100, [1] * 12 + [0])])  # no room behind the last group's units
 def test_grouped_weight_gradient_in_large_tiles(m, n, counts, dtype):
     """Every size of tiles, blocks that stay for tile after tile (odd and even numbers of units, groups without rows, tiles
     that are not full), exact; also added to C."""
