@@ -109,7 +109,7 @@ struct Fp8Plan {
 Fp8Plan fp8_plan(int batch, int m, int n, int k);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, Fp8Kind kind, hipStream_t s);
 hipError_t launch_fp8_join(const Fp8GemmArgs& a, hipStream_t s);  // the pieces' sums into C
-Fp8Kind fp8_row_group_kind(int groups, int m, int n);
+Fp8Kind fp8_row_group_kind(int groups, int m, int n, int k);
 hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStream_t s);
 Fp8Kind fp8_k_group_kind(int groups, int rows, int m, int n, bool fp32);
 hipError_t launch_fp8_k_groups(const Fp8KGroupArgs& a, Fp8Kind kind, hipStream_t s);

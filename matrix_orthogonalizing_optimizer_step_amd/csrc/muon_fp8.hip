@@ -716,7 +716,7 @@ muon_status muon_fp8_grouped_matmul(int groups, int rows, int n, int k, const in
     return MUON_ERR_INVALID_ARG;
   if (c_dtype == MUON_F16) return MUON_ERR_UNSUPPORTED;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const Fp8Kind kind = fp8_row_group_kind(groups, rows, n);
+  const Fp8Kind kind = fp8_row_group_kind(groups, rows, n, k);
   for (int at = 0; at < groups; at += kF8Groups) {
     Fp8RowGroupArgs a;
     a.count = groups - at < kF8Groups ? groups - at : kF8Groups;

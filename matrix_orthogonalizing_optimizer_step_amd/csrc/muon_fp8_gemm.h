@@ -33,6 +33,7 @@
 // are limited by power and gain nothing (8192x8192x8192 bf16 389 and 391 us).
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "muon_fp8.h"
@@ -512,6 +513,19 @@ constexpr int kBlocksPerCU = T::TM == 256 ? 1 : 2;
 template <class T>
 uint32_t blocks_of(int64_t tiles) {
   return static_cast<uint32_t>(T::kStays && tiles > kCUs ? kCUs : tiles);
+}
+
+// Whether 256 x 256 tiles take less time than 128 x 128 ones, by what was measured of
+// both (us, bf16 results; fp32 ones take 1.85 times both).  A 256 x 256 tile takes 1.42 a
+// unit and 10 that nothing of its compute unit overlaps (the first loads, the
+// results), by whole rounds of 256 tiles; where compute units are left without work
+// the others have their power, so that half of what is missing counts.  128 x 128
+// tiles, two blocks a compute unit and rounds of a quarter, take 1.77 and 6 for the
+// same area.  work: elements of C in 256 x 256; big, mid: tiles of either size.
+inline bool big_tiles_pay(double work, double big, double mid, int units, double mid_slower) {
+  const double rounds = std::ceil(big / kCUs);
+  const double big_us = (work / kCUs + rounds) / 2 * 1.42 * units + 10.0 * rounds;
+  return big_us <= (work + mid / 4) / 2 / kCUs * (1.77 * units + 6.0) * mid_slower;
 }
 
 }  // namespace fp8

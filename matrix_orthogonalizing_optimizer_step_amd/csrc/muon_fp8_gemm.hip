@@ -32,7 +32,8 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_tile_gemm_kernel(Fp8
 }
 
 // ---------------------------------------------------------------------------
-// The pieces of a product that was split along k, added in their order.
+// The pieces of a product that was split along k, added in their order.  Some 4 us
+// behind the product, most of it the launch.
 // ---------------------------------------------------------------------------
 template <int DC>
 __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs a) {
@@ -65,7 +66,9 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs a) {
 // 16 rows is two runs of 1 KB) and every NW-th unit of k, straight from memory into
 // registers, and multiplies as kExact does (16x16x32 MFMAs; memory takes longer than
 // the conversions).  The block's NW sums are added in LDS, in their order.  Rows of A
-// behind the last one repeat it and are not stored.
+// behind the last one repeat it and are not stored.  Bound by memory: 18944 x 3584 codes
+// 13.4 us, 5.0 TB/s, 100000 x 4096 78 us, 5.3 (two units ahead of 8 waves; four of 4
+// waves 16.7 us, loads past the caches slower).
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;
 constexpr int kUnitsAhead = 2;
@@ -135,9 +138,12 @@ int64_t tiles_of(int batch, int m, int n) {
 }
 
 // Pieces along k of a product in 64 x 128 tiles that leave compute units idle:
-// the fewest microseconds of a unit (two slabs, one block on a compute unit) plus,
-// for more than one piece, the joining launch and the partial sums' way through
-// memory (8 bytes an element and piece at 6 TB/s).
+// the fewest microseconds of a unit (two slabs, one block on a compute unit; 0.55 for
+// fp32 results, 0.33 for bf16, whose workspace must be the same) plus, for more than
+// one piece, the joining launch and the partial sums' way through memory (8 bytes an
+// element and piece at 6 TB/s).  Split / whole, bf16 and fp32 results (us): 64 x 3584 x
+// 18944 19 / 51, 22 / 87; 64 x 2048 x 7168 14.5 / 20, 16 / 36; 64 x 4096 x 4096 13.7 / 13.0,
+// 15 / 23; 200 x 3584 x 3584 14.1 / 12.6, 18.5 / 21.
 void split_k(int64_t tiles, int units, double elements, Fp8Plan* p) {
   constexpr int kMinUnits = 4;  // of a piece
   double best = 0.0;
@@ -181,22 +187,31 @@ void launch_few(const Fp8GemmArgs& a, hipStream_t s) {
 
 using namespace fp8;
 
+// Which kernel, by the times measured (us, bf16 results; m x n x k):
+//   few rows   up to the 16 of its MFMA: 1 x 18944 x 3584 15.3, in 64 x 128 tiles 18.1; 1 x
+//              3584 x 18944 13.4 and 19.0; 16 x 18944 x 3584 18.6 and 18.7
+//   64 x 128   where one round of them leaves nothing for larger ones: 512 x 4096 x 4096
+//              16.0, in 128 x 128 tiles 16.8, fp32 26 and 32; not 576 rows 23.5 and 17.4, fp32
+//              34 and 33
+//   128 x 128 or 256 x 256, whichever takes less (big_tiles_pay).  Measured: 8192 x 8192 x
+//              8192 477 / 391, 3584 x 7168 x 8192 207 / 193, 8192 x 7168 x 3584 199 / 193; 4864 x
+//              4608 x 8192 171 / 178, 5000 x 6656 x 2048 77 / 94, 3584 x 7168 x 2048 60 / 66,
+//              8192 x 7168 x 1024 75 / 90, 2048 x 4096 x 8192 63 / 90.  For 46 products of random
+//              sizes, in either type, the other tiles never took over 5 % less.
 Fp8Plan fp8_plan(int batch, int m, int n, int k) {
   const int units = static_cast<int>(fp8_units(k));
   Fp8Plan p{kF8FewRows, 1, units, 0};
   if (m <= kFewRows) return p;
-  const int64_t big = tiles_of<Big>(batch, m, n), low = tiles_of<Low>(batch, m, n);
-  const int64_t rounds = (big + kCUs - 1) / kCUs;
-  if (big * 3 >= rounds * kCUs * 2) {
-    p.kind = kF8Big;
-  } else if (low * 2 <= kCUs * 3) {
+  const int64_t low = tiles_of<Low>(batch, m, n);
+  if (low <= kCUs) {
     p.kind = kF8Low;
     const double elements = static_cast<double>(batch) * m * n;
     split_k(low, units, elements, &p);
     if (p.pieces > 1) p.bytes = static_cast<size_t>(p.pieces) * batch * m * n * sizeof(float);
-  } else {
-    p.kind = kF8Mid;
+    return p;
   }
+  const double big = static_cast<double>(tiles_of<Big>(batch, m, n)), mid = static_cast<double>(tiles_of<Mid>(batch, m, n));
+  p.kind = big_tiles_pay(big, big, mid, units, 1.0) ? kF8Big : kF8Mid;
   return p;
 }
 
@@ -206,6 +221,9 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, Fp8Kind kind, hipStream_t s) {
     case kF8Mid: launch_tiles<Mid>(a, s); break;
     case kF8Low: launch_tiles<Low>(a, s); break;
     default:
+      // 8 waves of a block and several blocks on a compute unit, or 16 where there is one
+      // and k is long (8 / 16 waves, us): 1 x 18944 x 3584 15.3 / 18.2; 1 x 2048 x 16384 13.5 /
+      // 10.2, 1 x 3584 x 18944 16.1 / 13.4, 1 x 4096 x 8192 9.0 / 8.1, 1 x 4096 x 4096 6.7 both
       if (a.units >= 64 && ceil_div(a.n, 16) * a.batch <= kCUs) {
         launch_few<16>(a, s);
       } else {

@@ -163,20 +163,23 @@ using namespace fp8;
 // Which tiles, for rows that are not known here but as a sum: a group's last tile row
 // is taken to be half full.  Times in us, 64 x 128 / 128 x 128 / 256 x 256 tiles, rows
 // spread unevenly:
-//   256 x 256  where that leaves at least 3/5 of their rounds on 256 compute units to
-//              real work: 64 groups, n 2048, k 7168, 16380 rows 430 / 341 / 300, 32768
-//              rows 749 / 589 / 528; not 8000 rows 275 / 254 / 270, nor 16 groups with
-//              8190 rows 170 / 137 / 160, fp32 270 / 240 / 300
+//   256 x 256  where they take less than 128 x 128 (big_tiles_pay; these are some 7 %
+//              slower here than without groups): 64 groups, n 2048, k 7168, 16380 rows 430 /
+//              341 / 300, 32768 rows 749 / 589 / 528; 8 groups, 4096, 2048, 32768 rows 425 /
+//              301 / 275; not 16 groups with 8190 rows 170 / 137 / 160, with n 7168 and k 2048
+//              205 / 152 / 160, k 1024 114 / 84 / 103; 4 groups, 8192, 4096, 4000 rows 172 /
+//              135 / 148
 //   128 x 128  from a mean of 96 rows on: those, and 8 groups, 1024 x 1024, 4096 rows 13 /
 //              12 / 20
 //   64 x 128   for fewer: 64 groups, 4000 rows 188 / 194 / 197, fp32 207 / 259 / 340, 24
 //              rows 62 / 74 / 87; 8 groups, 1024 x 1024, 600 rows 7.2 / 8.0 / 18
-Fp8Kind fp8_row_group_kind(int groups, int m, int n) {
-  const int64_t big = (static_cast<int64_t>(m) / Big::TM + (groups + 1) / 2) * ceil_div(n, Big::TN);
-  const int64_t rounds = (big + kCUs - 1) / kCUs;
+Fp8Kind fp8_row_group_kind(int groups, int m, int n, int k) {
+  if (m / groups < 96) return kF8Low;
+  const int units = static_cast<int>(fp8_units(k));
+  const double big = (m / Big::TM + (groups + 1) / 2) * static_cast<double>(ceil_div(n, Big::TN));
+  const double mid = (m / Mid::TM + (groups + 1) / 2) * static_cast<double>(ceil_div(n, Mid::TN));
   const double work = static_cast<double>(m) * n / (Big::TM * Big::TN);
-  if (work * 5 >= static_cast<double>(rounds) * kCUs * 3) return kF8Big;
-  return m / groups >= 96 ? kF8Mid : kF8Low;
+  return big_tiles_pay(work, big, mid, units, 1.07) ? kF8Big : kF8Mid;
 }
 
 hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStream_t s) {

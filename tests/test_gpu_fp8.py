@@ -256,6 +256,20 @@ def test_product_exact(dtype, batch, m, n, k):
     check_product(mu.fp8_matmul(A, B, DT[dtype]), A, B, dtype, exact=True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(4090, 3999, 2300), (4000, 4095, 2750)])
+def test_product_in_the_largest_tiles(m, n, k, dtype):
+    """A whole round of 256 x 256 tiles and k long enough for them (18 and 22 units), exact and with scales."""
+    print(dtype, m, n, k, flush=True)
+    A, B = random_code(1, m, k, 15, 127, 127, whole=True), random_code(1, n, k, 16, 127, 127, whole=True)
+    check_product(mu.fp8_matmul(A, B, DT[dtype]), A, B, dtype, exact=True)
+    A, B = random_code(1, m, k, 17, fmt="e5m2"), random_code(1, n, k, 18)
+    C0 = [torch.randn(m, n, device=DEV).to(DT[dtype])]
+    C = [C0[0].clone()]
+    mu.fp8_matmul(A, B, out=C, accumulate=True)
+    check_product(C, A, B, dtype, C0)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("batch,m,n,k", SHAPES)
 def test_product_with_scales(fmt, batch, m, n, k):
@@ -379,6 +393,22 @@ def test_grouped_product_in_larger_tiles(rows, groups, n, k):
         for e, i, j in groups_of(counts, rows):
             check(C[i:j], a[i:j], b[e], dtype, exact=True)
         assert not C[-3:].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grouped_product_in_the_largest_tiles(dtype):
+    """256 x 256 tiles, which need a long k, with an empty group and rows behind the last one: exact, and added to C."""
+    rows, n, k, counts = 7600, 2040, 1900, [2563, 0, 4900]
+    A, B = random_code(1, rows, k, 36, 127, 127, whole=True), random_code(3, n, k, 37, 127, 127, whole=True)
+    a, b = values(A)[0], values(B)
+    C0 = torch.randint(-8, 8, (rows, n), device=DEV).to(DT[dtype])
+    C, D = mu.fp8_grouped_matmul(A, B, device_counts(counts), DT[dtype])[0], [C0.clone()]
+    mu.fp8_grouped_matmul(A, B, device_counts(counts), out=D, accumulate=True)
+    for e, i, j in groups_of(counts, rows):
+        want = a[i:j] @ b[e].T  # whole numbers under 2^24, as what C holds
+        for got, w in ((C[i:j], want), (D[0][i:j], want + f64(C0[i:j]))):
+            assert np.array_equal(f64(got), f64(torch.from_numpy(w.astype(np.float32)).to(DT[dtype])))
+    assert not C[-137:].any() and torch.equal(D[0][-137:], C0[-137:])
 
 
 def test_grouped_product_with_counts_that_do_not_fit():
