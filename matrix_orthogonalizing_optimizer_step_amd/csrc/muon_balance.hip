@@ -5,7 +5,10 @@
 //   dL/dz_te = alpha / (S T_s) slope_te (f_e - <f, p_t>),
 // slope = p (softmax) or s (1 - s) / sum s (sigmoids s).  So once the counts are
 // there one pass over the logits gives both: a row's <f, p> is its share of the loss
-// and what its gradient needs; no mean of p is kept.
+// and what its gradient needs; no mean of p is kept.  Since the p of a row add up to
+// 1, d = f - min f stands in for f, made from the difference of the counts: near
+// balance, where f_e - <f, p> is a small difference, less is lost, and where all experts
+// have as many tokens the gradient is 0.
 //
 // Two launches: the choices are counted in LDS, a partial count for each block; then
 // every block adds the partial counts of its sequence up to f, takes its rows, and
@@ -99,15 +102,15 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_kernel(BalanceArg
   }
 }
 
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // quads, reversal within 8 and 16 lanes
 
 // Over L neighbouring lanes, the same result in each of them.
-template <int L, class F>
-__device__ __forceinline__ float lanes(float x, F op) {
+template <int L, class T, class F>
+__device__ __forceinline__ T lanes(T x, F op) {
   if constexpr (L >= 2) x = op(x, dpp<kXor1>(x));
   if constexpr (L >= 4) x = op(x, dpp<kXor2>(x));
   if constexpr (L >= 8) x = op(x, dpp<kHalfMirror>(x));
@@ -185,9 +188,10 @@ __device__ __forceinline__ float exp_of(float x) {
   return fmaf(e, l * kLn2, e);
 }
 
-// p of a row's logits x, and the gradient's factor slope, in place; returns <f, p>.
+// The gradient's factor slope for a row's logits x (which are used up); returns <d, p>.
+// some: whether any expert has p > 0.
 template <int L, int N>
-__device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], const float (&f)[N], bool sigmoid) {
+__device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], const float (&d)[N], bool sigmoid, bool* some) {
   float sum = 0.0f, inner = 0.0f;
   if (sigmoid) {
 #pragma unroll
@@ -198,11 +202,12 @@ __device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], co
       sum += x[e];
     }
     sum = lanes_sum<L>(sum);
+    *some = sum != 0.0f;
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       slope[e] *= inverse;
-      inner += f[e] * (x[e] * inverse);
+      inner += d[e] * (x[e] * inverse);
     }
   } else {
     float m = -INFINITY;
@@ -216,11 +221,12 @@ __device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], co
       sum += x[e];
     }
     sum = lanes_sum<L>(sum);
+    *some = sum != 0.0f;
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       slope[e] = x[e] * inverse;
-      inner += f[e] * slope[e];
+      inner += d[e] * slope[e];
     }
   }
   return lanes_sum<L>(inner);
@@ -244,13 +250,23 @@ __device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* 
   constexpr int N = NV * kElems;
   const int o = threadIdx.x % L, E = a.experts, tokens = bins[E];
   const float unit = tokens > 0 ? static_cast<float>(E) / (static_cast<float>(a.top) * static_cast<float>(tokens)) : 0.0f;
-  float f[N];
+  int least = INT32_MAX;  // count of an expert
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < kElems; ++e) {
+      const int c = kElems * (o + L * v) + e, n = c < E ? bins[c] : INT32_MAX;
+      least = n < least ? n : least;
+    }
+  least = lanes<L>(least, [](int p, int q) { return p < q ? p : q; });
+  const float all = static_cast<float>(least) * unit;  // of f, in every expert's
+  float d[N];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < kElems; ++e) {
       const int c = kElems * (o + L * v) + e;
-      f[v * kElems + e] = c < E ? static_cast<float>(bins[c]) * unit : 0.0f;
+      d[v * kElems + e] = c < E ? static_cast<float>(bins[c] - least) * unit : 0.0f;
     }
   const float by = tokens > 0 ? scale / static_cast<float>(tokens) : 0.0f;  // of the gradient
   float total = 0.0f;
@@ -262,10 +278,11 @@ __device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* 
     float next[N], g[N];
     if (valid_after) load_row<D, L, NV>(a, after, next);
     if (valid) {
-      const float inner = row_scores<L>(x, g, f, a.sigmoid != 0);
-      if (o == 0) total += inner;
+      bool some;
+      const float inner = row_scores<L>(x, g, d, a.sigmoid != 0, &some);
+      if (o == 0) total += some ? all + inner : 0.0f;
 #pragma unroll
-      for (int e = 0; e < N; ++e) g[e] *= (f[e] - inner) * by;
+      for (int e = 0; e < N; ++e) g[e] *= (d[e] - inner) * by;
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) g[e] = 0.0f;
@@ -429,8 +446,9 @@ Plan plan_of(int sequences, int tokens, int experts, int top) {
   const int64_t limit = sequences < 8 ? 48 : 8;
   count_blocks = count_blocks > limit ? limit : count_blocks;
   int64_t blocks = (tokens + per - 1) / per;
-  // one block a compute unit: all of them count themselves as done at one address,
-  // 1024 blocks of a quarter of the threads took 25 us where these take 10
+  // one block a compute unit: all of them count themselves as done at one address.
+  // 1024 blocks of a quarter of the threads take 25 us for 32768 x 256 bf16 where these
+  // take 18, and 19 instead of 11 for 16 x 2049 x 61
   const int64_t most = sequences < 256 ? 256 / sequences : 1;
   blocks = blocks > most ? most : blocks;
   return Plan{static_cast<int>(count_blocks), static_cast<int>(blocks)};

@@ -91,6 +91,16 @@ def test_masks_and_rows_that_do_not_count(S, T, E, K):
         assert torch.equal(G[~mask.to(DEV)].cpu(), G0[~mask])
 
 
+@pytest.mark.parametrize("S,T,E", [(1, 5, 8), (1, 1, 1), (3, 300, 61), (1, 3000, 520), (2, 4100, 3)])
+def test_all_experts_alike(S, T, E):
+    """As many tokens for every expert: f is the same for all, so the gradient is 0, whatever the logits, and the loss 1."""
+    z, _ = case(S, T, E, 1, "f32", 12, 5.0)
+    index = torch.arange(E).expand(S, T, E).contiguous()
+    for score in ("softmax", "sigmoid"):
+        loss, counts, grad = mu.expert_balance(z.to(DEV), index.to(DEV), 1.0, score, grad=True)
+        assert abs(float(loss) - 1.0) <= (T + 8) * 2.0 ** -24 and (counts == S * T).all() and not grad.any()
+
+
 def test_nothing_counts():
     z, index = case(3, 50, 16, 2)
     for T in (2, 50):
