@@ -505,7 +505,7 @@ muon_status muon_mx4_matmul(int batch, int m, int n, int k,
  * muon_fp8_dequantize writes the values of a code (without groups) as F32 or BF16,
  * both exact down to 2^-133; smaller values are rounded to the type.
  */
-typedef enum { MUON_E4M3 = 0, MUON_E5M2 = 1, MUON_FP8_FORMAT_RANGE_ = 0x7fffffff } muon_fp8_format;
+typedef enum { MUON_E4M3 = 0, MUON_E5M2 = 1, MUON_FP8_FORMAT_RANGE_ = -0x7fffffff - 1 } muon_fp8_format;
 
 muon_status muon_fp8_quantize(int batch, int rows, int cols, const void *const *X, muon_dtype x_dtype,
                               int tile, muon_fp8_format format, const int32_t *counts, int groups,
@@ -598,7 +598,7 @@ muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, con
  * rows x top must be under 2^31, sequences at most 65535.
  */
 #define MUON_MAX_EXPERTS 1024
-typedef enum { MUON_SOFTMAX = 0, MUON_SIGMOID = 1, MUON_EXPERT_SCORE_RANGE_ = 0x7fffffff } muon_expert_score;
+typedef enum { MUON_SOFTMAX = 0, MUON_SIGMOID = 1, MUON_EXPERT_SCORE_RANGE_ = -0x7fffffff - 1 } muon_expert_score;
 
 size_t muon_expert_balance_workspace_size(int sequences, int tokens, int experts, int top);
 muon_status muon_expert_balance(int sequences, int tokens, int experts, int top,
