@@ -95,8 +95,16 @@ typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 // pieces of rows.  LDS holds C's type, or fp32 where C is added to: C is rounded
 // once.  Measured on 8192x7168x3584 against 8-byte stores of 32 rows at a time
 // straight from the accumulators: 138 -> 122 us.  XS: columns of MFMA tiles that are
-// staged together (the LDS takes 32 rows of them).
-template <class T, int DC, bool ADD, int XS = T::FN>
+// staged together (the LDS takes 32 rows of them).  FULL: all of the wave's rows and
+// columns are there.
+//
+// Where C is added to, full tiles have what is there on its way kAhead steps ahead of
+// its use: loads and stores end in order, so a load behind the stores of the rows before
+// would wait for those.  (us, us without: 8-bit products' fp32 G of 16 experts of
+// 2048x7168, 8190 rows, 436 / 730, 8192x8192x2048 278 / 358; 4-bit 3584x7168x8192 126 /
+// 153.)  Not for bf16 in 256 x 256 tiles: there it takes registers that the products need
+// (16 experts 319 / 436, but 274 / 241 where C is not added to).
+template <class T, int DC, bool ADD, int XS = T::FN, bool FULL = false>
 __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
                                            int m, int n, int lane) {
   constexpr int kSize = DC == kF32 ? 4 : 2, kHeld = ADD || DC == kF32 ? 4 : 2;  // bytes of an element of C, in LDS
@@ -105,10 +113,32 @@ __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN]
   static_assert(T::FN % XS == 0 && 32 * kPitch * 16 <= sizeof(typename T::Stage) && kLanes <= 64, "staging");
   const int row = lane & 31, half = lane >> 5, r0 = lane / kLanes, chunk = lane % kLanes;
   constexpr int kElems = 16 / kSize;
+  if constexpr (ADD && !FULL && (DC == kF32 || T::FM * T::FN < 16)) {
+    if (i + 32 * T::FM <= m && j + 32 * T::FN <= n) {
+      store_tile<T, DC, ADD, XS, true>(C, acc, stage, i, j, m, n, lane);
+      return;
+    }
+  }
+  constexpr int kSteps = T::FM * (T::FN / XS), kLoads = 32 / kRows, kAhead = kLoads < 12 ? 12 / kLoads : 1;
+  u32x4_t was[ADD && FULL ? kSteps : 1][kLoads];
+  const auto load = [&](int yx) {
+    const int y = yx / (T::FN / XS), x0 = yx % (T::FN / XS) * XS;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int64_t at = static_cast<int64_t>(i + 32 * y + q * kRows + r0) * n + j + 32 * x0 + chunk * kElems;
+      was[yx][q] = *reinterpret_cast<const u32x4_a2*>(static_cast<const char*>(C) + at * kSize);
+    }
+  };
+  if constexpr (ADD && FULL) {
+#pragma unroll
+    for (int yx = 0; yx < kAhead && yx < kSteps; ++yx) load(yx);
+  }
 #pragma unroll
   for (int yx = 0; yx < T::FM * (T::FN / XS); ++yx) {
     const int y = yx / (T::FN / XS), x0 = yx % (T::FN / XS) * XS;
     const int jc = j + 32 * x0 + chunk * kElems;
+    if constexpr (ADD && FULL)
+      if (yx + kAhead < kSteps) load(yx + kAhead);
 #pragma unroll
     for (int x = 0; x < XS; ++x)
 #pragma unroll
@@ -128,7 +158,7 @@ __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN]
 #pragma unroll
     for (int q = 0; q < 32 / kRows; ++q) {
       const int r = q * kRows + r0, ir = i + 32 * y + r;
-      if (ir < m && jc < n) {
+      if (FULL || (ir < m && jc < n)) {
         char* const p = static_cast<char*>(C) + (static_cast<int64_t>(ir) * n + jc) * kSize;
         float f[kElems];
         uint4 h;
@@ -141,10 +171,15 @@ __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN]
         } else {
           h = stage[r * kPitch + chunk];
         }
-        if (jc + kElems <= n) {
+        if (FULL || jc + kElems <= n) {
           if constexpr (kHeld == 4) {
             if constexpr (ADD) {
-              const u32x4_t c = *reinterpret_cast<const u32x4_a2*>(p);
+              u32x4_t c;
+              if constexpr (FULL) {
+                c = was[yx][q];
+              } else {
+                c = *reinterpret_cast<const u32x4_a2*>(p);
+              }
 #pragma unroll
               for (int e = 0; e < kElems; ++e)
                 f[e] += DC == kF32 ? __uint_as_float(c[e & 3])
