@@ -546,7 +546,8 @@ muon_status muon_fp8_matmul(int batch, int m, int n, int k,
  * whose tokens lie behind one another): C[rows of g] = A[rows of g] B_g^T, or +=.
  * A is rows x k (one matrix, coded along its rows), B_g n x k, C rows x n.
  *   counts      device array of `groups` row counts, read by the kernels; as for
- *               muon_fp8_quantize (no bound on rows / 128 + groups).
+ *               muon_fp8_quantize (no bound on rows / 128 + groups).  Rows in no group
+ *               (those that muon_expert_balance does not count) come behind the last one.
  *   clear_rest  0: rows of C behind the last group are left as they were; 1: they
  *               become 0.
  * One launch per 128 groups.  No workspace.

@@ -928,7 +928,8 @@ def fp8_workspace_size(batch: int, m: int, n: int, k: int) -> int:
 def fp8_grouped_matmul(A: FP8, B: FP8, counts, dtype=torch.bfloat16, out=None, accumulate: bool = False, stream=None):
     """The product over experts: ``A`` is one matrix whose rows are sorted by expert, ``counts`` an int32 device tensor of
     the rows of each (as expert_balance gives it), ``B`` one n x k matrix for each expert: C[rows of e] = A[rows of e]
-    B_e^T, a list of one matrix.  Rows behind the last expert's are 0 in a new C and left as they are in ``out``."""
+    B_e^T, a list of one matrix.  Rows that the counts leave out (of masked tokens, of choices outside the experts) come
+    behind the last expert's: they are 0 in a new C and left as they are in ``out``."""
     status, C = _fp8_call("fp8_grouped_matmul", stream, A.codes, A._args(), B._args(), counts, dtype, out, accumulate)
     if status:
         _check(status)
@@ -960,7 +961,8 @@ def expert_balance(logits, index, coefficient: float, score: str = "softmax", ma
 
     ``grad``: None, True (a new tensor) or a tensor of the logits' shape and type to write dloss/dlogits into, with
     ``accumulate`` to add it to; ``grad_scale``: None or a one-element float32 device tensor it is multiplied with.
-    ``loss`` is a float32 scalar, ``counts`` int32, over all sequences."""
+    ``loss`` is a float32 scalar, ``counts`` int32, over all sequences, without masked tokens and choices that are not
+    counted: what is sorted by expert for the products over experts has those rows behind the last expert's."""
     if score not in ("softmax", "sigmoid"):
         raise ValueError('score must be "softmax" or "sigmoid"')
     status, loss, counts, g = _fp8_call("expert_balance", stream, (logits,), logits, index, coefficient, score == "sigmoid",
