@@ -580,8 +580,7 @@ muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, con
  * A whole batch balanced as one is sequences = 1.
  *   logits    row r at logits + r row_stride elements (z_dtype F32, BF16 or F16);
  *             -infinity takes an expert out of a row, and a row without any
- *             expert has p = 0.  NaN propagates.  Sigmoids that all are under fp32's
- *             range count as 0.
+ *             expert has p = 0.  NaN propagates.
  *   index     contiguous, index_bits 32 or 64.  An index outside 0 .. experts - 1 is a
  *             choice that is not counted; one that is there twice counts twice.
  *   mask      NULL, or a byte for each row: rows with 0 (padding) do not count, their

@@ -191,11 +191,19 @@ __device__ __forceinline__ float exp_of(float x) {
   return fmaf(e, l * kLn2, e);
 }
 
+// Sigmoids that add up to less than this leave fp32's range, or are about to (2^-126 is
+// nothing beside it): every logit is under -44, where 1 + e^z is 1 and p the softmax, each
+// to 2^-64 of itself.
+constexpr float kSmallSum = 0x1p-64f;
+
 // The gradient's factor slope for a row's logits x (which are used up); returns <d, p>.
-// some: whether any expert has p > 0.
+// some: whether any expert has p > 0.  small: the sigmoids are too small, nothing else is
+// set (p is the softmax).
 template <int L, int N>
-__device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], const float (&d)[N], bool sigmoid, bool* some) {
+__device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], const float (&d)[N], bool sigmoid, bool* some,
+                                            bool* small) {
   float sum = 0.0f, inner = 0.0f;
+  *small = false;
   if (sigmoid) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -205,8 +213,9 @@ __device__ __forceinline__ float row_scores(float (&x)[N], float (&slope)[N], co
       sum += x[e];
     }
     sum = lanes_sum<L>(sum);
-    *some = sum != 0.0f;
-    const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *some = true;
+    *small = sum < kSmallSum;
+    const float inverse = 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       slope[e] *= inverse;
@@ -281,8 +290,12 @@ __device__ __forceinline__ float take_rows(const BalanceArgs& a, const int32_t* 
     float next[N], g[N];
     if (valid_after) load_row<D, L, NV>(a, after, next);
     if (valid) {
-      bool some;
-      const float inner = row_scores<L>(x, g, d, a.sigmoid != 0, &some);
+      bool some, small;
+      float inner = row_scores<L>(x, g, d, a.sigmoid != 0, &some, &small);
+      if (small) {  // the same in all lanes of a row
+        load_row<D, L, NV>(a, r, x);
+        inner = row_scores<L>(x, g, d, false, &some, &small);
+      }
       if (o == 0) total += some ? all + inner : 0.0f;
 #pragma unroll
       for (int e = 0; e < N; ++e) g[e] *= (d[e] - inner) * by;
