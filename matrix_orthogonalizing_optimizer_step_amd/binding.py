@@ -710,7 +710,8 @@ def _on_stream(stream, tensors):
 def _call(entry: str, stream, tensors, *args):
     """Calls an entry of the extension module on ``stream`` (None = the current stream of the tensors' device)."""
     f = getattr(_native or _load_native(), entry)
-    if stream is None:
+    first = tensors[0] if isinstance(tensors, (list, tuple)) and tensors else None
+    if stream is None or not isinstance(first, torch.Tensor) or not first.is_cuda:  # what has no device is refused there
         return f(*args)
     with _on_stream(stream, tensors):
         return f(*args)
