@@ -525,8 +525,8 @@ muon_status muon_fp8_dequantize(int batch, int rows, int cols, const void *const
  * under 2^-133 are rounded to bf16's subnormals, those over its range infinite).
  *   BF16 results of more than 16 rows take the 8-bit matrix instruction, twice as
  * fast, which adds eight neighbouring products at a time to 13 bits below the
- * largest of the eight, and those sums in fp32: some 2^-16 of a normal sum off,
- * where BF16 rounds to 2^-9.
+ * largest of the eight, and those sums in fp32: 2^-16 of the sums off on normal data
+ * (root mean square), where BF16 rounds by up to 2^-8.
  *
  *   workspace  device buffer of at least muon_fp8_workspace_size() bytes, 256-byte
  *              aligned; contents on entry are ignored.  Calls that share it
@@ -550,7 +550,8 @@ muon_status muon_fp8_matmul(int batch, int m, int n, int k,
  *               (those that muon_expert_balance does not count) come behind the last one.
  *   clear_rest  0: rows of C behind the last group are left as they were; 1: they
  *               become 0.
- * One launch per 128 groups.  No workspace.
+ * One launch per 128 groups.  No workspace.  All BF16 results, of few rows too, take the
+ * 8-bit matrix instruction (muon_fp8_matmul); F32 results add exact products.
  */
 muon_status muon_fp8_grouped_matmul(int groups, int rows, int n, int k, const int32_t *counts,
                                     const void *A_codes, const void *A_scales, muon_fp8_format a_format,
@@ -561,7 +562,8 @@ muon_status muon_fp8_grouped_matmul(int groups, int rows, int n, int k, const in
  * Their weight gradients, the product along groups of k: C_g = A_g B_g^T, or +=,
  * C_g m x n.  A and B are the columns' codes of a rows x m and a rows x n matrix
  * (of the output gradient and of the input), made by muon_fp8_quantize with the
- * same counts.  A group without rows gives zeros (or leaves C_g as it is).
+ * same counts.  A group without rows gives zeros (or leaves C_g as it is).  Accuracy as
+ * for muon_fp8_grouped_matmul.
  */
 muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, const int32_t *counts,
                                          const void *A_codes, const void *A_scales, muon_fp8_format a_format,
@@ -593,9 +595,9 @@ muon_status muon_fp8_grouped_weight_grad(int groups, int rows, int m, int n, con
  *   workspace device buffer of at least muon_expert_balance_workspace_size() bytes,
  *             256-byte aligned; contents on entry are ignored.  Calls that share it
  *             must not overlap.
- * Sums are fp32 over a block's rows and fp64 over blocks.  Results do not depend on
- * timing.  muon_expert_balance_workspace_size returns 0 for invalid arguments: rows and
- * rows x top must be under 2^31, sequences at most 65535.
+ * Sums are fp32 over a row and over the rows that one thread takes, fp64 from there on.
+ * Results do not depend on timing.  muon_expert_balance_workspace_size returns 0 for
+ * invalid arguments: rows and rows x top must be under 2^31, sequences at most 65535.
  */
 #define MUON_MAX_EXPERTS 1024
 typedef enum { MUON_SOFTMAX = 0, MUON_SIGMOID = 1, MUON_EXPERT_SCORE_RANGE_ = -0x7fffffff - 1 } muon_expert_score;

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon.so")
 SOURCES = ["muon_gemm_bf16.hip", "muon_gemm_f16.hip", "muon_gemm_f32.hip", "muon_gemm.hip",
            "muon_elementwise.hip", "muon_grasp.hip", "muon_adamw.hip", "muon_mx4.hip", "muon_mx4_gemm.hip",
-           "muon_fp8.hip", "muon_fp8_gemm.hip", "muon_fp8_groups.hip", "muon_balance.hip", "muon_api.hip", "muon_schedule.cpp", "muon_ceiling.hip"]
+           "muon_fp8.hip", "muon_fp8_gemm.hip", "muon_fp8_groups.hip", "muon_balance.hip", "muon_api.hip",
+           "muon_schedule.cpp", "muon_ceiling.hip"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

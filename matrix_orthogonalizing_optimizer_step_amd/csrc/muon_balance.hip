@@ -13,10 +13,12 @@
 // Two launches: the choices are counted in LDS, a partial count for each block; then
 // every block adds the partial counts of its sequence up to f, takes its rows, and
 // the last block to finish adds the blocks' sums in their order, so results do not
-// depend on timing.  Small calls do all of it in one block and one launch (6.2 us).
-// 32768 x 256 bf16 with the gradient: counts 4 us, rows 18, of which the logits' and the
-// gradient's way through memory is 5, the arithmetic 9 (16 instructions an element) and
-// the wait for the last block's sum 4.
+// depend on timing.  Small calls do all of it in one block and one launch (5.5 us).
+// 32768 x 256 bf16 with the gradient: counts 4 us, rows 18 to 20.  Those issue 39 vector
+// instructions an element (counted; with the counts' sums and the reductions over a row),
+// which alone would take 8.6 us, the logits' and the gradient's way through memory 5.
+// 16 x 2049 x 61 fp32 sigmoid, padded to 64: 86 an element, 4.8 us, of 12.  The rest is
+// waiting: four waves a SIMD, the reductions' chains, the last block's sum.
 //
 // The blocks' sums are all that passes from block to block within a launch.  They go
 // by agent-scope atomic stores, which write through to memory, and are waited for
@@ -455,10 +457,19 @@ struct Plan {
 Plan plan_of(int sequences, int tokens, int experts, int top) {
   const int64_t rows = static_cast<int64_t>(sequences) * tokens;
   const int lanes = lanes_of(experts);
+  // one block / two launches, us: 7 x 8, top 2, 5.6 / 8.7; 512 x 8, top 2, 5.7 / 9.4; 128 x 64,
+  // top 6, 7.4 / 10.6; 32 x 256, top 8, 8.1 / 11.5; 16 x 1024, top 8, 11.8 / 12.1; past the bounds
+  // 2048 x 8, top 1, 9.3 / 10.4; 512 x 64, top 2, 15.8 / 10.9; 32 x 1024, top 8, 17.4 / 12.2.
+  // Sequences are taken one after the other: 2 x 64 x 64, top 6, 9.2 / 9.6, but 4 x 8 x 64
+  // 12.8 / 9.5; 8 x 8 x 8, top 2, 19.3 / 9.5
   if (rows * top <= 4 * kSmallThreads && rows <= 4 * kSmallThreads / lanes && sequences <= 4) return Plan{0, 1};
   const int per = (experts > 64 * kElems ? kThreads / 2 : kThreads) / lanes;  // rows of a block at a time
   const int64_t entries = static_cast<int64_t>(tokens) * top;
   int64_t count_blocks = (entries + 2047) / 2048;  // two rounds of loads of a thread
+  // and few enough that every block can add them up (at most 8 / 16 / 48 a sequence, us, top
+  // 6, bf16): 32768 x 64 17.0 / 16.0 / 15.0, 131072 x 64 33 / 26 / 21, 2 x 65536 x 64 26 / 23 / 20, 7 x
+  // 32768 x 64 26.6 / 25.6 / 25.3, 8 x 32768 x 64 27.6 / 26.8 / 26.4, 16 x 16384 x 64 26.5 / 26.2 /
+  // 27.6; up to 8192 tokens a sequence within 0.5 of each other
   const int64_t limit = sequences < 8 ? 48 : 8;
   count_blocks = count_blocks > limit ? limit : count_blocks;
   int64_t blocks = (tokens + per - 1) / per;

@@ -24,19 +24,27 @@
 // A slab's fragments are read into registers while the MFMAs of the slab before
 // run, so that behind the one barrier of a slab its stage can be filled anew.
 //
-// 256 x 256 tiles are bound by power: 4096 x 4096 x 18944 of normal numbers 238 us, 2.66
-// PFLOP/s, of zeros 165 us, 3.85.  8192 x 8192 x 8192 391 us, 2.81 PFLOP/s, with fp32 results
-// 755 us, 1.46.  128 x 128 tiles, two blocks a compute unit, read LDS for half as many
-// products: 2048 x 4096 x 8192 61 us, 2.25 PFLOP/s.  64 x 128 tiles wait for loads and
-// barriers, 0.33 us a unit (fp32 results 0.55).
+// 256 x 256 tiles are bound by power: 4096 x 4096 x 18944 of normal numbers 216 us, 2.94
+// PFLOP/s, of zeros 158 us, 4.02 (another time 238 and 165).  8192 x 8192 x 8192 394 us,
+// 2.79 PFLOP/s, with fp32 results 756 us, 1.45.  128 x 128 tiles, two blocks a compute unit,
+// read LDS for half as many products: 2048 x 4096 x 8192 59 us, 2.34 PFLOP/s.  64 x 128 tiles
+// wait for loads and barriers, 0.33 us a unit (fp32 results 0.55).  The kernels of 256 x 256
+// tiles with bf16 results spill 32 to 48 registers, the one whose blocks stay 11, none of
+// them within the loop over slabs.
+//
+// Times beside the rules that choose between tiles: medians of 7 turns of 20 calls, the
+// sides in turn on one card (turns within 3 % of each other).  In one row of calls a kernel
+// that is bound by power starts as fast, is up to a quarter slower about the tenth to the
+// twentieth call, and settles between: 16380 rows over 64 experts 265, 360, then 300 us.
 //
 // Blocks that fill a compute unit can stay for tile after tile: what they load runs 4
 // slabs ahead of what they multiply, over the end of a tile into the next one, whose
 // first slabs are there when a tile's results have gone.  A tile takes whole rounds of
 // the ring: behind an odd number of units two slabs are loaded for nothing.  That pays
 // where k is short against the results: the weight gradients of 16 experts of 2048 x
-// 7168 with 8190 rows in all take 350 us so and 387 with a block a tile.  Long products
-// are limited by power and gain nothing (8192x8192x8192 bf16 389 and 391 us).
+// 7168 with 8190 rows in all take 334 us so and 350 with a block a tile (with as many rows
+// for every expert 296 and 356).  Long products are limited by power and gain nothing
+// (8192x8192x8192 bf16 389 and 391 us).
 #pragma once
 
 #include <cmath>
@@ -48,7 +56,6 @@
 namespace muon {
 namespace fp8 {
 
-constexpr int kStages = 4;
 constexpr bool kFast = false, kExact = true;
 
 template <int TM_, int TN_, int WM_, bool STAYS = false>

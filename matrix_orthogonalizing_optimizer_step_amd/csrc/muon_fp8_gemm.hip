@@ -138,12 +138,14 @@ int64_t tiles_of(int batch, int m, int n) {
 }
 
 // Pieces along k of a product in 64 x 128 tiles that leave compute units idle:
-// the fewest microseconds of a unit (two slabs, one block on a compute unit; 0.55 for
-// fp32 results, 0.33 for bf16, whose workspace must be the same) plus, for more than
-// one piece, the joining launch and the partial sums' way through memory (8 bytes an
-// element and piece at 6 TB/s).  Split / whole, bf16 and fp32 results (us): 64 x 3584 x
-// 18944 19 / 51, 22 / 87; 64 x 2048 x 7168 14.5 / 20, 16 / 36; 64 x 4096 x 4096 13.7 / 13.0,
-// 15 / 23; 200 x 3584 x 3584 14.1 / 12.6, 18.5 / 21.
+// the fewest microseconds of units (two slabs, one block on a compute unit) plus, for
+// more than one piece, the joining launch and the partial sums' way through memory (8
+// bytes an element and piece at 6 TB/s).  One time of a unit stands for both types (0.55
+// for fp32 results, 0.33 for bf16): the plan, like the workspace query, does not know C's
+// type.  So fp32 results always gain, and bf16 ones lose where a split saves little.
+// Split / whole, bf16 and fp32 results (us): 64 x 3584 x 18944 19 / 51, 21 / 86; 64 x 2048 x
+// 7168 14.5 / 19.2, 15.8 / 35; 64 x 4096 x 4096 13.6 / 12.8, 14.8 / 22; 200 x 3584 x 3584 14.3 /
+// 11.9, 18.4 / 20.4; 93 x 1875 x 2233 bf16 12.0 / 9.0.
 void split_k(int64_t tiles, int units, double elements, Fp8Plan* p) {
   constexpr int kMinUnits = 4;  // of a piece
   double best = 0.0;
@@ -188,16 +190,21 @@ void launch_few(const Fp8GemmArgs& a, hipStream_t s) {
 using namespace fp8;
 
 // Which kernel, by the times measured (us, bf16 results; m x n x k):
-//   few rows   up to the 16 of its MFMA: 1 x 18944 x 3584 15.3, in 64 x 128 tiles 18.1; 1 x
-//              3584 x 18944 13.4 and 19.0; 16 x 18944 x 3584 18.6 and 18.7
+//   few rows   up to the 16 of its MFMA: 1 x 18944 x 3584 13.6, in 64 x 128 tiles 13.9; 1 x
+//              3584 x 18944 12.8 and 17.4; 16 x 18944 x 3584 12.8 and 13.4
 //   64 x 128   where one round of them leaves nothing for larger ones: 512 x 4096 x 4096
-//              16.0, in 128 x 128 tiles 16.8, fp32 26 and 32; not 576 rows 23.5 and 17.4, fp32
-//              34 and 33
+//              14.9, in 128 x 128 tiles 15.8, fp32 23.5 and 29.6; not 576 rows 24.0 and 16.3,
+//              fp32 32 and 30
 //   128 x 128 or 256 x 256, whichever takes less (big_tiles_pay).  Measured: 8192 x 8192 x
-//              8192 477 / 391, 3584 x 7168 x 8192 207 / 193, 8192 x 7168 x 3584 199 / 193; 4864 x
-//              4608 x 8192 171 / 178, 5000 x 6656 x 2048 77 / 94, 3584 x 7168 x 2048 60 / 66,
-//              8192 x 7168 x 1024 75 / 90, 2048 x 4096 x 8192 63 / 90.  For 46 products of random
-//              sizes, in either type, the other tiles never took over 5 % less.
+//              8192 451 / 394, 3584 x 7168 x 8192 189 / 182, 4096 x 3584 x 18944 240 / 204; 4864 x
+//              4608 x 8192 163 / 180, 5000 x 6656 x 2048 71 / 92, 3584 x 7168 x 2048 55 / 63,
+//              8192 x 7168 x 1024 66 / 87, 2048 x 4096 x 8192 59 / 82.  Near the border either may
+//              lead by some percent, by card (8192 x 7168 x 3584, in 256 x 256: 186 / 195, on
+//              another 199 / 193).  Of 46 products of random sizes, in either type, what is
+//              chosen takes 2 % over the best at most in nine of ten, 6 % at the worst; of 24
+//              of up to 1500 rows 7 and 33 % (bf16 ones that are split, above).
+// None of the rules knows whether C is added to.  bf16 C in 256 x 256 tiles is read in
+// place then: += 8192 x 8192 x 2048 141 / 178 (fp32 268 / 285), 8192 x 8192 x 8192 461 / 452.
 Fp8Plan fp8_plan(int batch, int m, int n, int k) {
   const int units = static_cast<int>(fp8_units(k));
   Fp8Plan p{kF8FewRows, 1, units, 0};
@@ -222,8 +229,8 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs& a, Fp8Kind kind, hipStream_t s) {
     case kF8Low: launch_tiles<Low>(a, s); break;
     default:
       // 8 waves of a block and several blocks on a compute unit, or 16 where there is one
-      // and k is long (8 / 16 waves, us): 1 x 18944 x 3584 15.3 / 18.2; 1 x 2048 x 16384 13.5 /
-      // 10.2, 1 x 3584 x 18944 16.1 / 13.4, 1 x 4096 x 8192 9.0 / 8.1, 1 x 4096 x 4096 6.7 both
+      // and k is long (8 / 16 waves, us): 1 x 18944 x 3584 13.1 / 15.1, 16 x 18944 x 3584 12.7 /
+      // 15.4; 1 x 2048 x 16384 9.7 / 8.5, 1 x 3584 x 18944 12.5 / 12.4, 1 x 4096 x 8192 6.9 both
       if (a.units >= 64 && ceil_div(a.n, 16) * a.batch <= kCUs) {
         launch_few<16>(a, s);
       } else {

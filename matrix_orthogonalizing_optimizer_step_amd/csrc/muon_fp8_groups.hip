@@ -31,8 +31,9 @@ __device__ __forceinline__ void read_counts(Counts& c, const int32_t* counts, in
 
 // As many row tiles as there are at most are launched; a block finds its group by a
 // scan of the counts, and those behind the last tile end at once.  Few rows are bound by
-// the weights: 24 rows, 64 groups of 2048 x 7168 65 us, 5.0 TB/s.  Many are bound by power
-// and by tiles that are not full: 16380 rows 308 us, 1.56 PFLOP/s.
+// the weights: 24 rows, 64 groups of 2048 x 7168 62 to 65 us, 5.0 TB/s.  Many are bound by
+// power and by tiles that are not full: 16380 rows 282 us, 1.71 PFLOP/s; with as many rows in
+// every group, so that all tiles are full, 226.
 template <class T, int FA, bool EXACT>
 __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp8RowGroupArgs a, int tn) {
   FP8_LDS(T);
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_row_groups_kernel(Fp
 
 // k of a group is its rows, in whole units; the last one is filled up with zero codes.
 // Bound by the products (fp32 results: converted codes at half the rate) and, k being
-// short, by the results' way to memory: 16 groups of 2048 x 7168, 8190 rows, fp32 350 us
+// short, by the results' way to memory: 16 groups of 2048 x 7168, 8190 rows, fp32 334 us
 // for 940 MB of results.
 template <class T, int FA, bool EXACT>
 __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8KGroupArgs a, int tm, int tn, int ids) {
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(256, kBlocksPerCU<T>) void fp8_k_groups_kernel(Fp8K
   __syncthreads();
   // consecutive ids go to the 8 XCDs in turn: each gets a contiguous eighth of every
   // group's tiles, since groups take very different times (with whole groups to an
-  // XCD, 16 of 2048 x 7168 with 8190 rows in all took 524 us, so 387)
+  // XCD, 16 of 2048 x 7168 with 8190 rows in all took 524 us, so 387 then)
   const int per = tm * tn, share = (per + 7) >> 3;
   if (!a.accumulate)
     for (int e0 = 0; e0 < a.count; e0 += 64)
@@ -170,15 +171,21 @@ using namespace fp8;
 // is taken to be half full.  Times in us, 64 x 128 / 128 x 128 / 256 x 256 tiles, rows
 // spread unevenly:
 //   256 x 256  where they take less than 128 x 128 (big_tiles_pay; these are some 7 %
-//              slower here than without groups): 64 groups, n 2048, k 7168, 16380 rows 430 /
-//              341 / 300, 32768 rows 749 / 589 / 528; 8 groups, 4096, 2048, 32768 rows 425 /
-//              301 / 275; not 16 groups with 8190 rows 170 / 137 / 160, with n 7168 and k 2048
-//              205 / 152 / 160, k 1024 114 / 84 / 103; 4 groups, 8192, 4096, 4000 rows 172 /
-//              135 / 148
-//   128 x 128  from a mean of 96 rows on: those, and 8 groups, 1024 x 1024, 4096 rows 13 /
-//              12 / 20
-//   64 x 128   for fewer: 64 groups, 4000 rows 188 / 194 / 197, fp32 207 / 259 / 340, 24
-//              rows 62 / 74 / 87; 8 groups, 1024 x 1024, 600 rows 7.2 / 8.0 / 18
+//              slower here than without groups): 64 groups, n 2048, k 7168, 16380 rows 419 /
+//              342 / 282, 32768 rows 769 / 587 / 518; 8 groups, 4096, 2048, 32768 rows 412 /
+//              309 / 277; not 16 groups with 8190 rows 170 / 138 / 154, with n 7168 and k 2048
+//              195 / 152 / 159, k 1024 111 / 83 / 103; 4 groups, 8192, 4096, 4000 rows 180 /
+//              133 / 148
+//   128 x 128  from a mean of 96 rows on: those, and 8 groups, 1024 x 1024, 4096 rows 14 /
+//              12 / 19
+//   64 x 128   for fewer: 64 groups, 24 rows 62 / 70 / 77; 8 groups, 1024 x 1024, 600 rows
+//              6.9 / 7.9 / 17; 64 groups, 4000 rows 186 / 193 / 181, fp32 219 / 230 / 307, spread
+//              otherwise 183 / 170 / 178, fp32 215 / 208 / 299, with as many in every group
+//              173 / 180 / 192, fp32 189 / 205 / 293
+// How the rows are spread decides as much as their sum (16 groups of 7168 x 2048 with as
+// many in each 155 / 131 in 128 x 128 / 256 x 256).  Of 30 random sizes and spreads what is
+// chosen takes the best time at the median, 15 % over it in one of ten, 28 % at the worst
+// (few tiles of 128 x 128: 2 groups, 670 rows, 1704 x 5751 fp32 31 / 40 / 109).
 Fp8Kind fp8_row_group_kind(int groups, int m, int n, int k) {
   if (m / groups < 96) return kF8Low;
   const int units = static_cast<int>(fp8_units(k));
@@ -197,16 +204,21 @@ hipError_t launch_fp8_row_groups(const Fp8RowGroupArgs& a, Fp8Kind kind, hipStre
   return hipGetLastError();
 }
 
-// Which tiles (us, 128 x 128 / 256 x 256 / 256 x 256 by blocks that stay):
+// Which tiles (us, 128 x 128 / 256 x 256 / 256 x 256 by blocks that stay, rows spread
+// unevenly):
 //   that stay  fp32 results from three rounds of tiles on, where the results' way to
-//              memory counts most: 16 groups of 2048 x 7168, 8190 rows 400 / 387 / 350, 64
-//              groups, 16380 rows 1195 / 1069 / 979, 4 groups, 8190 rows 231 / 234 / 219.
-//              A fixed share of the tiles is no good for fewer: 8 groups of 2048 x 2048,
-//              32768 rows (two rounds) 235 / 240 / 288
+//              memory counts most: 16 groups of 2048 x 7168, 8190 rows 385 / 350 / 334, 64
+//              groups, 16380 rows 1220 / 1099 / 1000, 4 groups, 8190 rows 229 / 228 / 212.  A
+//              fixed share of the tiles is no good for fewer: 8 groups of 2048 x 2048, 32768
+//              rows (two rounds) 233 / 232 / 284, spread otherwise 261 / 246 / 232
 //   256 x 256  otherwise from two rounds on, if groups have 192 rows on average: bf16
-//              271 / 242 / 270, 815 / 795 / 937, 131 / 126 / 131, 131 / 121 / 141
-//   128 x 128  for fewer tiles or rows: 16 groups of 1024 x 1024, 2000 rows bf16 15 / 20 /
-//              22; 64 of 512 x 2048, 1000 rows 35 / 49 / 59
+//              266 / 237, 913 / 802, 125 / 127, 124 / 122
+//   128 x 128  for fewer tiles or rows: 16 groups of 1024 x 1024, 2000 rows bf16 15 / 17; 64
+//              of 512 x 2048, 1000 rows 50 / 55
+// Of 30 random sizes what is chosen takes the best time at the median, 11 % over it in one
+// of ten, 35 % at the worst (11 groups of 1383 x 2665, 3084 rows bf16 35 / 47).  The rule does
+// not know whether C is added to: bf16 C in 256 x 256 tiles is read in place then (16 groups
+// 279 / 436; fp32 424 / 425 / 412).
 Fp8Kind fp8_k_group_kind(int groups, int rows, int m, int n, bool fp32) {
   const int64_t big = static_cast<int64_t>(ceil_div(m, Big::TM)) * ceil_div(n, Big::TN) * groups;
   if (fp32 && big >= 3 * kCUs) return kF8Staying;

@@ -101,8 +101,8 @@ typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 // Where C is added to, full tiles have what is there on its way kAhead steps ahead of
 // its use: loads and stores end in order, so a load behind the stores of the rows before
 // would wait for those.  (us, us without: 8-bit products' fp32 G of 16 experts of
-// 2048x7168, 8190 rows, 436 / 730, 8192x8192x2048 278 / 358; 4-bit 3584x7168x8192 126 /
-// 153.)  Not for bf16 in 256 x 256 tiles: there it takes registers that the products need
+// 2048x7168, 8190 rows, 436 / 730, 8192x8192x2048 278 / 358; 4-bit 3584x7168x8192 114 /
+// 140.)  Not for bf16 in 256 x 256 tiles: there it takes registers that the products need
 // (16 experts 319 / 436, but 274 / 241 where C is not added to).
 template <class T, int DC, bool ADD, int XS = T::FN, bool FULL = false>
 __device__ __forceinline__ void store_tile(void* C, const f32x16_t (&acc)[T::FN][T::FM], uint4* stage, int i, int j,
